@@ -20,7 +20,11 @@
  *     q4_1 GEMV) and packed int2 with one scale per row (the colibri summary);
  *   - a host-memory expert tier: the expert set in host RAM, a slot cache of
  *     experts in HBM (the Camelid README's experts-in-RAM lane with a VRAM
- *     expert cache; the TurboFieldfare summary's expert slots).
+ *     expert cache; the TurboFieldfare summary's expert slots);
+ *   - the attention block beside it in 8-bit integers: the linear layers with a
+ *     scale for each token and output channel (int8 rows, any number of
+ *     tokens), a paged cache of keys and values with a scale for each page and
+ *     head, the attention that reads it, and the bookkeeping of its pages.
  *
  * Conventions (every entry point):
  *   - Pointers marked "device" are HIP device pointers, "host" are host
@@ -43,7 +47,7 @@
  * Supported shapes: hidden / input widths (cols) are multiples of 256 and at
  * most 16384; rows 1..65536; E <= 256; 1 <= k <= 8; T <= 128 tokens per
  * layer call (longer prompts are split by the caller into chunks of at most
- * 128 tokens); batch <= 8 for md_qgemv.
+ * 128 tokens); batch <= 8 for md_qgemv; md_i8_* and md_kv_*: see there.
  *
  * Accuracy contract.  Weights are decoded exactly (scale times code) and
  * every contraction y = sum_c w_c x_c is accumulated in fp32 or exactly in
@@ -404,6 +408,185 @@ md_status md_moe_cached_forward(const md_moe_layer *src /*host*/, const md_moe_l
                                 md_expert_cache *c /*host*/, const float *x, int32_t T, float *y, int32_t *idx_out,
                                 float *gates_out, void *workspace, size_t workspace_bytes, hipStream_t stream,
                                 hipStream_t copy_stream, hipEvent_t copy_done);
+
+/* ---- 8-bit products --------------------------------------------------------
+ * The linear layer for any number of tokens on the int8 matrices that md_qgemv
+ * reads (MD_I8_ROW), with the activations rounded to 8-bit integers too:
+ *     s_t  = max_c |x_tc| / 127               (fp32, correctly rounded)
+ *     q_tc = x_tc / s_t to the nearest integer, ties to even (-127..127)
+ *     y_tn = s_t * w_n * sum_c q_tc W_nc (+ bias_n),   w_n = row_scale[n].
+ * The codes are exactly these (not off by one near a tie); the sum is exact in
+ * int32, so the result does not depend on T, on the launch shape or on the
+ * other tokens; the conversion, the two scale products and the bias add round
+ * to fp32 once each, a bf16 y once more.  A row of zeros gives zeros (plus
+ * bias); a row that holds an infinity or a NaN gets the scale NaN, and only its
+ * own outputs are NaN.  md_qgemv keeps the activations in fp32 and reads the
+ * same weights: it is the more exact one for up to 8 tokens.
+ * T: 0..2^20 tokens (0: nothing to do); x, codes, y are dense row-major
+ * T x cols, T x cols and T x rows, none overlapping another.  Errors: an
+ * unknown xtype / ytype or a null pointer -> MD_ERR_INVALID_ARG; T < 0 or
+ * cols <= 0 -> MD_ERR_SHAPE; T > 2^20, a width that is no multiple of 256 or
+ * over 16384, a W of another type -> MD_ERR_UNSUPPORTED. */
+
+/* The codes and scales of T rows of K values (xtype: md_xtype). */
+md_status md_i8_quantize(const void *x, int32_t xtype, int32_t T, int32_t K, int8_t *codes, float *scales,
+                         hipStream_t stream);
+/* y from codes and scales; bias: device, W->rows fp32, or NULL; ytype: md_xtype. */
+md_status md_i8_matmul(const md_qmatrix *W /*host*/, const int8_t *codes, const float *scales, int32_t T,
+                       const float *bias, void *y, int32_t ytype, hipStream_t stream);
+/* Both: y = W Q(x) (+ bias), the codes in the workspace. */
+md_status md_i8_linear_workspace_size(const md_qmatrix *W /*host*/, int32_t T, size_t *bytes /*host*/);
+md_status md_i8_linear(const md_qmatrix *W /*host*/, const void *x, int32_t xtype, int32_t T, const float *bias,
+                       void *y, int32_t ytype, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---- paged 8-bit cache of keys and values -----------------------------------
+ * One layer's cache: n_pages pages of `page` tokens (64, 128 or 256) for
+ * kv_heads heads (1..256) of head_dim channels (64, 128 or 256), as 8-bit codes
+ * with one fp32 scale for each page and head; a value is scale * code.  The
+ * values are held transposed (a channel's tokens together).  All device memory,
+ * the caller's; nothing needs to start cleared. */
+typedef struct md_kv_cache {
+    int32_t n_pages, page, kv_heads, head_dim;
+    int8_t *k;                 /* [n_pages][kv_heads][page][head_dim]         */
+    int8_t *v;                 /* [n_pages][kv_heads][head_dim][page]         */
+    float *k_scale, *v_scale;  /* [n_pages][kv_heads]                         */
+} md_kv_cache;
+
+/* A batch of sequences, each with a run of new tokens (any lengths, none
+ * included).  Rows q_start[s] .. q_start[s+1]-1 of a call's tensors are
+ * sequence s's new tokens; kv_len[s] is its length in the cache, for md_kv_append
+ * and causal attention with those tokens counted in, so that token i of n is
+ * at position kv_len[s] - n + i.  Its position p lies in page
+ * table[s * table_stride + p / page].  Rows behind the last sequence are left
+ * as they are.  The arrays are device memory (4-byte aligned) and are read when
+ * the kernels run, so a captured graph follows their contents; what the host
+ * states bounds them: a sequence with kv_len outside 0..max_kv or past its
+ * table, or with more than max_q rows, is bad: the cache is neither read nor
+ * written for it, and attention gives NaN for its first max_q rows.  One whose
+ * q_start is not ascending within 0..rows is left out altogether.  A page
+ * number outside the cache: nothing is written to it, and attention gives NaN
+ * for the rows that see one of its positions. */
+typedef struct md_kv_batch {
+    int32_t n_seqs;            /* 1..65535                                    */
+    int32_t rows;              /* rows of the call's tensors, 0..2^20         */
+    int32_t max_q, max_kv;     /* bounds of the runs and of kv_len, >= 1      */
+    int32_t table_stride;      /* entries per sequence, * page >= max_kv      */
+    const int32_t *q_start;    /* [n_seqs + 1]                                */
+    const int32_t *kv_len;     /* [n_seqs]                                    */
+    const int32_t *table;      /* [n_seqs][table_stride]                      */
+} md_kv_batch;
+
+/* Writes the new tokens' keys and values (rows x kv_heads x head_dim fp32 or
+ * bf16, row strides in values, a multiple of 16 bytes) into the cache.  Keys
+ * and values alike, for each page and head that new tokens reach:
+ *   - where the page's first token is new, scale = max |new| / 127 over the
+ *     call's tokens of that page;
+ *   - else the scale stays unless max |new| / 127 is above it; then it doubles
+ *     until it is not, and the held codes are halved as often, ties to even
+ *     (by powers of two, so that all raises together cost a held value at most
+ *     one step of the page's scale);
+ *   - code = new / scale to the nearest integer, ties to even (-127..127).
+ * A token's codes thus depend on which tokens of its page came before or with
+ * it, not on the batch around it.  A page and head that an infinity or a NaN
+ * reaches has the scale NaN until its first token is written again: the rows
+ * that see one of its tokens become NaN, the others do not.  Tokens at negative
+ * positions (kv_len below the run's length) are left out.  No page may be
+ * written for two sequences in one call: md_kv_pages_extend gives each writer
+ * its own.  Errors: as md_kv_attention's. */
+md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, const void *k, int64_t k_stride,
+                       const void *v, int64_t v_stride, int32_t xtype, hipStream_t stream);
+
+/* out[row] = softmax(scale * q[row] K^T + mask) V for each of q_heads heads (a
+ * multiple of kv_heads, at most 1024; head h reads key head h / (q_heads /
+ * kv_heads)) over the row's sequence.  causal 1: a row at position p sees
+ * positions 0..p, or with window > 0 the last `window` of them (its own
+ * included); causal 0: every position below kv_len, whatever the run's length
+ * (an encoder's states).  A row that sees nothing gives zeros.  q, out: rows x
+ * q_heads x head_dim, fp32 or bf16 (xtype, ytype), row strides in values, a
+ * multiple of 16 bytes; out must not overlap q.
+ * Accuracy: the cache's codes enter exactly; a query row (one head) is rounded
+ * to integers of its largest magnitude / 8355704 (bf16 out: / 32638), a softmax
+ * weight to integers of 1 / 8355711 (1 / 32639) of the largest weight among its
+ * workgroup's tokens so far; the integer products are exact and everything
+ * else is fp32.  A non-finite q makes its own row and head NaN.
+ * Sequences are split over workgroups and joined by a second kernel where few
+ * rows are to fill the chip; the split follows max_kv, max_q, n_seqs and the
+ * heads, so results are the same for the same descriptor.
+ * Errors: a null pointer, an unknown type, causal not 0 or 1, window < 0 or
+ * without causal, a scale that is not finite, out == q -> MD_ERR_INVALID_ARG;
+ * sizes that are not positive, a stride below its row, q_heads no multiple of
+ * kv_heads, table_stride * page < max_kv -> MD_ERR_SHAPE; sizes outside the
+ * sets above -> MD_ERR_UNSUPPORTED; a pointer or row stride off its alignment
+ * -> MD_ERR_ALIGNMENT; a workspace below md_kv_attention_workspace_size ->
+ * MD_ERR_WORKSPACE. */
+md_status md_kv_attention_workspace_size(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, int32_t q_heads,
+                                         int32_t causal, int32_t window, size_t *bytes /*host*/);
+md_status md_kv_attention(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, const void *q, int32_t xtype,
+                          int32_t q_heads, int64_t q_stride, float scale, int32_t causal, int32_t window, void *out,
+                          int32_t ytype, int64_t out_stride, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* The values that n pages hold (pages: device, n int32): k and v as
+ * [n][kv_heads][page][head_dim] in ytype, both with the token before the
+ * channel.  Slots that no token has reached give what their codes stand for; a
+ * page number outside the cache gives NaN.  n = 0: nothing to do. */
+md_status md_kv_read_pages(const md_kv_cache *c /*host*/, const int32_t *pages, int32_t n, void *k, void *v,
+                           int32_t ytype, hipStream_t stream);
+
+/* Copies pages, codes and scales: page dst[i] becomes page src[i] for every
+ * i < n (src, dst: host arrays, read before the call returns).  The copies run
+ * side by side, so a page that is written may appear only once among all src
+ * and dst -> MD_ERR_INVALID_ARG, as for a number outside the cache.  One launch
+ * for every 448 pairs, the pairs in its arguments: a captured graph keeps
+ * them.  n = 0: nothing to do. */
+md_status md_kv_copy_pages(const md_kv_cache *c /*host*/, const int32_t *src /*host*/, const int32_t *dst /*host*/,
+                           int32_t n, hipStream_t stream);
+
+/* Which pages are in use, and by how many sequences (host state; the layers
+ * of a model that share their tables share one).  The caller owns the arrays
+ * and keeps each sequence's table (page numbers, ceil(length / page) of them)
+ * and length.  Not thread-safe. */
+typedef struct md_kv_pages {
+    int32_t n_pages, page;
+    int32_t *refs;             /* [n_pages]: tables that name the page        */
+    int32_t *free_pages;       /* [n_pages]: the free ones, a heap            */
+    int32_t n_free;
+} md_kv_pages;
+
+/* Every page free. */
+md_status md_kv_pages_reset(md_kv_pages *p /*host*/);
+
+/* Makes positions len .. new_len-1 of a sequence writable: new pages for what
+ * lies past its last one, lowest number first, and where len ends inside a page
+ * that another table names too, a page of its own in that one's place, which
+ * the caller fills with md_kv_copy_pages (in every layer) before it appends:
+ * copy_src[0] -> copy_dst[0] and *n_copy = 1, else *n_copy = 0.
+ * Errors: too few free pages -> MD_ERR_UNSUPPORTED; lengths that shrink or a
+ * table too short -> MD_ERR_SHAPE; an entry that names no page in use ->
+ * MD_ERR_INVALID_ARG; nothing changes on error (all md_kv_pages_* calls). */
+md_status md_kv_pages_extend(md_kv_pages *p /*host*/, int32_t *table /*host*/, int32_t capacity, int32_t len,
+                             int32_t new_len, int32_t *copy_src /*host*/, int32_t *copy_dst /*host*/,
+                             int32_t *n_copy /*host*/);
+
+/* A second sequence with the first `len` positions of this one: its table
+ * names the same pages. */
+md_status md_kv_pages_fork(md_kv_pages *p /*host*/, const int32_t *table /*host*/, int32_t len,
+                           int32_t *new_table /*host*/, int32_t capacity);
+
+/* Gives up the pages of a sequence past new_len (0: all of them; a draft's
+ * rejected tokens: those behind the accepted ones).  A page is free when no
+ * table names it any more. */
+md_status md_kv_pages_truncate(md_kv_pages *p /*host*/, const int32_t *table /*host*/, int32_t len, int32_t new_len);
+
+/* Moves the used pages to the lowest numbers: the tables (n_seqs rows of
+ * table_stride entries, every sequence that holds pages among them) are
+ * rewritten, and the caller copies copy_src[i] -> copy_dst[i], i < *n_copy, with
+ * md_kv_copy_pages (in every layer) before the next use.  The copy arrays hold
+ * n_pages entries.  Errors: a page that the tables do not name as often as it
+ * is held -> MD_ERR_INVALID_ARG. */
+md_status md_kv_pages_compact(md_kv_pages *p /*host*/, int32_t *tables /*host*/, int32_t table_stride,
+                              const int32_t *lens /*host*/, int32_t n_seqs, int32_t *copy_src /*host*/,
+                              int32_t *copy_dst /*host*/, int32_t *n_copy /*host*/);
 
 /* Measurement aid: reads nbytes of device memory at src once, in address
  * order, with every compute unit busy, and writes nothing unless some lane's

@@ -26,7 +26,11 @@ EXPORTS = ("md_abi_version", "md_status_string", "md_last_error_detail", "md_row
            "md_moe_layer_forward_timed", "md_moe_layer_forward_residual", "md_add",
            "md_hbm_read_probe", "md_moe_experts_forward", "md_expert_cache_reset", "md_expert_cache_plan",
            "md_expert_cache_fill", "md_moe_cached_workspace_size", "md_moe_cached_forward",
-           "md_moe_layer_forward_noalloc", "md_moe_layer_stage_relaunch")
+           "md_moe_layer_forward_noalloc", "md_moe_layer_stage_relaunch",
+           "md_i8_quantize", "md_i8_matmul", "md_i8_linear_workspace_size", "md_i8_linear",
+           "md_kv_append", "md_kv_attention_workspace_size", "md_kv_attention", "md_kv_read_pages",
+           "md_kv_copy_pages", "md_kv_pages_reset", "md_kv_pages_extend", "md_kv_pages_fork",
+           "md_kv_pages_truncate", "md_kv_pages_compact")
 STAGES = {"shared": 0, "router": 1, "select": 2, "gateup": 3, "down": 4, "combine": 5}
 
 
@@ -68,7 +72,7 @@ def lib():
         # (two runtimes in one process would each see the device as busy)
         import torch  # noqa: F401
         L = ctypes.CDLL(LIBPATH)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         psz = ctypes.POINTER(ctypes.c_size_t)
         sig = {
             "md_abi_version": (i32, []),
@@ -96,6 +100,20 @@ def lib():
             "md_moe_cached_forward": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp, vp, vp]),
             "md_moe_layer_forward_noalloc": (i32, [vp, vp, i32, vp, vp, vp, vp]),
             "md_moe_layer_stage_relaunch": (i32, [vp, vp, i32, vp, vp, vp, vp, sz, vp, i32]),
+            "md_i8_quantize": (i32, [vp, i32, i32, i32, vp, vp, vp]),
+            "md_i8_matmul": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
+            "md_i8_linear_workspace_size": (i32, [vp, i32, psz]),
+            "md_i8_linear": (i32, [vp, vp, i32, i32, vp, vp, i32, vp, sz, vp]),
+            "md_kv_append": (i32, [vp, vp, vp, i64, vp, i64, i32, vp]),
+            "md_kv_attention_workspace_size": (i32, [vp, vp, i32, i32, i32, psz]),
+            "md_kv_attention": (i32, [vp, vp, vp, i32, i32, i64, ctypes.c_float, i32, i32, vp, i32, i64, vp, sz, vp]),
+            "md_kv_read_pages": (i32, [vp, vp, i32, vp, vp, i32, vp]),
+            "md_kv_copy_pages": (i32, [vp, vp, vp, i32, vp]),
+            "md_kv_pages_reset": (i32, [vp]),
+            "md_kv_pages_extend": (i32, [vp, vp, i32, i32, i32, vp, vp, vp]),
+            "md_kv_pages_fork": (i32, [vp, vp, i32, vp, i32]),
+            "md_kv_pages_truncate": (i32, [vp, vp, i32, i32]),
+            "md_kv_pages_compact": (i32, [vp, vp, i32, vp, i32, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -454,3 +472,327 @@ class ExpertTier:
                                            ctypes.byref(self.cache.state), _ptr(x), T, _ptr(y), _ptr(idx),
                                            _ptr(gates), _ptr(ws), wsb, _stream(stream), cs, ev))
         return y
+
+
+# ---- the attention block in 8-bit integers -----------------------------------
+
+def _xtype(dtype):
+    import torch
+    if dtype == torch.float32:
+        return X_F32
+    if dtype == torch.bfloat16:
+        return X_BF16
+    raise TypeError(f"float32 or bfloat16 wanted, got {dtype}")
+
+
+def _dense(name, t, shape, dtype, device):
+    """Checks what the C call cannot see: a tensor's type, shape, layout, device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} wanted, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t
+
+
+def _rows(name, t, heads, dim, device):
+    """A [rows][heads][dim] tensor whose rows may be strided (a slice of a
+    projection's output): its row stride in values."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != device:
+        raise ValueError(f"{name}: a tensor [rows][{heads}][{dim}] on {device} wanted, got {tuple(t.shape)} on "
+                         f"{t.device}")
+    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: a row's heads and channels must lie together, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+class _on:
+    """The device of a call's tensors made current, and its stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors on a GPU wanted, got {device}")
+        self.back = None
+        now = torch.cuda.current_device()
+        if device.index is not None and device.index != now:
+            self.back = now
+            torch.cuda.set_device(device)
+        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        import torch
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def i8_quantize(x, codes=None, scales=None, stream=None):
+    """The 8-bit codes of x ([T][K] fp32 or bf16) and their scale for each row."""
+    import torch
+    T, K = x.shape
+    dev = x.device
+    _dense("x", x, (T, K), x.dtype, dev)
+    with _on(dev, stream) as st:
+        codes = torch.empty(T, K, dtype=torch.int8, device=dev) if codes is None else \
+            _dense("codes", codes, (T, K), torch.int8, dev)
+        scales = torch.empty(T, dtype=torch.float32, device=dev) if scales is None else \
+            _dense("scales", scales, (T,), torch.float32, dev)
+        _check(lib().md_i8_quantize(_ptr(x), _xtype(x.dtype), T, K, _ptr(codes), _ptr(scales), st))
+    return codes, scales
+
+
+def _i8_args(W, T, bias, y, out_dtype, device):
+    import torch
+    if W.count != 1:
+        raise ValueError(f"one matrix wanted, got a stack of {W.count}")
+    if bias is not None:
+        _dense("bias", bias, (W.rows,), torch.float32, device)
+    if y is None:
+        return torch.empty(T, W.rows, dtype=out_dtype or torch.float32, device=device)
+    if out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+    return _dense("y", y, (T, W.rows), y.dtype, device)
+
+
+def i8_matmul(W, codes, scales, bias=None, y=None, out_dtype=None, stream=None):
+    """y[t][n] = scales[t] * W.row_scale[n] * sum_c codes[t][c] W[n][c] (+ bias[n])
+    for an "i8_row" matrix W; y fp32 or bf16 (out_dtype, fp32 by default)."""
+    import torch
+    T, dev = codes.shape[0], codes.device
+    _dense("codes", codes, (T, W.cols), torch.int8, dev)
+    _dense("scales", scales, (T,), torch.float32, dev)
+    with _on(dev, stream) as st:
+        y = _i8_args(W, T, bias, y, out_dtype, dev)
+        _check(lib().md_i8_matmul(ctypes.byref(W.desc()), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
+                                  _xtype(y.dtype), st))
+    return y
+
+
+def i8_linear_workspace_size(W, T):
+    need = ctypes.c_size_t(0)
+    _check(lib().md_i8_linear_workspace_size(ctypes.byref(W.desc()), T, ctypes.byref(need)))
+    return need.value
+
+
+def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=None):
+    """i8_matmul of i8_quantize(x): x [T][cols] fp32 or bf16, any T."""
+    T, dev = x.shape[0], x.device
+    _dense("x", x, (T, W.cols), x.dtype, dev)
+    with _on(dev, stream) as st:
+        y = _i8_args(W, T, bias, y, out_dtype, dev)
+        d = W.desc()
+        need = ctypes.c_size_t(0)
+        _check(lib().md_i8_linear_workspace_size(ctypes.byref(d), T, ctypes.byref(need)))
+        ws, wsb = _workspace(need.value, dev, workspace)
+        _check(lib().md_i8_linear(ctypes.byref(d), _ptr(x), _xtype(x.dtype), T, _ptr(bias), _ptr(y), _xtype(y.dtype),
+                                  _ptr(ws), wsb, st))
+    return y
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("table_stride", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p)]
+
+
+class KVCache:
+    """One layer's paged cache of keys and values in 8 bits: int8 codes
+    k [n_pages][kv_heads][page][head_dim] and v [n_pages][kv_heads][head_dim][page],
+    fp32 scales [n_pages][kv_heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4:
+            raise ValueError(f"k: [n_pages][kv_heads][page][head_dim] wanted, got {tuple(k.shape)}")
+        self.n_pages, self.kv_heads, self.page, self.head_dim = k.shape
+        dev = self.device = k.device
+        n, h, p, d = k.shape
+        self.k = _dense("k", k, (n, h, p, d), torch.int8, dev)
+        self.v = _dense("v", v, (n, h, d, p), torch.int8, dev)
+        self.k_scale = _dense("k_scale", k_scale, (n, h), torch.float32, dev)
+        self.v_scale = _dense("v_scale", v_scale, (n, h), torch.float32, dev)
+        self.desc = KVCacheDesc(n, p, h, d, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, n_pages, kv_heads, head_dim, page=64, device="cuda"):
+        import torch
+        scale = lambda: torch.empty(n_pages, kv_heads, dtype=torch.float32, device=device)  # noqa: E731
+        return cls(torch.empty(n_pages, kv_heads, page, head_dim, dtype=torch.int8, device=device),
+                   torch.empty(n_pages, kv_heads, head_dim, page, dtype=torch.int8, device=device), scale(), scale())
+
+
+class KVBatch:
+    """Sequences with a run of new tokens each: q_start (int32 [S + 1]), kv_len
+    (int32 [S]) and table (int32 [S][entries]) on the GPU, and the bounds max_q
+    of the runs and max_kv of kv_len.  The arrays are read when the kernels run,
+    so they may be rewritten in place between calls (and graph replays)."""
+
+    def __init__(self, q_start, kv_len, table, max_q, max_kv):
+        import torch
+        S, dev = kv_len.shape[0], kv_len.device
+        if table.dim() != 2:
+            raise ValueError(f"table: [sequences][entries] wanted, got {tuple(table.shape)}")
+        self.q_start = _dense("q_start", q_start, (S + 1,), torch.int32, dev)
+        self.kv_len = _dense("kv_len", kv_len, (S,), torch.int32, dev)
+        self.table = _dense("table", table, (S, table.shape[1]), torch.int32, dev)
+        self.max_q, self.max_kv, self.device = max_q, max_kv, dev
+        self._desc = KVBatchDesc(S, 0, max_q, max_kv, table.shape[1], q_start.data_ptr(), kv_len.data_ptr(),
+                                 table.data_ptr())
+
+    def desc(self, rows):
+        d = KVBatchDesc.from_buffer_copy(self._desc)
+        d.rows = rows
+        return d
+
+
+def kv_append(cache, batch, k, v, stream=None):
+    """Writes the rows of k and v ([rows][kv_heads][head_dim], fp32 or bf16, rows
+    may be strided) into the cache as the batch's new tokens."""
+    ks = _rows("k", k, cache.kv_heads, cache.head_dim, cache.device)
+    vs = _rows("v", v, cache.kv_heads, cache.head_dim, cache.device)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0] or batch.device != cache.device:
+        raise ValueError(f"k and v of one type and length, the batch on {cache.device} wanted")
+    with _on(cache.device, stream) as st:
+        _check(lib().md_kv_append(ctypes.byref(cache.desc), ctypes.byref(batch.desc(k.shape[0])), _ptr(k), ks, _ptr(v),
+                                  vs, _xtype(k.dtype), st))
+
+
+def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0):
+    need = ctypes.c_size_t(0)
+    _check(lib().md_kv_attention_workspace_size(ctypes.byref(cache.desc), ctypes.byref(batch.desc(rows)), q_heads,
+                                                int(causal), window, ctypes.byref(need)))
+    return need.value
+
+
+def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, out_dtype=None, workspace=None,
+                 stream=None):
+    """Attention of the batch's new rows q ([rows][q_heads][head_dim], fp32 or
+    bf16, rows may be strided) over the cache; scale 1 / sqrt(head_dim) by
+    default.  causal: a row sees the positions up to its own (window > 0: the
+    last `window` of them); else every position of its sequence.  out: fp32 or
+    bf16 (out_dtype, fp32 by default); rows behind the last sequence are left as
+    they are."""
+    import torch
+    if q.dim() != 3 or batch.device != cache.device:
+        raise ValueError(f"q [rows][q_heads][head_dim] and the batch on {cache.device} wanted")
+    rows, heads, dim = q.shape
+    qs = _rows("q", q, heads, cache.head_dim, cache.device)
+    with _on(cache.device, stream) as st:
+        if out is None:
+            out = torch.empty(rows, heads, dim, dtype=out_dtype or torch.float32, device=cache.device)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        if out.shape[0] != rows:
+            raise ValueError(f"out has {out.shape[0]} rows, q {rows}")
+        os_ = _rows("out", out, heads, cache.head_dim, cache.device)
+        L, d = lib(), batch.desc(rows)
+        need = ctypes.c_size_t(0)
+        _check(L.md_kv_attention_workspace_size(ctypes.byref(cache.desc), ctypes.byref(d), heads, int(causal), window,
+                                                ctypes.byref(need)))
+        ws, wsb = _workspace(need.value, cache.device, workspace)
+        _check(L.md_kv_attention(ctypes.byref(cache.desc), ctypes.byref(d), _ptr(q), _xtype(q.dtype), heads, qs,
+                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out),
+                                 _xtype(out.dtype), os_, _ptr(ws), wsb, st))
+    return out
+
+
+def kv_read_pages(cache, pages, k=None, v=None, out_dtype=None, stream=None):
+    """The values that pages (int32 on the GPU) hold, keys and values both as
+    [n][kv_heads][page][head_dim]."""
+    import torch
+    n, dev = pages.shape[0], cache.device
+    _dense("pages", pages, (n,), torch.int32, dev)
+    shape = (n, cache.kv_heads, cache.page, cache.head_dim)
+    with _on(dev, stream) as st:
+        dt = out_dtype or (k.dtype if k is not None else torch.float32)
+        k = torch.empty(shape, dtype=dt, device=dev) if k is None else _dense("k", k, shape, dt, dev)
+        v = torch.empty(shape, dtype=dt, device=dev) if v is None else _dense("v", v, shape, dt, dev)
+        _check(lib().md_kv_read_pages(ctypes.byref(cache.desc), _ptr(pages), n, _ptr(k), _ptr(v), _xtype(dt), st))
+    return k, v
+
+
+def kv_copy_pages(cache, src, dst, stream=None):
+    """Page dst[i] of the cache becomes page src[i] (host sequences of page
+    numbers); a page that is written appears once among all of them."""
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError(f"{n} source pages and {len(dst)} destinations")
+    array = ctypes.c_int32 * max(n, 1)
+    with _on(cache.device, stream) as st:
+        _check(lib().md_kv_copy_pages(ctypes.byref(cache.desc), array(*src), array(*dst), n, st))
+
+
+class KVPagesState(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page", ctypes.c_int32), ("refs", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_int32)]
+
+
+class KVPages:
+    """Which pages of a cache are in use (host state).  Sequences are kept here
+    by a number each: their length and their row of `tables` (int32
+    [max_seqs][entries], ready to be copied to the GPU)."""
+
+    def __init__(self, n_pages, page, max_seqs, entries):
+        import numpy as np
+        self.refs, self.free = np.empty(n_pages, dtype=np.int32), np.empty(n_pages, dtype=np.int32)
+        self._src, self._dst = np.empty(n_pages, dtype=np.int32), np.empty(n_pages, dtype=np.int32)
+        self.tables = np.zeros((max_seqs, entries), dtype=np.int32)
+        self.lens = np.zeros(max_seqs, dtype=np.int32)
+        self.state = KVPagesState(n_pages, page, self.refs.ctypes.data, self.free.ctypes.data, 0)
+        self.reset()
+
+    def _row(self, s):
+        if not 0 <= s < len(self.lens):
+            raise IndexError(f"sequence {s} of {len(self.lens)}")
+        return self.tables.ctypes.data + 4 * s * self.tables.shape[1]
+
+    def reset(self):
+        _check(lib().md_kv_pages_reset(ctypes.byref(self.state)))
+        self.lens[:] = 0
+
+    @property
+    def n_free(self):
+        return self.state.n_free
+
+    def _pairs(self, n):
+        return list(zip(self._src[:n].tolist(), self._dst[:n].tolist()))
+
+    def extend(self, s, n_tokens):
+        """Room for n_tokens more of sequence s: returns the (src, dst) page
+        copies to make before they are appended (none, or one)."""
+        n = ctypes.c_int32(0)
+        new = int(self.lens[s]) + n_tokens
+        _check(lib().md_kv_pages_extend(ctypes.byref(self.state), self._row(s), self.tables.shape[1],
+                                        int(self.lens[s]), new, self._src.ctypes.data, self._dst.ctypes.data,
+                                        ctypes.byref(n)))
+        self.lens[s] = new
+        return self._pairs(n.value)
+
+    def fork(self, s, to, n_tokens=None):
+        """Sequence `to` (an empty one) starts with s's first n_tokens (all)."""
+        n = int(self.lens[s]) if n_tokens is None else n_tokens
+        if s == to or not 0 <= n <= self.lens[s] or self.lens[to]:
+            raise ValueError(f"fork {n} tokens of sequence {s} ({self.lens[s]}) into {to} ({self.lens[to]})")
+        _check(lib().md_kv_pages_fork(ctypes.byref(self.state), self._row(s), n, self._row(to), self.tables.shape[1]))
+        self.lens[to] = n
+
+    def truncate(self, s, n_tokens=0):
+        """Sequence s back to its first n_tokens."""
+        _check(lib().md_kv_pages_truncate(ctypes.byref(self.state), self._row(s), int(self.lens[s]), n_tokens))
+        self.lens[s] = n_tokens
+
+    def compact(self):
+        """Moves the used pages to the lowest numbers: the (src, dst) copies to
+        make before the next use."""
+        n = ctypes.c_int32(0)
+        _check(lib().md_kv_pages_compact(ctypes.byref(self.state), self.tables.ctypes.data, self.tables.shape[1],
+                                         self.lens.ctypes.data, len(self.lens), self._src.ctypes.data,
+                                         self._dst.ctypes.data, ctypes.byref(n)))
+        return self._pairs(n.value)

@@ -12,13 +12,14 @@
 #include "moe_decode.h"
 #include "common.hpp"
 #include "digits.hpp"
+#include "host.hpp"
 #include "kernels.hpp"
 
 namespace {
-
 thread_local char g_detail[512] = "";
+}
 
-md_status fail(md_status s, const char* fmt, ...) {
+md_status md::fail(md_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_detail, sizeof g_detail, fmt, ap);
@@ -26,16 +27,23 @@ md_status fail(md_status s, const char* fmt, ...) {
   return s;
 }
 
-md_status ok() {
+md_status md::ok() {
   g_detail[0] = 0;
   return MD_OK;
 }
 
-md_status hip_fail(hipError_t e, const char* what) {
+md_status md::hip_fail(hipError_t e, const char* what) {
   return fail(MD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
+
+using md::align256;
+using md::aligned16;
+using md::check_qmatrix;
+using md::fail;
+using md::hip_fail;
+using md::ok;
 
 bool valid_type(int32_t t) { return t >= MD_Q8_0 && t <= MD_I2_ROW; }
 bool row_type(int32_t t) { return t == MD_I8_ROW || t == MD_I4_ROW || t == MD_I2_ROW; }
@@ -50,8 +58,6 @@ constexpr int kMaxBatch = 8;
 // problem in one launch; above it the pairs are grouped by expert.
 using md::kMaxPairT;
 
-size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
-
 md_status check_width(const char* what, int32_t n) {
   if (n <= 0) return fail(MD_ERR_SHAPE, "%s = %d must be positive", what, n);
   if (n % 256 || n > kMaxCols)
@@ -59,7 +65,9 @@ md_status check_width(const char* what, int32_t n) {
   return MD_OK;
 }
 
-md_status check_qmatrix(const char* what, const md_qmatrix* W) {
+}  // namespace
+
+md_status md::check_qmatrix(const char* what, const md_qmatrix* W) {
   if (!W) return fail(MD_ERR_INVALID_ARG, "%s: null matrix descriptor", what);
   if (!valid_type(W->type)) return fail(MD_ERR_INVALID_ARG, "%s: unknown type %d", what, W->type);
   if (W->rows <= 0 || W->cols <= 0) return fail(MD_ERR_SHAPE, "%s: rows %d cols %d", what, W->rows, W->cols);
@@ -74,6 +82,8 @@ md_status check_qmatrix(const char* what, const md_qmatrix* W) {
   }
   return MD_OK;
 }
+
+namespace {
 
 md_status check_ffn(const md_ffn* f, int32_t H) {
   if (!f) return fail(MD_ERR_INVALID_ARG, "null FFN descriptor");

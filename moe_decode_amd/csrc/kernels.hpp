@@ -192,4 +192,46 @@ hipError_t launch_clamp_idx(const int* in, int n, int E, int* out, hipStream_t s
 hipError_t launch_combine(const float* o, const int* pos_of_pair, const float* gates, int T, int k, int H,
                           const float* y_shared, const float* y_residual, float* y, hipStream_t st);
 
+// ---- 8-bit products (i8gemm.hip) -------------------------------------------
+hipError_t launch_i8_quantize(const void* x, int xt, int T, int K, int8_t* codes, float* scales, hipStream_t st);
+hipError_t launch_i8_matmul(const int8_t* W, const float* ws, int N, int K, const int8_t* xq, const float* xs, int T,
+                            const float* bias, void* y, int yt, hipStream_t st);
+
+// ---- paged 8-bit cache (kv.hip, kvattn.hip) --------------------------------
+struct KvCache {
+  int n_pages, page, Hkv, D;
+  int8_t *k, *v;              // [n_pages][Hkv][page][D], [n_pages][Hkv][D][page]
+  float *k_scale, *v_scale;   // [n_pages][Hkv]
+};
+// S sequences: rows q_start[s] .. q_start[s + 1] - 1 of the call's tensors are
+// sequence s's new tokens (host: rows tensors' rows, max_q, max_kv bounds).
+struct KvBatch {
+  int S, rows, max_q, max_kv, table_stride;
+  const int *q_start, *kv_len, *table;
+};
+struct KvAttn {
+  KvCache c;
+  KvBatch b;
+  const void* q;
+  void* out;
+  int64_t q_stride, out_stride;
+  int xt, yt, G, causal, window, pshift;
+  float scale;
+  int splits, chunk;          // a split covers chunk tiles of 64 positions
+  float *part, *part_m;       // [rows][Hq][splits][D], [rows][Hq][splits][2]
+};
+struct KvPlan {
+  int splits, chunk;
+};
+constexpr int kPairsPerLaunch = 448;  // page pairs that fit a launch's 4 KB of arguments
+struct PagePairs {
+  int src[kPairsPerLaunch], dst[kPairsPerLaunch];
+};
+hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int xt, hipStream_t st);
+hipError_t launch_kv_read(const KvCache& c, const int* pages, int n, void* k, void* v, int yt, hipStream_t st);
+hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int n, hipStream_t st);
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal);
+hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st);
+
 }  // namespace md
