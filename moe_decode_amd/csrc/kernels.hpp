@@ -217,11 +217,13 @@ struct KvAttn {
   int64_t q_stride, out_stride;
   int xt, yt, G, causal, window, pshift;
   float scale;
+  int tile;                   // columns (query, head) of a workgroup
+  int snake;                  // all workgroups run at once, two on a compute unit
   int splits, chunk;          // a split covers chunk tiles of 64 positions
   float *part, *part_m;       // [rows][Hq][splits][D], [rows][Hq][splits][2]
 };
 struct KvPlan {
-  int splits, chunk;
+  int tile, splits, chunk;
 };
 constexpr int kPairsPerLaunch = 448;  // page pairs that fit a launch's 4 KB of arguments
 struct PagePairs {

@@ -59,6 +59,16 @@ MD_DEV Span span_of(const KvAttn& a, const Seq& q, int c0, int c1) {
   return s;
 }
 
+// The column tile of a workgroup, the b-th of n: where the mask is causal the
+// last columns see the most, so the heaviest tiles start first; when all run
+// at once, two on a compute unit, the second half goes the other way round and
+// each unit gets a heavy and a light one.
+MD_DEV int column_tile(const KvAttn& a, int b, int n) {
+  if (!a.causal) return b;
+  const int half = (n + 1) / 2;
+  return a.snake && b >= half ? b - half : n - 1 - b;
+}
+
 // Four neighbouring outputs of a row's head.
 MD_DEV void store_out4(const KvAttn& a, int64_t row, int head, int D, int d, float x, float y, float z, float w) {
   const int64_t at = row * a.out_stride + (int64_t)head * D + d;

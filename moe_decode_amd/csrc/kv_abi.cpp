@@ -124,7 +124,7 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
     return fail(MD_ERR_INVALID_ARG, "attention: window %d%s", window, causal ? "" : " without causal");
   const int G = q_heads / c->kv_heads;
   *plan = md::kv_attn_plan(dev(c), dev(b), G, window, causal);
-  const int64_t groups = ((int64_t)b->max_q * G + 15) / 16 * c->kv_heads * plan->splits;
+  const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
   if (groups > INT32_MAX) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
   const size_t slots = plan->splits > 1 ? (size_t)b->rows * q_heads * plan->splits : 0;
   *bytes = slots ? align256(slots * 2 * sizeof(float)) + align256(slots * c->head_dim * sizeof(float)) : 0;
@@ -334,6 +334,7 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
   a.window = window;
   a.pshift = c->page == 64 ? 6 : c->page == 128 ? 7 : 8;
   a.scale = scale;
+  a.tile = plan.tile;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
   if (need) {

@@ -53,11 +53,16 @@ struct Digits<2> {
   static constexpr int bias = 0x8080, pbias = 0x80;
 };
 
-// Four integers' bytes k: dword of byte k of a, b, c, d.
-MD_DEV uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int k) {
-  const uint32_t sel = 0x0C0C0400u + 0x0101u * k;  // [a.k, b.k, 0, 0]
-  const uint32_t lo = __builtin_amdgcn_perm(b, a, sel), hi = __builtin_amdgcn_perm(d, c, sel);
-  return lo | hi << 16;
+// Byte k of four integers, as one dword, for every digit k < ND.
+template <int ND>
+MD_DEV void bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&out)[ND]) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u), cd = __builtin_amdgcn_perm(d, c, 0x05010400u);
+  out[0] = __builtin_amdgcn_perm(cd, ab, 0x05040100u);  // a.0 b.0 c.0 d.0
+  out[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
+  if constexpr (ND == 3) {
+    const uint32_t ab2 = __builtin_amdgcn_perm(b, a, 0x0C0C0602u), cd2 = __builtin_amdgcn_perm(d, c, 0x06020C0Cu);
+    out[2] = ab2 | cd2;
+  }
 }
 
 template <int ND>
@@ -67,6 +72,138 @@ MD_DEV float join(const i32x4 (&a)[ND], int r) {
   else return fmaf((float)a[2][r], 65536.0f, (float)low);
 }
 
+MD_DEV i32x4 load16(rsrc_t r, int off, int soff) {
+  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
+  return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+}
+
+MD_DEV float nan_f() { return __uint_as_float(0x7FC00000u); }
+
+// A column's query digits (the lane's 16 channels of each 64) and its state.
+// The sign of the score scale goes into the digits, so that a tile's factor is
+// never negative and the raw integer scores can be compared before they are
+// scaled.
+template <int D, int ND>
+struct Column {
+  i32x4 qd[ND][D / 64];
+  float qscale, m, l;
+  int hi, lo;  // the positions it sees
+};
+template <int D, int ND>
+MD_DEV void column_init(Column<D, ND>& o, const KvAttn& a, const Seq& q, int h, int c, int cols, int g) {
+  const int cc = min(c, cols - 1), qt = cc / a.G, hq = h * a.G + (cc - qt * a.G);  // past the last one: that one again
+  const int pos = q.len - q.nq + qt;
+  o.hi = a.causal ? pos : q.len - 1;
+  o.lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  float v[D / 64][16], poison = q.bad ? nan_f() : 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float w[8];
+      const int64_t at = ((int64_t)q.row0 + qt) * a.q_stride + (int64_t)hq * D + 64 * k + 16 * g + 8 * e;
+      if (a.xt == XF32) load8<XF32>(a.q, at, w);
+      else load8<XBF16>(a.q, at, w);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        v[k][8 * e + m] = w[m];
+        top = max(top, __float_as_uint(w[m]) & 0x7FFFFFFFu);
+      }
+    }
+  float t = __uint_as_float(top);
+  if (top >= 0x7F800000u) poison = nan_f(), t = 0.0f;
+  t = fmaxf(t, xor_lanes<16>(t));
+  t = fmaxf(t, xor_lanes<32>(t));
+  poison += xor_lanes<16>(poison);
+  poison += xor_lanes<32>(poison);
+  const float up = t >= 0x1p-100f ? copysignf(Digits<ND>::qtop / t, a.scale) : 0.0f;
+  o.qscale = t * (1.0f / Digits<ND>::qtop) * fabsf(a.scale) * kLog2e;
+  o.m = -INFINITY;
+  o.l = poison;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t n[4], d[ND];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float f = poison == poison ? v[k][4 * w + m] * up : 0.0f;
+        n[m] = (uint32_t)(__float2int_rn(f) + Digits<ND>::bias);
+      }
+      bytes4<ND>(n[0], n[1], n[2], n[3], d);
+#pragma unroll
+      for (int e = 0; e < ND; ++e) o.qd[e][k][w] = (int)(d[e] ^ 0x80808080u);
+    }
+}
+
+// A page's scales for a head.  One that the append did not write (negative or
+// not finite) makes the rows that see the page NaN: off is added to their sums.
+struct Scales {
+  float ks, vs, off;
+};
+MD_DEV Scales scales_of(float ks, float vs) {
+  const bool good = ks >= 0.0f && ks < INFINITY && vs >= 0.0f && vs < INFINITY;
+  return Scales{good ? ks : 0.0f, good ? vs : 0.0f, good ? 0.0f : nan_f()};
+}
+
+// One tile's raw scores masked (where it is cut), the running maximum moved:
+// returns the factor of a raw score and the reference, and alpha for what has
+// been summed so far.
+template <int D, int ND, int N>
+MD_DEV float advance(Column<D, ND>& o, float (&x)[N], const float (&f)[N / 16], const float (&off)[N / 16], bool cut,
+                     int first, float& ref) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) {
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (first + 64 * t + i > o.hi || first + 64 * t + i < o.lo) x[16 * t + i] = -INFINITY;
+    }
+    float raw = x[16 * t];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) raw = fmaxf(raw, x[16 * t + i]);
+    if (raw > -INFINITY) o.l += off[t];
+    top = fmaxf(top, raw * f[t]);
+  }
+  top = fmaxf(top, xor_lanes<16>(top));
+  top = fmaxf(top, xor_lanes<32>(top));
+  if (top == INFINITY) o.l = nan_f();
+  const float m1 = fmaxf(o.m, top);
+  ref = m1 > -INFINITY ? m1 : 0.0f;
+  const float alpha = __builtin_amdgcn_exp2f(o.m - ref);
+  o.m = m1;
+  return alpha;
+}
+
+// Sixteen raw scores to softmax weights and their digits.  The fused product
+// and subtraction may leave the largest one just above 0, so the weight is
+// clamped to 1 (a digit past the top would wrap).
+template <int ND>
+MD_DEV float weights(const float* x, float f, float ref, float scale, i32x4 (&pd)[ND]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t n[4], d[ND];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float p = __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(fmaf(x[4 * j + r], f, -ref)), 0.0f, 1.0f);
+      sum += p;
+      n[r] = __float_as_uint(fmaf(p, scale, 8388608.0f + (float)Digits<ND>::pbias));
+    }
+    bytes4<ND>(n[0], n[1], n[2], n[3], d);
+#pragma unroll
+    for (int e = 0; e < ND; ++e) pd[e][j] = (int)(e < ND - 1 ? d[e] ^ 0x80808080u : d[e]);
+  }
+  return sum;
+}
+
+// Few columns (decode): a workgroup's four waves take turns at the tiles of one
+// column tile of 16 and meet in LDS.  Bound by the read of the cache: keys and
+// values go from HBM straight into the matrix cores' operand registers, the
+// next tile's keys while this one's weights are formed and summed, its values
+// while the next one's scores are.
 template <int D, int ND>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAttn a) {
   constexpr int KS = D / 64, DT = D / 16;
@@ -85,58 +222,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
   if (split >= active) return;
   const int t_begin = sp.t0 + split * per, t_end = min(t_begin + per, sp.t1);
 
-  // this lane's column: query t, head hq; past the last one the last one again
-  const int cc = min(ct * 16 + col, cols - 1), qt = cc / a.G, hq = h * a.G + (cc - qt * a.G);
-  const int64_t row = (int64_t)q.row0 + qt;
-  const int pos = q.len - q.nq + qt;
-  const int hi = a.causal ? pos : q.len - 1;                     // last position it sees
-  const int lo = a.window ? max(pos - a.window + 1, 0) : 0;      // first
-
-  // its digits
-  i32x4 qd[ND][KS];
-  float qs, poison = q.bad ? __uint_as_float(0x7FC00000u) : 0.0f;
-  {
-    float v[KS][16];
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float w[8];
-        const int64_t at = row * a.q_stride + (int64_t)hq * D + 64 * k + 16 * g + 8 * e;
-        if (a.xt == XF32) load8<XF32>(a.q, at, w);
-        else load8<XBF16>(a.q, at, w);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          v[k][8 * e + m] = w[m];
-          top = max(top, __float_as_uint(w[m]) & 0x7FFFFFFFu);
-        }
-      }
-    float t = __uint_as_float(top);
-    if (top >= 0x7F800000u) poison = __uint_as_float(0x7FC00000u), t = 0.0f;
-    t = fmaxf(t, xor_lanes<16>(t));
-    t = fmaxf(t, xor_lanes<32>(t));
-    poison += xor_lanes<16>(poison);
-    poison += xor_lanes<32>(poison);
-    const float up = t >= 0x1p-100f ? Digits<ND>::qtop / t : 0.0f;
-    qs = t * (1.0f / Digits<ND>::qtop);
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t n[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float f = poison == poison ? v[k][4 * w + m] * up : 0.0f;
-          n[m] = (uint32_t)(__float2int_rn(f) + Digits<ND>::bias);
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) qd[d][k][w] = (int)(bytes4(n[0], n[1], n[2], n[3], d) ^ 0x80808080u);
-      }
-  }
-  const float qscale = qs * a.scale * kLog2e;
-
-  float m = -INFINITY, l = poison;
+  Column<D, ND> o;
+  column_init<D, ND>(o, a, q, h, ct * 16 + col, cols, g);
   float acc[DT][4];
 #pragma unroll
   for (int i = 0; i < DT; ++i)
@@ -144,101 +231,90 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     for (int r = 0; r < 4; ++r) acc[i][r] = 0.0f;
 
   const int pshift = a.pshift;
-  const int ktok = 16 * (col >> 2) + (col & 3);  // token of this lane's A row in key tile 0
-  int id = t_begin + wave < t_end ? q.table[(t_begin + wave) * kTile >> pshift] : 0;
-  for (int t = t_begin + wave; t < t_end; t += kWaves) {
-    const int base = t * kTile, sub = base & ((1 << pshift) - 1);
-    const int page = __builtin_amdgcn_readfirstlane(id);
-    if (t + kWaves < t_end) id = q.table[(t + kWaves) * kTile >> pshift];
-    if ((unsigned)page >= (unsigned)c.n_pages) {  // a page that is none: the rows that see it are NaN
-      if (lo <= base + kTile - 1 && hi >= base) l = __uint_as_float(0x7FC00000u);
-      continue;
-    }
-    const int64_t ph = (int64_t)page * c.Hkv + h;
-    const int8_t* kp = c.k + (ph << pshift) * D + (int64_t)sub * D;
-    const int8_t* vp = c.v + (ph << pshift) * D + sub;
-    float ks = c.k_scale[ph], vs = c.v_scale[ph];
-    i32x4 kf[4][KS], vf[DT];
+  const int koff = (16 * (col >> 2) + (col & 3)) * D + 16 * g;  // this lane's A row of key tile 0
+  const int voff = (col << pshift) + 16 * g;
+  i32x4 kf[4][KS], vf[DT];
+  // a page that is none reads page 0 and counts as one with scale NaN
+  auto page_at = [&](int t) { return t < t_end ? q.table[t * kTile >> pshift] : 0; };
+  // buffer loads: past the last tile the resources are empty, and the same
+  // loads read zeros without memory traffic
+  auto load_k = [&](int t, int page) {
+    const int sub = (t * kTile) & ((1 << pshift) - 1);
+    const rsrc_t r = make_res(c.k + ((((int64_t)page * c.Hkv + h) << pshift) + sub) * D, t < t_end ? kTile * D : 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-        kf[j][k] = *reinterpret_cast<const i32x4*>(kp + (ktok + 4 * j) * D + 64 * k + 16 * g);
+      for (int k = 0; k < KS; ++k) kf[j][k] = load16(r, koff + 4 * j * D + 64 * k, 0);
+  };
+  auto load_v = [&](int t, int page) {
+    const int sub = (t * kTile) & ((1 << pshift) - 1);
+    const rsrc_t r = make_res(c.v + (((int64_t)page * c.Hkv + h) << pshift) * D + sub, t < t_end ? (D << pshift) - sub : 0);
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
-      vf[i] = *reinterpret_cast<const i32x4*>(vp + ((int64_t)(16 * i + col) << pshift) + 16 * g);
-    float off = 0.0f;  // NaN where a scale is not finite
-    if (!(ks < INFINITY) || !(vs < INFINITY)) {
-      off = __uint_as_float(0x7FC00000u);
-      ks = vs = 0.0f;
-    }
-    float x[16];
-    const float f = qscale * ks;
+    for (int i = 0; i < DT; ++i) vf[i] = load16(r, voff, (16 * i) << pshift);
+  };
+  int t = t_begin + wave;
+  if (t < t_end) {
+    int id = __builtin_amdgcn_readfirstlane(page_at(t)), next = page_at(t + kWaves);
+    bool good = (unsigned)id < (unsigned)c.n_pages;
+    int page = good ? id : 0;
+    load_k(t, page);
+    load_v(t, page);
+    float ks = c.k_scale[(int64_t)page * c.Hkv + h], vs = c.v_scale[(int64_t)page * c.Hkv + h];
+    for (; t < t_end; t += kWaves) {
+      const Scales sc = scales_of(good ? ks : -1.0f, vs);
+      id = __builtin_amdgcn_readfirstlane(next);
+      good = (unsigned)id < (unsigned)c.n_pages;
+      page = good ? id : 0;
+      next = page_at(t + 2 * kWaves);
+      float x[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      i32x4 d[ND];
+      for (int j = 0; j < 4; ++j) {
+        i32x4 d[ND];
 #pragma unroll
-      for (int e = 0; e < ND; ++e) {
-        d[e] = i32x4{0, 0, 0, 0};
+        for (int e = 0; e < ND; ++e) {
+          d[e] = i32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][k], qd[e][k], d[e], 0, 0, 0);
+          for (int k = 0; k < KS; ++k)
+            d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][k], o.qd[e][k], d[e], 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * j + r] = join<ND>(d, r);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      load_k(t + kWaves, page);
+      ks = c.k_scale[(int64_t)page * c.Hkv + h];
+      vs = c.v_scale[(int64_t)page * c.Hkv + h];
+      const float f[1] = {fmaxf(o.qscale * sc.ks, 1e-37f)}, off[1] = {sc.off};
+      float ref;
+      const int base = t * kTile;
+      const float alpha = advance<D, ND, 16>(o, x, f, off, base + kTile - 1 > sp.full_hi || base < sp.full_lo,
+                                             base + 16 * g, ref);
+      i32x4 pd[ND];
+      o.l = fmaf(o.l, alpha, weights<ND>(x, f[0], ref, Digits<ND>::top, pd));
+      const float fv = sc.vs * (1.0f / Digits<ND>::top);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[4 * j + r] = join(d, r) * f;
-    }
-    const int first = base + 16 * g;
-    if (base + kTile - 1 > sp.full_hi || base < sp.full_lo) {
+      for (int i = 0; i < DT; ++i) {
+        i32x4 d[ND];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (first + i > hi || first + i < lo) x[i] = -INFINITY;
-    }
-    float top = x[0];
+        for (int e = 0; e < ND; ++e)
+          d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf[i], pd[e], i32x4{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-    if (top > -INFINITY) l += off;
-    top = fmaxf(top, xor_lanes<16>(top));
-    top = fmaxf(top, xor_lanes<32>(top));
-    const float m1 = fmaxf(m, top), ref = m1 > -INFINITY ? m1 : 0.0f;
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    m = m1;
-    uint32_t n[16];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = __builtin_amdgcn_exp2f(x[i] - ref);
-      sum += p;
-      n[i] = __float_as_uint(fmaf(p, Digits<ND>::top, 8388608.0f + (float)Digits<ND>::pbias));
-    }
-    l = fmaf(l, alpha, sum);
-    i32x4 pd[ND];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < ND; ++e)
-        pd[e][j] = (int)(bytes4(n[4 * j], n[4 * j + 1], n[4 * j + 2], n[4 * j + 3], e) ^
-                         (e < ND - 1 ? 0x80808080u : 0u));
-    const float vf32 = vs * (1.0f / Digits<ND>::top);
-#pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      i32x4 d[ND];
-#pragma unroll
-      for (int e = 0; e < ND; ++e)
-        d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf[i], pd[e], i32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(join(d, r), vf32, acc[i][r] * alpha);
+        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(join<ND>(d, r), fv, acc[i][r] * alpha);
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      load_v(t + kWaves, page);
     }
   }
-  l += xor_lanes<16>(l);
-  l += xor_lanes<32>(l);
+  o.l += xor_lanes<16>(o.l);
+  o.l += xor_lanes<32>(o.l);
 
   // the waves' shares meet in LDS
 #pragma unroll
   for (int i = 0; i < DT; ++i)
     *reinterpret_cast<float4*>(&s_acc[wave][col][16 * i + 4 * g]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   if (g == 0) {
-    s_m[wave][col] = m;
-    s_l[wave][col] = l;
+    s_m[wave][col] = o.m;
+    s_l[wave][col] = o.l;
   }
   __syncthreads();
   const int oc = threadIdx.x >> 4, part = threadIdx.x & 15;
@@ -251,7 +327,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     w[i] = __builtin_amdgcn_exp2f(s_m[i][oc] - ref);
-    ll += w[i] > 0.0f || !(s_l[i][oc] == s_l[i][oc]) ? s_l[i][oc] * (w[i] > 0.0f ? w[i] : 1.0f) : 0.0f;
+    ll = fmaf(w[i], s_l[i][oc], ll);  // 0 * NaN stays NaN
   }
   const int64_t orow = (int64_t)q.row0 + ot;
   const bool direct = active == 1;
@@ -260,13 +336,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 #pragma unroll
   for (int i = 0; i < DT / 4; ++i) {
     const int d = 4 * part + 64 * i;
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = fmaf(w[k], s_acc[k][oc][d + r], o[r]);
-    if (direct) store_out4(a, orow, oh, D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    else *reinterpret_cast<float4*>(a.part + slot * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+      for (int r = 0; r < 4; ++r) y[r] = fmaf(w[k], s_acc[k][oc][d + r], y[r]);
+    if (direct) store_out4(a, orow, oh, D, d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    else *reinterpret_cast<float4*>(a.part + slot * D + d) = make_float4(y[0], y[1], y[2], y[3]);
   }
   if (!direct && part == 0) {
     a.part_m[2 * slot] = mm;
@@ -274,28 +350,297 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
   }
 }
 
-// The splits of a row: D / 4 lanes per (row, head), 1024 / D heads a workgroup.
-__global__ __launch_bounds__(256) void k_kv_join(KvAttn a, int D) {
-  const int s = blockIdx.z, head = blockIdx.y * (1024 / D) + (int)threadIdx.x / (D / 4), d = 4 * ((int)threadIdx.x % (D / 4));
+// Many columns (prompts): a workgroup's four waves own 32 columns each and walk
+// the same tiles of 64 tokens, staged in LDS; a byte of the cache is read from
+// L2 once for 128 columns.  Here the arithmetic around the products counts, so
+// they run on the f16 matrix cores, which accumulate in fp32 and need no joins:
+// the codes are exact in f16 (converted once per workgroup on their way to
+// LDS), a query row is scaled by a power of two to below 2^14 and rounded to
+// f16, and so is a weight p times 2^14 vs / R, R the largest value scale met so
+// far.  NS = 2 (fp32 outputs) takes a second f16 for what the first one leaves,
+// 22 bits together.  Per score that leaves half a maximum, one fma, one exp2
+// (a quarter of the rate), the sum and half a conversion on the vector ALU.
+//
+// 32 x 32 tiles: score row 8 a + 4 hh + b of a 32-token block is its token
+// 16 hh + 4 a + b, so lane half hh holds tokens 16 hh .. 16 hh + 15 and feeds
+// them, eight consecutive ones a step, as the second product's B operand.
+// LDS chunks of 16 bytes are permuted by their row so that the rows a fragment
+// read touches fall into different banks.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Four codes as f16: 1024 + 128 + code has the bit pattern 0x6400 | (code ^ 0x80).
+MD_DEV uint2 codes_f16(uint32_t w) {
+  const uint32_t u = w ^ 0x80808080u;
+  const f16x2 bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  const uint32_t lo = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), hi = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, lo) + bias),
+                    __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, hi) + bias));
+}
+
+constexpr int kRowCols = 128;  // columns of a workgroup
+
+template <int D, int NS>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a) {
+  constexpr int KS = D / 16, DT = D / 32;
+  constexpr int L = kTile * D / 16 / 256;  // 16-byte chunks of codes per thread, keys or values
+  __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kTile * D], s_v[2][kTile * D];
+  const KvCache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
+  const int h = rest % c.Hkv, s = blockIdx.y;
+  const Seq q = seq_of(a.b, s, c.page);
+  const int cols = q.nq * a.G;
+  const int ct = column_tile(a, rest / c.Hkv, (int)(gridDim.x / (a.splits * c.Hkv)));
+  if (ct * kRowCols >= cols) return;
+  const Span sp = span_of(a, q, ct * kRowCols, min(ct * kRowCols + kRowCols, cols));
+  const int per = a.chunk, active = max(1, (sp.t1 - sp.t0 + per - 1) / per);
+  if (split >= active) return;
+  const int t_begin = sp.t0 + split * per, t_end = min(t_begin + per, sp.t1);
+  const int c0 = ct * kRowCols + wave * 32;
+  const bool any = c0 < cols;  // a wave past the last column only helps with the loads
+  const Span mine = span_of(a, q, any ? c0 : 0, any ? min(c0 + 32, cols) : 1);
+
+  const int pshift = a.pshift;
+  u32x4 kr[L], vr[L];
+  float ks_n, vs_n;
+  auto load = [&](int t) {  // tile t's codes and scales; a page that is none is page 0 with a scale that is none
+    const int id = __builtin_amdgcn_readfirstlane(t < t_end ? q.table[t * kTile >> pshift] : 0);
+    const bool good = (unsigned)id < (unsigned)c.n_pages;
+    const int page = good ? id : 0, sub = (t * kTile) & ((1 << pshift) - 1);
+    const int64_t ph = (int64_t)page * c.Hkv + h;
+    ks_n = good ? c.k_scale[ph] : -1.0f;
+    vs_n = c.v_scale[ph];
+    const int8_t *kp = c.k + ((ph << pshift) + sub) * D, *vp = c.v + (ph << pshift) * D + sub;
+#pragma unroll
+    for (int n = 0; n < L; ++n) {
+      const int ch = n * 256 + tid;
+      kr[n] = *reinterpret_cast<const u32x4*>(kp + 16 * ch);
+      vr[n] = *reinterpret_cast<const u32x4*>(vp + ((ch >> 2) << pshift) + 16 * (ch & 3));
+    }
+  };
+  auto kkey = [](int tok) { return (tok & 3) | ((tok >> 4) & 1) << 2; };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int n = 0; n < L; ++n) {
+      const int ch = n * 256 + tid;
+      const int tok = ch / (D / 16), kc = 2 * (ch % (D / 16)), d = ch >> 2, vc = 2 * (ch & 3);
+      u32x4 w[2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint2 f = codes_f16(kr[n][m]);
+        w[m >> 1][2 * (m & 1)] = f.x;
+        w[m >> 1][2 * (m & 1) + 1] = f.y;
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_k[buf][tok * D + 8 * ((kc + m) ^ kkey(tok))]) = w[m];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint2 f = codes_f16(vr[n][m]);
+        w[m >> 1][2 * (m & 1)] = f.x;
+        w[m >> 1][2 * (m & 1) + 1] = f.y;
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_v[buf][d * kTile + 8 * ((vc + m) ^ (d & 7))]) = w[m];
+    }
+  };
+  if (t_begin < t_end) load(t_begin);
+
+  // this lane's column
+  const int cc = min(c0 + col, cols - 1), qt = cc / a.G, hq = h * a.G + (cc - qt * a.G);
+  const int pos = q.len - q.nq + qt;
+  const int hi = a.causal ? pos : q.len - 1, lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  f16x8 qf[NS][KS];
+  float m = -INFINITY, l = q.bad ? nan_f() : 0.0f, qscale;
+  {
+    const int64_t at = ((int64_t)q.row0 + qt) * a.q_stride + (int64_t)hq * D + 8 * hh;
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      float w[8];
+      if (a.xt == XF32) load8<XF32>(a.q, at + 16 * k, w);
+      else load8<XBF16>(a.q, at + 16 * k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(w[e]) & 0x7FFFFFFFu);
+    }
+    top = max(top, __float_as_uint(xor_lanes<32>(__uint_as_float(top))));
+    if (top >= 0x7F800000u) l = nan_f(), top = 0;
+    const int ex = (int)(top >> 23) - 127;  // below -100: as a row of zeros
+    const float up = ex >= -100 ? copysignf(__uint_as_float((uint32_t)(127 + 13 - ex) << 23), a.scale) : 0.0f;
+    qscale = ex >= -100 ? __uint_as_float((uint32_t)(127 - 13 + ex) << 23) * fabsf(a.scale) * kLog2e : 0.0f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      float w[8];
+      if (a.xt == XF32) load8<XF32>(a.q, at + 16 * k, w);
+      else load8<XBF16>(a.q, at + 16 * k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = l == l ? w[e] * up : 0.0f;
+        qf[0][k][e] = (_Float16)f;
+        if constexpr (NS == 2) qf[1][k][e] = (_Float16)(f - (float)qf[0][k][e]);
+      }
+    }
+  }
+  f32x16 acc[DT];
+#pragma unroll
+  for (int n = 0; n < DT; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[n][i] = 0.0f;
+  float R = 0.0f;  // the largest value scale so far; acc is in steps of R / 2^14
+
+  Scales sc{};
+  if (t_begin < t_end) {
+    stage(0);
+    sc = scales_of(ks_n, vs_n);
+    load(t_begin + 1);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int t = t_begin; t < t_end; ++t, buf ^= 1) {
+    if (any && t < mine.t1 && t >= mine.t0) {
+      f32x16 x[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int tok = 32 * b + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][tok * D + 8 * ((2 * k + hh) ^ kkey(tok))]);
+#pragma unroll
+          for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
+        }
+      }
+      const int base = t * kTile, first = base + 16 * hh;
+      if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (first + 32 * b + i > hi || first + 32 * b + i < lo) x[b][i] = -INFINITY;
+      }
+      const float f = fmaxf(qscale * sc.ks, 1e-37f);
+      float raw = x[0][0];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) raw = fmaxf(raw, x[b][i]);
+      if (raw > -INFINITY) l += sc.off;
+      raw = fmaxf(raw, xor_lanes<32>(raw)) * f;
+      if (raw == INFINITY) l = nan_f();
+      const float m1 = fmaxf(m, raw), ref = m1 > -INFINITY ? m1 : 0.0f;
+      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      m = m1;
+      const float R1 = fmaxf(R, sc.vs), down = R1 > 0.0f ? R / R1 : 1.0f, w = R1 > 0.0f ? sc.vs / R1 * 16384.0f : 0.0f;
+      R = R1;
+      f16x8 pf[NS][4];
+      float sum = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[b][i], f, -ref));
+          sum += p;
+          const float pw = p * w;
+          pf[0][2 * b + (i >> 3)][i & 7] = (_Float16)pw;
+          if constexpr (NS == 2) pf[1][2 * b + (i >> 3)][i & 7] = (_Float16)(pw - (float)pf[0][2 * b + (i >> 3)][i & 7]);
+        }
+      l = fmaf(l, alpha, sum);
+      const float scale = alpha * down;
+      if (__builtin_amdgcn_ballot_w64(scale != 1.0f)) {
+#pragma unroll
+        for (int n = 0; n < DT; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[n][i] *= scale;
+      }
+#pragma unroll
+      for (int n = 0; n < DT; ++n) {
+        const int d = 32 * n + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // block k / 2, step k % 2: tokens 32 (k / 2) + 16 hh + 8 (k % 2) ..
+          const f16x8 vf = *reinterpret_cast<const f16x8*>(&s_v[buf][d * kTile + 8 * ((4 * (k >> 1) + 2 * hh + (k & 1)) ^ (d & 7))]);
+#pragma unroll
+          for (int e = 0; e < NS; ++e) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[e][k], acc[n], 0, 0, 0);
+        }
+      }
+    }
+    if (t + 1 < t_end) {
+      stage(buf ^ 1);
+      sc = scales_of(ks_n, vs_n);
+      load(t + 2);
+    }
+    __syncthreads();
+  }
+  l += xor_lanes<32>(l);
+  if (c0 + col >= cols) return;
+  const int64_t orow = (int64_t)q.row0 + qt;
+  const float unit = R * (1.0f / 16384.0f);
+  if (active == 1) {
+    const float inv = l == 0.0f ? 0.0f : unit / l;
+#pragma unroll
+    for (int n = 0; n < DT; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        store_out4(a, orow, hq, D, 32 * n + 2 * i + 4 * hh, acc[n][i] * inv, acc[n][i + 1] * inv, acc[n][i + 2] * inv,
+                   acc[n][i + 3] * inv);
+  } else {
+    const int64_t slot = (orow * (a.G * c.Hkv) + hq) * a.splits + split;
+#pragma unroll
+    for (int n = 0; n < DT; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(a.part + slot * D + 32 * n + 2 * i + 4 * hh) =
+            make_float4(acc[n][i] * unit, acc[n][i + 1] * unit, acc[n][i + 2] * unit, acc[n][i + 3] * unit);
+    if (hh == 0) {
+      a.part_m[2 * slot] = m;
+      a.part_m[2 * slot + 1] = l;
+    }
+  }
+}
+
+// The splits of a row and head, one workgroup each: D / 4 lanes for the
+// channels, the other lanes share the splits out and meet in LDS.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttn a) {
+  constexpr int L = D / 4, P = 256 / L;
+  __shared__ float s_l[P];
+  __shared__ __attribute__((aligned(16))) float s_o[P][D];
+  const int s = blockIdx.z, head = blockIdx.y, part = threadIdx.x / L, d = 4 * ((int)threadIdx.x % L);
   const Seq q = seq_of(a.b, s, a.c.page);
-  if ((int)blockIdx.x >= q.nq || head >= a.G * a.c.Hkv) return;
+  if ((int)blockIdx.x >= q.nq) return;
   const int64_t row = (int64_t)q.row0 + blockIdx.x, slot0 = (row * (a.G * a.c.Hkv) + head) * a.splits;
-  const int cols = q.nq * a.G, ct = ((int)blockIdx.x * a.G + head % a.G) / 16;
-  const Span sp = span_of(a, q, ct * 16, min(ct * 16 + 16, cols));
+  const int cols = q.nq * a.G, ct = ((int)blockIdx.x * a.G + head % a.G) / a.tile;
+  const Span sp = span_of(a, q, ct * a.tile, min(ct * a.tile + a.tile, cols));
   const int active = (sp.t1 - sp.t0 + a.chunk - 1) / a.chunk;
   if (active <= 1) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_m) + slot0;
   float m = -INFINITY;
-  for (int i = 0; i < active; ++i) m = fmaxf(m, a.part_m[2 * (slot0 + i)]);
+  for (int i = threadIdx.x & 63; i < active; i += 64) m = fmaxf(m, ml[i].x);
+  m = group_max<64>(m);
   const float ref = m > -INFINITY ? m : 0.0f;
   float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < active; ++i) {
-    const float w = __builtin_amdgcn_exp2f(a.part_m[2 * (slot0 + i)] - ref), li = a.part_m[2 * (slot0 + i) + 1];
-    l += li == li ? w * li : li;
+#pragma unroll 4
+  for (int i = part; i < active; i += P) {
+    const float2 x = ml[i];
+    const float w = __builtin_amdgcn_exp2f(x.x - ref);
     const float4 p = *reinterpret_cast<const float4*>(a.part + (slot0 + i) * D + d);
+    l = fmaf(w, x.y, l);
     o[0] = fmaf(w, p.x, o[0]);
     o[1] = fmaf(w, p.y, o[1]);
     o[2] = fmaf(w, p.z, o[2]);
     o[3] = fmaf(w, p.w, o[3]);
+  }
+  *reinterpret_cast<float4*>(&s_o[part][d]) = make_float4(o[0], o[1], o[2], o[3]);
+  if (d == 0) s_l[part] = l;
+  __syncthreads();
+  if (part) return;
+  for (int i = 1; i < P; ++i) {
+    l += s_l[i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += s_o[i][d + r];
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   store_out4(a, row, head, D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
@@ -308,19 +653,29 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int c
   int64_t most = b.max_kv;
   if (causal && window && (int64_t)window + b.max_q < most) most = (int64_t)window + b.max_q;
   const int64_t tiles = (most + kTile - 1) / kTile + 1;
-  const int64_t base = (int64_t)b.S * c.Hkv * (((int64_t)b.max_q * G + 15) / 16);
-  int64_t chunk = (tiles * base + 1023) / 1024;
-  if (chunk < kWaves) chunk = kWaves;
   KvPlan p;
+  p.tile = (int64_t)b.max_q * G > 64 ? kRowCols : 16;
+  const int64_t base = (int64_t)b.S * c.Hkv * (((int64_t)b.max_q * G + p.tile - 1) / p.tile);
+  const int64_t want = p.tile == 16 ? 1024 : 512;
+  int64_t chunk = (tiles * base + want - 1) / want;
+  if (chunk < kWaves) chunk = kWaves;
+  chunk += chunk & 1;  // whole steps
   p.chunk = (int)(chunk < tiles ? chunk : tiles);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
   return p;
 }
 
-hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st) {
-  const int64_t cts = ((int64_t)a.b.max_q * a.G + 15) / 16;
+hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
+  KvAttn a = a0;
+  const int64_t cts = ((int64_t)a.b.max_q * a.G + a.tile - 1) / a.tile;
   const dim3 grid((unsigned)(a.splits * cts * a.c.Hkv), a.b.S), block(64 * kWaves);
-#define MD_ATT(D_, N_) hipLaunchKernelGGL((k_kv_attn<D_, N_>), grid, block, 0, st, a)
+  const int64_t groups = (int64_t)grid.x * grid.y;
+  a.snake = groups > device_cus() && groups <= 2 * device_cus();
+#define MD_ATT(D_, N_)                                                                     \
+  do {                                                                                     \
+    if (a.tile == 16) hipLaunchKernelGGL((k_kv_attn<D_, N_>), grid, block, 0, st, a);      \
+    else hipLaunchKernelGGL((k_kv_attn_rows<D_, N_ - 1>), grid, block, 0, st, a);          \
+  } while (0)
   if (yt == XF32) {
     if (D == 64) MD_ATT(64, 3);
     else if (D == 128) MD_ATT(128, 3);
@@ -333,7 +688,10 @@ hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st) {
 #undef MD_ATT
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(k_kv_join, dim3(a.b.max_q, (a.G * a.c.Hkv * D + 1023) / 1024, a.b.S), dim3(256), 0, st, a, D);
+  const dim3 jgrid(a.b.max_q, a.G * a.c.Hkv, a.b.S);
+  if (D == 64) hipLaunchKernelGGL((k_kv_join<64>), jgrid, dim3(256), 0, st, a);
+  else if (D == 128) hipLaunchKernelGGL((k_kv_join<128>), jgrid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((k_kv_join<256>), jgrid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

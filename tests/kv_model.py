@@ -72,7 +72,7 @@ class Cache:
         return v.transpose(0, 2, 1, 3).reshape(-1, v.shape[1], v.shape[3])[:n]
 
 
-def attention(q, k, v, scale, causal, window, out):
+def attention(q, k, v, scale, causal, window, out, many=False):
     """One sequence: q [n][Hq][D], k, v [len][Hkv][D] in 64 bits.  Returns the
     output and how far the library's may be off.
 
@@ -88,7 +88,14 @@ def attention(q, k, v, scale, causal, window, out):
       1 + e, e = score error + 4 u, and its grid by 1/2 + (its fma) < 1 step of 1 / t;
     - both sums are chains of one product and one addition a tile, and 16 terms
       in a lane, 2 levels across lanes, 4 waves and the splits: (2 tiles + 40) u.
-    The quotient takes both sums' errors."""
+    The quotient takes both sums' errors.
+
+    many (over 64 columns, max_q * Hq / Hkv): both products in f16 with fp32
+    sums.  A query's channel and a weight are off relatively by c = 2^-12 (bf16
+    outputs), or 2^-23 where a second f16 holds the first one's remainder (13 of
+    24 bits, rounded to 11), with floors (2^-25 of 2^14) that the weights show
+    as n 2^-38 max |v|; a sum of D products is off by D u of its terms' sizes, one
+    of n weights by n u."""
     n, Hq, D = q.shape
     L, Hkv = k.shape[0], k.shape[1]
     G, u, t = Hq // Hkv, 2.0 ** -24, TOP[out]
@@ -110,6 +117,11 @@ def attention(q, k, v, scale, causal, window, out):
             V = w @ np.abs(vv)
             chain = (2 * (hi - lo) / 64 + 40) * u
             grid = np.abs(vv).sum(0) / t / e.sum() + (hi - lo) / t / e.sum() * V
+            if many:
+                c = 2.0 ** -12 if out == "bf16" else 2.0 ** -23
+                ds = A * (c + D * u) + 24 * u * np.abs(s).max()
+                chain += c + (hi - lo) * u
+                grid = (hi - lo) * 2.0 ** -38 * np.abs(vv).max(0) / e.sum()
             tol[i, h] = 1.05 * (2 * (ds + 4 * u + chain) * V + grid) + HALF[out] * np.abs(o[i, h]) + 1e-37
     return o, tol
 

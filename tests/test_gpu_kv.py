@@ -214,6 +214,9 @@ ATTN = [  # key heads, group, dim, page, (new, length) of each sequence, causal,
     (1, 2, 64, 64, [(150, 150)], True, 0),
     (1, 4, 128, 64, [(130, 333)], True, 0),
     (1, 64, 64, 64, [(1, 100), (2, 70)], True, 0),
+    (2, 4, 128, 64, [(40, 1500), (3, 50), (17, 17)], True, 0),
+    (1, 16, 64, 128, [(4, 900), (5, 1000)], False, 0),
+    (1, 5, 256, 64, [(13, 700), (20, 90)], True, 200),
 ]
 
 
@@ -239,7 +242,7 @@ def test_attention(case, xt, out):
     worst = 0.0
     for i, (a, b) in enumerate(seqs):
         want, tol = attention(qn[at:at + a], m.values("k", table[i], b), m.values("v", table[i], b), scale, causal,
-                              window, out)
+                              window, out, many=max(nq) * G > 64)
         err = np.abs(got[at:at + a] - want)
         assert (err <= tol).all(), (i, float((err / tol).max()))
         worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()) if a else 0.0)
@@ -352,9 +355,11 @@ def test_scales_far_apart_and_large_scores():
     c = _to_gpu(m)
     q, qn = _rn(rng, (4, G, dim), "f32")
     for scale in (4.0, -4.0, 0.0):
-        y = md.kv_attention(c, _batch([4], lens, table), q, scale=scale).double().cpu().numpy()
-        want, tol = attention(qn, m.values("k", table[0], 300), m.values("v", table[0], 300), scale, True, 0, "f32")
-        assert (np.abs(y - want) <= tol).all()
+        for max_q in (4, 40):       # the forms for few and for many columns
+            y = md.kv_attention(c, _batch([4], lens, table, max_q=max_q), q, scale=scale).double().cpu().numpy()
+            want, tol = attention(qn, m.values("k", table[0], 300), m.values("v", table[0], 300), scale, True, 0,
+                                  "f32", many=max_q == 40)
+            assert (np.abs(y - want) <= tol).all()
 
 
 # ---- copies, and all of it together --------------------------------------------
@@ -466,7 +471,7 @@ def test_a_decoder_layer_eager_captured_forked_and_compacted():
         for n, s in zip(nq, seqs):
             t = int(kv.lens[s])
             want, tol = attention(qkv[at:at + n, :4], m.values("k", kv.tables[s], t), m.values("v", kv.tables[s], t),
-                                  0.125, True, 0, "f32")
+                                  0.125, True, 0, "f32", many=b.max_q * 2 > 64)
             assert (np.abs(a[at:at + n] - want) <= tol).all()
             at += n
     nq = [70, 33]
