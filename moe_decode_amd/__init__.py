@@ -487,7 +487,7 @@ def _xtype(dtype):
 
 def _dense(name, t, shape, dtype, device):
     """Checks what the C call cannot see: a tensor's type, shape, layout, device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} wanted, got "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
     return t
@@ -496,35 +496,60 @@ def _dense(name, t, shape, dtype, device):
 def _rows(name, t, heads, dim, device):
     """A [rows][heads][dim] tensor whose rows may be strided (a slice of a
     projection's output): its row stride in values."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.device != device:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.device != device:
         raise ValueError(f"{name}: a tensor [rows][{heads}][{dim}] on {device} wanted, got {tuple(t.shape)} on "
                          f"{t.device}")
-    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{name}: a row's heads and channels must lie together, got strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    st = t.stride()
+    if shape[0] and ((dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim)):
+        raise ValueError(f"{name}: a row's heads and channels must lie together, got strides {st}")
+    return st[0] if shape[0] > 1 else heads * dim
+
+
+def _raw_stream(index):
+    """The handle of a device's current stream (its object costs 2 us to make,
+    as long as a small kernel runs)."""
+    global _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
 
 
 class _on:
     """The device of a call's tensors made current, and its stream's handle."""
+    __slots__ = ("back", "stream")
 
     def __init__(self, device, stream):
         import torch
         if device.type != "cuda":
             raise ValueError(f"tensors on a GPU wanted, got {device}")
+        now, want = torch.cuda.current_device(), device.index
         self.back = None
-        now = torch.cuda.current_device()
-        if device.index is not None and device.index != now:
+        if want is not None and want != now:
             self.back = now
-            torch.cuda.set_device(device)
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+            torch.cuda.set_device(want)
+            now = want
+        self.stream = _raw_stream(now) if stream is None else stream.cuda_stream
 
     def __enter__(self):
         return self.stream
 
     def __exit__(self, *exc):
-        import torch
         if self.back is not None:
+            import torch
             torch.cuda.set_device(self.back)
+
+
+def _i8_desc(W):
+    """The C descriptor of an int8 matrix, made once while its tensors stay."""
+    d, q, sc = W.__dict__.get("_i8"), W.q.data_ptr(), _ptr(W.row_scale)
+    if d is None or d.q != q or d.row_scale != sc:
+        if W.count != 1:
+            raise ValueError(f"one matrix wanted, got a stack of {W.count}")
+        d = W._i8 = W.desc()
+        W._i8_ref = ctypes.byref(d)
+    return W._i8_ref
 
 
 def i8_quantize(x, codes=None, scales=None, stream=None):
@@ -544,8 +569,6 @@ def i8_quantize(x, codes=None, scales=None, stream=None):
 
 def _i8_args(W, T, bias, y, out_dtype, device):
     import torch
-    if W.count != 1:
-        raise ValueError(f"one matrix wanted, got a stack of {W.count}")
     if bias is not None:
         _dense("bias", bias, (W.rows,), torch.float32, device)
     if y is None:
@@ -564,14 +587,14 @@ def i8_matmul(W, codes, scales, bias=None, y=None, out_dtype=None, stream=None):
     _dense("scales", scales, (T,), torch.float32, dev)
     with _on(dev, stream) as st:
         y = _i8_args(W, T, bias, y, out_dtype, dev)
-        _check(lib().md_i8_matmul(ctypes.byref(W.desc()), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
+        _check(lib().md_i8_matmul(_i8_desc(W), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
                                   _xtype(y.dtype), st))
     return y
 
 
 def i8_linear_workspace_size(W, T):
     need = ctypes.c_size_t(0)
-    _check(lib().md_i8_linear_workspace_size(ctypes.byref(W.desc()), T, ctypes.byref(need)))
+    _check(lib().md_i8_linear_workspace_size(_i8_desc(W), T, ctypes.byref(need)))
     return need.value
 
 
@@ -581,12 +604,14 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
     _dense("x", x, (T, W.cols), x.dtype, dev)
     with _on(dev, stream) as st:
         y = _i8_args(W, T, bias, y, out_dtype, dev)
-        d = W.desc()
-        need = ctypes.c_size_t(0)
-        _check(lib().md_i8_linear_workspace_size(ctypes.byref(d), T, ctypes.byref(need)))
-        ws, wsb = _workspace(need.value, dev, workspace)
-        _check(lib().md_i8_linear(ctypes.byref(d), _ptr(x), _xtype(x.dtype), T, _ptr(bias), _ptr(y), _xtype(y.dtype),
-                                  _ptr(ws), wsb, st))
+        L, d = lib(), _i8_desc(W)
+        ws, wsb = None, 0
+        if T > 1:
+            need = ctypes.c_size_t(0)
+            _check(L.md_i8_linear_workspace_size(d, T, ctypes.byref(need)))
+            ws, wsb = _workspace(need.value, dev, workspace)
+        _check(L.md_i8_linear(d, x.data_ptr(), _xtype(x.dtype), T, _ptr(bias), y.data_ptr(), _xtype(y.dtype), _ptr(ws),
+                              wsb, st))
     return y
 
 
@@ -619,6 +644,7 @@ class KVCache:
         self.k_scale = _dense("k_scale", k_scale, (n, h), torch.float32, dev)
         self.v_scale = _dense("v_scale", v_scale, (n, h), torch.float32, dev)
         self.desc = KVCacheDesc(n, p, h, d, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self.desc)
 
     @classmethod
     def empty(cls, n_pages, kv_heads, head_dim, page=64, device="cuda"):
@@ -645,11 +671,17 @@ class KVBatch:
         self.max_q, self.max_kv, self.device = max_q, max_kv, dev
         self._desc = KVBatchDesc(S, 0, max_q, max_kv, table.shape[1], q_start.data_ptr(), kv_len.data_ptr(),
                                  table.data_ptr())
+        self._made = (-1, None)
 
     def desc(self, rows):
-        d = KVBatchDesc.from_buffer_copy(self._desc)
-        d.rows = rows
-        return d
+        """The C descriptor for a call on `rows` rows: the last one again, or a
+        new one (one that another thread's call may be reading is not changed)."""
+        made = self._made
+        if made[0] != rows:
+            d = KVBatchDesc.from_buffer_copy(self._desc)
+            d.rows = rows
+            made = self._made = (rows, ctypes.byref(d))
+        return made[1]
 
 
 def kv_append(cache, batch, k, v, stream=None):
@@ -660,13 +692,13 @@ def kv_append(cache, batch, k, v, stream=None):
     if k.dtype != v.dtype or k.shape[0] != v.shape[0] or batch.device != cache.device:
         raise ValueError(f"k and v of one type and length, the batch on {cache.device} wanted")
     with _on(cache.device, stream) as st:
-        _check(lib().md_kv_append(ctypes.byref(cache.desc), ctypes.byref(batch.desc(k.shape[0])), _ptr(k), ks, _ptr(v),
+        _check(lib().md_kv_append(cache._ref, batch.desc(k.shape[0]), _ptr(k), ks, _ptr(v),
                                   vs, _xtype(k.dtype), st))
 
 
 def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0):
     need = ctypes.c_size_t(0)
-    _check(lib().md_kv_attention_workspace_size(ctypes.byref(cache.desc), ctypes.byref(batch.desc(rows)), q_heads,
+    _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads,
                                                 int(causal), window, ctypes.byref(need)))
     return need.value
 
@@ -694,10 +726,9 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         os_ = _rows("out", out, heads, cache.head_dim, cache.device)
         L, d = lib(), batch.desc(rows)
         need = ctypes.c_size_t(0)
-        _check(L.md_kv_attention_workspace_size(ctypes.byref(cache.desc), ctypes.byref(d), heads, int(causal), window,
-                                                ctypes.byref(need)))
+        _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, ctypes.byref(need)))
         ws, wsb = _workspace(need.value, cache.device, workspace)
-        _check(L.md_kv_attention(ctypes.byref(cache.desc), ctypes.byref(d), _ptr(q), _xtype(q.dtype), heads, qs,
+        _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
                                  dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out),
                                  _xtype(out.dtype), os_, _ptr(ws), wsb, st))
     return out
@@ -714,19 +745,20 @@ def kv_read_pages(cache, pages, k=None, v=None, out_dtype=None, stream=None):
         dt = out_dtype or (k.dtype if k is not None else torch.float32)
         k = torch.empty(shape, dtype=dt, device=dev) if k is None else _dense("k", k, shape, dt, dev)
         v = torch.empty(shape, dtype=dt, device=dev) if v is None else _dense("v", v, shape, dt, dev)
-        _check(lib().md_kv_read_pages(ctypes.byref(cache.desc), _ptr(pages), n, _ptr(k), _ptr(v), _xtype(dt), st))
+        _check(lib().md_kv_read_pages(cache._ref, _ptr(pages), n, _ptr(k), _ptr(v), _xtype(dt), st))
     return k, v
 
 
 def kv_copy_pages(cache, src, dst, stream=None):
     """Page dst[i] of the cache becomes page src[i] (host sequences of page
     numbers); a page that is written appears once among all of them."""
+    from array import array
+    src, dst = array("i", src), array("i", dst)
     n = len(src)
     if len(dst) != n:
         raise ValueError(f"{n} source pages and {len(dst)} destinations")
-    array = ctypes.c_int32 * max(n, 1)
     with _on(cache.device, stream) as st:
-        _check(lib().md_kv_copy_pages(ctypes.byref(cache.desc), array(*src), array(*dst), n, st))
+        _check(lib().md_kv_copy_pages(cache._ref, src.buffer_info()[0], dst.buffer_info()[0], n, st))
 
 
 class KVPagesState(ctypes.Structure):

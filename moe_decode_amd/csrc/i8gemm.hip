@@ -20,10 +20,36 @@ namespace md {
 
 // ---- codes ---------------------------------------------------------------
 
+// A row's scale from its largest magnitude's bits.  One that holds an infinity
+// or a NaN gets the scale NaN and codes 0, so its products are NaN and no other
+// row's are.
+struct RowScale {
+  float s, up, ss, inv;
+  bool none;
+};
+MD_DEV RowScale row_scale_of(uint32_t top) {
+  RowScale o;
+  const float amax = __uint_as_float(top);
+  const bool bad = top >= 0x7F800000u;
+  o.s = bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
+  o.up = amax < kTiny ? kTinyUp : 1.0f;
+  o.none = bad || !(o.s > 0.0f);
+  o.ss = o.none ? 1.0f : o.s * o.up;
+  o.inv = 1.0f / o.ss;
+  return o;
+}
+MD_DEV uint2 codes8(const float (&v)[8], const RowScale& s) {
+  uint32_t w[2] = {0, 0};
+  if (!s.none) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) w[m >> 2] |= (uint32_t)(code_of(v[m] * s.up, s.ss, s.inv) & 255) << (8 * (m & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // One row per group of WPR waves (WPR 1: four rows a workgroup), the whole row
 // in registers between the maximum and the codes: x is read once.  Bound by
-// the read of x.  A row that holds an infinity or a NaN gets the scale NaN and
-// codes 0, so its products are NaN and no other row's are.
+// the read of x.
 template <int XT, int WPR, int STEPS>
 __global__ __launch_bounds__(256) void k_i8_quantize(const void* __restrict__ x, int T, int K,
                                                      int8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -56,23 +82,12 @@ __global__ __launch_bounds__(256) void k_i8_quantize(const void* __restrict__ x,
     __syncthreads();
     top = max(max(red[0], red[1]), max(red[2], red[3]));
   }
-  const float amax = __uint_as_float(top);
-  const bool bad = top >= 0x7F800000u;
-  const float s = bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
-  if (at == 0) scales[row] = s;
-  const float up = amax < kTiny ? kTinyUp : 1.0f;
-  const bool none = bad || !(s > 0.0f);
-  const float ss = none ? 1.0f : s * up, inv = 1.0f / ss;
+  const RowScale s = row_scale_of(top);
+  if (at == 0) scales[row] = s.s;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int c = at + i * kStep;
-    if (c >= K) continue;
-    uint32_t w[2] = {0, 0};
-    if (!none) {
-#pragma unroll
-      for (int m = 0; m < 8; ++m) w[m >> 2] |= (uint32_t)(code_of(v[i][m] * up, ss, inv) & 255) << (8 * (m & 3));
-    }
-    *reinterpret_cast<uint2*>(codes + base + c) = make_uint2(w[0], w[1]);
+    if (c < K) *reinterpret_cast<uint2*>(codes + base + c) = codes8(v[i], s);
   }
 }
 
@@ -95,6 +110,10 @@ hipError_t launch_i8_quantize(const void* x, int xt, int T, int K, int8_t* codes
 }
 
 // ---- products ------------------------------------------------------------
+
+constexpr int kOwnTokens = 1;      // up to these: each workgroup forms the codes itself
+constexpr int kFewTokens = 32;     // up to these: k_i8_few
+constexpr int kSplitTokens = 512;  // up to these the sum may be split
 
 // Four consecutive outputs of one token; the ones past N are left alone.
 template <int YT>
@@ -131,25 +150,65 @@ MD_DEV void put4(void* y, int64_t row, int N, int n, const i32x4& a, float xs, c
 // its waves split the sum and meet in LDS.  Weights go from HBM straight into
 // the matrix cores' operand registers (lane l: row l % 16, 16 bytes at
 // 64 step + 16 (l / 16)), codes of x from the L2.
-template <int YT, int NT>
+// OWN (one token; four took longer, 12.8 -> 21.7 us at 6144 x 6144): x itself comes in, and every workgroup
+// rounds the whole rows to codes in its LDS while its first weights are on
+// their way: one launch less, which is half of a small call.
+template <int YT, int NT, bool OWN, int XT>
 __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, const float* __restrict__ ws, int N,
-                                                 int K, const int8_t* __restrict__ xq, const float* __restrict__ xs,
+                                                 int K, const void* __restrict__ x, const float* __restrict__ xs_in,
                                                  int T, const float* __restrict__ bias, void* __restrict__ y) {
-  extern __shared__ int part[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  extern __shared__ __attribute__((aligned(16))) int8_t few_lds[];  // shares of the sum; OWN: then T rows of codes
+  __shared__ uint32_t red[kOwnTokens][16];
+  int* part = reinterpret_cast<int*>(few_lds);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int n0 = blockIdx.x * 16, r = lane & 15, g = lane >> 4;
   const int8_t* wp = W + (int64_t)min(n0 + r, N - 1) * K + 16 * g;
-  const int8_t* xp[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) xp[t] = xq + (int64_t)min(t * 16 + r, T - 1) * K + 16 * g;
-  i32x4 acc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+  i32x4 a[4], acc[NT];
   // wave w takes the 256-byte pieces w, w + nw, ...
-  for (int k = wave * 256; k < K; k += nw * 256) {
-    i32x4 a[4], b[NT][4];
+  auto weights = [&](int k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const i32x4*>(wp + k + 64 * i);
+  };
+  if (wave * 256 < K) weights(wave * 256);
+  const int8_t* xp[NT];
+  float own = 0.0f;  // OWN: the scale of this lane's token
+  if constexpr (OWN) {
+    int8_t* codes = few_lds + nw * 1024;
+    uint32_t top[kOwnTokens] = {};
+    for (int t = 0; t < T; ++t)
+      for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
+        float v[8];
+        load8<XT>(x, (int64_t)t * K + c, v);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) top[t] = max(top[t], __float_as_uint(v[m]) & 0x7FFFFFFFu);
+      }
+#pragma unroll
+    for (int t = 0; t < kOwnTokens; ++t) {
+      const uint32_t w = wave_max_u32(top[t]);
+      if (lane == 0) red[t][wave] = w;
+    }
+    __syncthreads();
+    for (int t = 0; t < T; ++t) {
+      uint32_t m = 0;
+      for (int w = 0; w < nw; ++w) m = max(m, red[t][w]);
+      const RowScale s = row_scale_of(m);
+      if (t == min(r, T - 1)) own = s.s;
+      for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
+        float v[8];
+        load8<XT>(x, (int64_t)t * K + c, v);
+        *reinterpret_cast<uint2*>(codes + t * K + c) = codes8(v, s);
+      }
+    }
+    __syncthreads();
+    xp[0] = codes + min(r, T - 1) * K + 16 * g;
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xp[t] = static_cast<const int8_t*>(x) + (int64_t)min(t * 16 + r, T - 1) * K + 16 * g;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+  for (int k = wave * 256; k < K;) {
+    i32x4 b[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -158,6 +217,8 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[t][i], acc[t], 0, 0, 0);
+    k += nw * 256;
+    if (k < K) weights(k);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) *reinterpret_cast<i32x4*>(part + ((wave * NT + t) * 64 + lane) * 4) = acc[t];
@@ -166,17 +227,37 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
     i32x4 sum{0, 0, 0, 0};
     for (int w = 0; w < nw; ++w) sum += *reinterpret_cast<const i32x4*>(part + ((w * NT + t) * 64 + lane) * 4);
     const int tok = t * 16 + r, n = n0 + 4 * g;
-    if (tok < T && n < N) put4<YT>(y, tok, N, n, sum, xs[tok], ws, bias);
+    if (tok < T && n < N) put4<YT>(y, tok, N, n, sum, OWN ? own : xs_in[tok], ws, bias);
   }
 }
 
 // Many tokens: BN channels x BT tokens per workgroup of WN x WT waves, 128
-// bytes of the sum per step, double-buffered in LDS.  Chunk p (16 bytes) of
-// tile row r holds chunk p ^ (r & 7) of the row, so the 16 rows that a fragment
-// read touches spread over the banks.
+// bytes of the sum per step, ST steps' tiles in LDS, filled ST - 1 steps ahead
+// by direct loads.  Chunk p (16 bytes) of tile row r holds chunk p ^ (r & 7) of
+// the row, so the rows that a fragment read touches spread over the banks (no
+// conflicts counted).  Every stage is a variable of its own and the loop is
+// unrolled over them: the compiler waits for all direct loads in flight before
+// an LDS read that might touch what they fill, and can only tell variables
+// apart (404 -> 326 us for 8191 tokens, 5632 channels, 6144 terms with the
+// quantizer's 35).  The large tile is bound by LDS reads, which deliver 64
+// bytes a clock here: 24 of 1 KB per wave and step against 64 products of 16
+// clocks, 1.95 Pop/s of 2.35 that a large library product reaches.  Measured
+// and dropped: fragments read half a step ahead (332), 64-byte steps in four
+// stages (342), four waves of 128 x 128 outputs (spills: 683), the weights
+// straight from L1 into registers (451 to 488).
 constexpr int kBK = 128;
 
-template <int YT, int BN, int BT, int WN, int WT>
+// All but the n youngest of this wave's loads have landed, and all waves are here.
+template <int N>
+MD_DEV void landed() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// part: one of gridDim.y equal shares of the sum, as int32 [share][T][N]; else y.
+template <int YT, int BN, int BT, int WN, int WT, int ST, bool PART>
 __global__ __launch_bounds__(64 * WN * WT) void k_i8_tile(const int8_t* __restrict__ W, const float* __restrict__ ws,
                                                           int N, int K, const int8_t* __restrict__ xq,
                                                           const float* __restrict__ xs, int T,
@@ -185,8 +266,8 @@ __global__ __launch_bounds__(64 * WN * WT) void k_i8_tile(const int8_t* __restri
   constexpr int NW = WN * WT, RN = BN / WN / 16, RT = BT / WT / 16;
   constexpr int LW = BN * kBK / 1024 / NW, LX = BT * kBK / 1024 / NW;  // 1 KB loads per wave and step
   static_assert(LW * NW * 1024 == BN * kBK && LX * NW * 1024 == BT * kBK, "tile");
-  __shared__ __attribute__((aligned(16))) int8_t sw[2][BN * kBK];
-  __shared__ __attribute__((aligned(16))) int8_t sx[2][BT * kBK];
+  __shared__ __attribute__((aligned(16))) int8_t w0[BN * kBK], w1[BN * kBK], w2[ST > 2 ? BN * kBK : 16], w3[ST > 2 ? BN * kBK : 16];
+  __shared__ __attribute__((aligned(16))) int8_t x0[BT * kBK], x1[BT * kBK], x2[ST > 2 ? BT * kBK : 16], x3[ST > 2 ? BT * kBK : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups go round the 8 dies: give each die a run of neighbouring tiles
   const int total = tn * tt, per = (total + 7) >> 3;
@@ -195,25 +276,27 @@ __global__ __launch_bounds__(64 * WN * WT) void k_i8_tile(const int8_t* __restri
   constexpr int kGroup = 4;
   const int band = id / (kGroup * tn), in = id % (kGroup * tn), rows = min(kGroup, tt - band * kGroup);
   const int t0 = (band * kGroup + in % rows) * BT, n0 = (in / rows) * BN;
+  const int share = PART ? K / (int)gridDim.y : K, k0 = PART ? (int)blockIdx.y * share : 0;
 
   const int lr = lane >> 3, lc = (lane & 7) ^ lr;  // row and chunk of a load's 8 rows
   const int8_t* wsrc[LW];
   const int8_t* xsrc[LX];
 #pragma unroll
-  for (int i = 0; i < LW; ++i) wsrc[i] = W + (int64_t)min(n0 + (wave * LW + i) * 8 + lr, N - 1) * K + 16 * lc;
+  for (int i = 0; i < LW; ++i) wsrc[i] = W + (int64_t)min(n0 + (wave * LW + i) * 8 + lr, N - 1) * K + k0 + 16 * lc;
 #pragma unroll
-  for (int i = 0; i < LX; ++i) xsrc[i] = xq + (int64_t)min(t0 + (wave * LX + i) * 8 + lr, T - 1) * K + 16 * lc;
-  auto load = [&](int buf, int k) {
+  for (int i = 0; i < LX; ++i) xsrc[i] = xq + (int64_t)min(t0 + (wave * LX + i) * 8 + lr, T - 1) * K + k0 + 16 * lc;
+  const int steps = share / kBK;
+  // past the last step that one again: the number in flight stays the same
+  auto load = [&](int8_t* sw, int8_t* sx, int step) {
+    const int k = min(step, steps - 1) * kBK;
 #pragma unroll
     for (int i = 0; i < LW; ++i)
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wsrc[i] + k),
-                                       (__attribute__((address_space(3))) void*)(&sw[buf][(wave * LW + i) * 1024]), 16,
-                                       0, 0);
+                                       (__attribute__((address_space(3))) void*)(sw + (wave * LW + i) * 1024), 16, 0, 0);
 #pragma unroll
     for (int i = 0; i < LX; ++i)
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xsrc[i] + k),
-                                       (__attribute__((address_space(3))) void*)(&sx[buf][(wave * LX + i) * 1024]), 16,
-                                       0, 0);
+                                       (__attribute__((address_space(3))) void*)(sx + (wave * LX + i) * 1024), 16, 0, 0);
   };
   const int wn = wave % WN, wt = wave / WN, r = lane & 15, g = lane >> 4;
   i32x4 acc[RN][RT];
@@ -221,14 +304,9 @@ __global__ __launch_bounds__(64 * WN * WT) void k_i8_tile(const int8_t* __restri
   for (int i = 0; i < RN; ++i)
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  load(0, 0);
-  const int steps = K / kBK;
-  for (int s = 0; s < steps; ++s) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this step's tile has landed
-    __syncthreads();
-    if (s + 1 < steps) load((s + 1) & 1, (s + 1) * kBK);
-    const int8_t* bw = &sw[s & 1][(wn * RN * 16 + r) * kBK];
-    const int8_t* bx = &sx[s & 1][(wt * RT * 16 + r) * kBK];
+  auto multiply = [&](const int8_t* sw, const int8_t* sx) {
+    const int8_t* bw = sw + (wn * RN * 16 + r) * kBK;
+    const int8_t* bx = sx + (wt * RT * 16 + r) * kBK;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int o = ((4 * h + g) ^ (r & 7)) * 16;
@@ -242,53 +320,144 @@ __global__ __launch_bounds__(64 * WN * WT) void k_i8_tile(const int8_t* __restri
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
     }
-    __syncthreads();
+  };
+  load(w0, x0, 0);
+  if constexpr (ST == 4) {
+    load(w1, x1, 1);
+    load(w2, x2, 2);
   }
+  constexpr int kFly = (ST - 2) * (LW + LX);
+  for (int s = 0;;) {
+#define MD_STEP(W_, X_, NW_, NX_)  \
+  landed<kFly>();                  \
+  load(NW_, NX_, s + ST - 1);      \
+  __builtin_amdgcn_sched_barrier(0); \
+  multiply(W_, X_);                \
+  if (++s == steps) break;
+    if constexpr (ST == 2) {
+      MD_STEP(w0, x0, w1, x1)
+      MD_STEP(w1, x1, w0, x0)
+    } else {
+      MD_STEP(w0, x0, w3, x3)
+      MD_STEP(w1, x1, w0, x0)
+      MD_STEP(w2, x2, w1, x1)
+      MD_STEP(w3, x3, w2, x2)
+    }
+#undef MD_STEP
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // no load into this workgroup's LDS outlives it
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int tok = t0 + (wt * RT + j) * 16 + r;
     if (tok >= T) continue;
-    const float sc = xs[tok];
+    const float sc = PART ? 0.0f : xs[tok];
 #pragma unroll
     for (int i = 0; i < RN; ++i) {
       const int n = n0 + (wn * RN + i) * 16 + 4 * g;
-      if (n < N) put4<YT>(y, tok, N, n, acc[i][j], sc, ws, bias);
+      if (n >= N) continue;
+      if constexpr (PART) {  // rows of N rounded up to 4
+        const int64_t np = (N + 3) & ~3;
+        *reinterpret_cast<i32x4*>(static_cast<int*>(y) + ((int64_t)blockIdx.y * T + tok) * np + n) = acc[i][j];
+      } else {
+        put4<YT>(y, tok, N, n, acc[i][j], sc, ws, bias);
+      }
     }
   }
 }
 
+// The shares of four outputs a thread, added and scaled.
+template <int YT>
+__global__ __launch_bounds__(256) void k_i8_join(const int* __restrict__ part, int S, int T, int N,
+                                                 const float* __restrict__ ws, const float* __restrict__ xs,
+                                                 const float* __restrict__ bias, void* __restrict__ y) {
+  const int n = 4 * (blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
+  const int64_t np = (N + 3) & ~3;
+  if (n >= N) return;
+  i32x4 a{0, 0, 0, 0};
+  for (int s = 0; s < S; ++s) a += *reinterpret_cast<const i32x4*>(part + ((int64_t)s * T + t) * np + n);
+  put4<YT>(y, t, N, n, a, xs[t], ws, bias);
+}
+
+// How many shares of the sum make enough workgroups where the outputs alone do
+// not: whole steps each, four at least, and together at most one workgroup a
+// compute unit (128 tokens, 6144 channels, 6144 terms: two shares 25 us, four
+// with up to 512 workgroups 28.6; without shares, on 64 x 64 tiles, 38).
+int i8_shares(int N, int K, int T) {
+  if (T <= kFewTokens || T > kSplitTokens) return 1;
+  const int64_t tiles = (int64_t)((N + 63) / 64) * ((T + 127) / 128);
+  int best = 1;
+  for (int s = 2; s <= 16 && tiles * s <= 256; ++s)
+    if (K % (s * kBK) == 0 && K / (s * kBK) >= 4) best = s;
+  return best;
+}
+
+static int few_waves(int K) { return K <= 1024 ? 4 : K <= 4096 ? 8 : 16; }
+
+bool i8_own_codes(int T) { return T <= kOwnTokens; }
+
+hipError_t launch_i8_own(const int8_t* W, const float* ws, int N, int K, const void* x, int xt, int T,
+                         const float* bias, void* y, int yt, hipStream_t st) {
+  const int nw = few_waves(K);
+  const dim3 grid((N + 15) / 16), block(64 * nw);
+  const size_t lds = (size_t)nw * 1024 + (size_t)T * K;
+#define MD_OWN(Y_, X_)                                                                                             \
+  hipLaunchKernelGGL((k_i8_few<Y_, 1, true, X_>), grid, block, lds, st, W, ws, N, K, x, (const float*)nullptr, T, bias, y)
+  if (yt == XF32) {
+    if (xt == XF32) MD_OWN(XF32, XF32);
+    else MD_OWN(XF32, XBF16);
+  } else {
+    if (xt == XF32) MD_OWN(XBF16, XF32);
+    else MD_OWN(XBF16, XBF16);
+  }
+#undef MD_OWN
+  return hipGetLastError();
+}
+
 template <int YT>
 static hipError_t matmul(const int8_t* W, const float* ws, int N, int K, const int8_t* xq, const float* xs, int T,
-                         const float* bias, void* y, hipStream_t st) {
-  if (T <= 64) {
-    const int nw = K <= 1024 ? 4 : K <= 4096 ? 8 : 16;
+                         const float* bias, void* y, int shares, int* part, hipStream_t st) {
+  if (T <= kFewTokens) {
+    const int nw = few_waves(K);
     const dim3 grid((N + 15) / 16), block(64 * nw);
-#define MD_FEW(NT_)                                                                                                  \
-  hipLaunchKernelGGL((k_i8_few<YT, NT_>), grid, block, (size_t)nw * NT_ * 1024, st, W, ws, N, K, xq, xs, T, bias, y)
-    if (T <= 16) MD_FEW(1);
-    else if (T <= 32) MD_FEW(2);
-    else MD_FEW(4);
-#undef MD_FEW
+    if (T <= 16)
+      hipLaunchKernelGGL((k_i8_few<YT, 1, false, XF32>), grid, block, (size_t)nw * 1024, st, W, ws, N, K, xq, xs, T, bias, y);
+    else
+      hipLaunchKernelGGL((k_i8_few<YT, 2, false, XF32>), grid, block, (size_t)nw * 2048, st, W, ws, N, K, xq, xs, T, bias, y);
     return hipGetLastError();
   }
-  auto tiles = [&](int b) { return (int64_t)((N + b - 1) / b) * ((T + b - 1) / b); };
-#define MD_TILE(B_, WN_, WT_)                                                                                       \
+  auto tiles = [&](int bn, int bt) { return (int64_t)((N + bn - 1) / bn) * ((T + bt - 1) / bt); };
+#define MD_TILE(BN_, BT_, WN_, WT_, ST_, P_, Y_, S_)                                                                  \
   do {                                                                                                              \
-    const int tn = (N + B_ - 1) / B_, tt = (T + B_ - 1) / B_;                                                       \
-    hipLaunchKernelGGL((k_i8_tile<YT, B_, B_, WN_, WT_>), dim3((unsigned)((((int64_t)tn * tt + 7) >> 3) << 3)),     \
-                       dim3(64 * WN_ * WT_), 0, st, W, ws, N, K, xq, xs, T, bias, y, tn, tt);                       \
+    const int tn = (N + BN_ - 1) / BN_, tt = (T + BT_ - 1) / BT_;                                                   \
+    hipLaunchKernelGGL((k_i8_tile<YT, BN_, BT_, WN_, WT_, ST_, P_>),                                                \
+                       dim3((unsigned)((((int64_t)tn * tt + 7) >> 3) << 3), S_), dim3(64 * WN_ * WT_), 0, st, W, ws, \
+                       N, K, xq, xs, T, bias, Y_, tn, tt);                                                          \
   } while (0)
-  if (tiles(256) >= 256) MD_TILE(256, 4, 2);
-  else if (tiles(128) >= 128) MD_TILE(128, 2, 2);
-  else MD_TILE(64, 2, 2);
+  if (shares > 1) {
+    MD_TILE(64, 128, 2, 2, 4, true, part, shares);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_i8_join<YT>), dim3((N + 1023) / 1024, T), dim3(256), 0, st, part, shares, T, N, ws, xs, bias,
+                       y);
+  } else if (tiles(256, 256) >= 192) {  // large tiles where they fill the chip: 2048 tokens, 6144 x 6144, 139 -> 113 us
+                                       // against the next size; below 192 of them slower (1024 tokens: 77 against 100)
+    MD_TILE(256, 256, 4, 2, 2, false, y, 1);
+  } else if (tiles(128, 128) >= 256) {  // 384 tokens, 6144 x 2048: 27.9 on 144 of these, 25.6 on the small ones
+    MD_TILE(128, 128, 2, 2, 2, false, y, 1);
+  } else {
+    MD_TILE(64, 64, 2, 2, 4, false, y, 1);
+  }
 #undef MD_TILE
   return hipGetLastError();
 }
 
+// part: i8_shares() * T * (N rounded up to 4) int32, or null (no split: the same
+// bits from fewer workgroups).
 hipError_t launch_i8_matmul(const int8_t* W, const float* ws, int N, int K, const int8_t* xq, const float* xs, int T,
-                            const float* bias, void* y, int yt, hipStream_t st) {
-  return yt == XF32 ? matmul<XF32>(W, ws, N, K, xq, xs, T, bias, y, st)
-                    : matmul<XBF16>(W, ws, N, K, xq, xs, T, bias, y, st);
+                            const float* bias, void* y, int yt, int* part, hipStream_t st) {
+  const int shares = part ? i8_shares(N, K, T) : 1;
+  return yt == XF32 ? matmul<XF32>(W, ws, N, K, xq, xs, T, bias, y, shares, part, st)
+                    : matmul<XBF16>(W, ws, N, K, xq, xs, T, bias, y, shares, part, st);
 }
 
 }  // namespace md

@@ -55,8 +55,13 @@ md_status check_device(const char* what, const void* p) {
   return MD_OK;
 }
 
-// codes, then scales
+// md_i8_linear's workspace: codes, scales, shares of the sum
 size_t codes_bytes(int32_t T, int32_t K) { return align256((size_t)T * K); }
+size_t scales_bytes(int32_t T) { return align256(sizeof(float) * (size_t)T); }
+size_t shares_bytes(const md_qmatrix* W, int32_t T) {
+  const int s = md::i8_shares(W->rows, W->cols, T);
+  return s > 1 ? align256(sizeof(int) * (size_t)s * T * ((W->rows + 3) & ~3)) : 0;
+}
 
 md_status check_cache(const md_kv_cache* c) {
   if (!c) return fail(MD_ERR_INVALID_ARG, "null cache descriptor");
@@ -196,7 +201,7 @@ md_status md_i8_matmul(const md_qmatrix* W, const int8_t* codes, const float* sc
       (s = check_device("y", y)) != MD_OK || (bias && (s = check_device("bias", bias)) != MD_OK))
     return s;
   const hipError_t e = md::launch_i8_matmul(static_cast<const int8_t*>(W->q), W->row_scale, W->rows, W->cols, codes,
-                                            scales, T, bias, y, ytype, stream);
+                                            scales, T, bias, y, ytype, nullptr, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "i8 product launch");
 }
 
@@ -204,7 +209,7 @@ md_status md_i8_linear_workspace_size(const md_qmatrix* W, int32_t T, size_t* by
   const md_status s = check_i8(W, T);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
-  *bytes = T ? codes_bytes(T, W->cols) + align256(sizeof(float) * (size_t)T) : 0;
+  *bytes = T && !md::i8_own_codes(T) ? codes_bytes(T, W->cols) + scales_bytes(T) + shares_bytes(W, T) : 0;
   return ok();
 }
 
@@ -218,6 +223,11 @@ md_status md_i8_linear(const md_qmatrix* W, const void* x, int32_t xtype, int32_
   if ((s = check_device("x", x)) != MD_OK || (s = check_device("y", y)) != MD_OK ||
       (bias && (s = check_device("bias", bias)) != MD_OK))
     return s;
+  if (md::i8_own_codes(T)) {
+    const hipError_t e = md::launch_i8_own(static_cast<const int8_t*>(W->q), W->row_scale, W->rows, W->cols, x, xtype, T,
+                                           bias, y, ytype, stream);
+    return e == hipSuccess ? ok() : hip_fail(e, "i8 linear launch");
+  }
   if (!workspace || workspace_bytes < need)
     return fail(MD_ERR_WORKSPACE, "workspace: %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
   if (!aligned16(workspace)) return fail(MD_ERR_ALIGNMENT, "workspace not 16-byte aligned");
@@ -225,8 +235,9 @@ md_status md_i8_linear(const md_qmatrix* W, const void* x, int32_t xtype, int32_
   float* scales = reinterpret_cast<float*>(codes + codes_bytes(T, W->cols));
   hipError_t e = md::launch_i8_quantize(x, xtype, T, W->cols, codes, scales, stream);
   if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  int* part = shares_bytes(W, T) ? reinterpret_cast<int*>(reinterpret_cast<char*>(scales) + scales_bytes(T)) : nullptr;
   e = md::launch_i8_matmul(static_cast<const int8_t*>(W->q), W->row_scale, W->rows, W->cols, codes, scales, T, bias, y,
-                           ytype, stream);
+                           ytype, part, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "i8 product launch");
 }
 

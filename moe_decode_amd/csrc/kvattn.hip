@@ -77,6 +77,10 @@ MD_DEV i32x4 load16(rsrc_t r, int off, int soff) {
   return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
+// Inside a wave-uniform branch around cheap work: without it the compiler may
+// turn the branch into selects that every tile pays for.
+MD_DEV void keep_branch() { asm volatile(""); }
+
 MD_DEV float nan_f() { return __uint_as_float(0x7FC00000u); }
 
 // A column's query digits (the lane's 16 channels of each 64) and its state.
@@ -137,13 +141,13 @@ MD_DEV void column_init(Column<D, ND>& o, const KvAttn& a, const Seq& q, int h, 
     }
 }
 
-// A page's scales for a head.  One that the append did not write (negative or
-// not finite) makes the rows that see the page NaN: off is added to their sums.
+// A page's scales for a head.  One that the append does not write (negative,
+// not finite, past 2^126) makes the rows that see the page NaN: off is added to their sums.
 struct Scales {
   float ks, vs, off;
 };
 MD_DEV Scales scales_of(float ks, float vs) {
-  const bool good = ks >= 0.0f && ks < INFINITY && vs >= 0.0f && vs < INFINITY;
+  const bool good = ks >= 0.0f && ks < 0x1p126f && vs >= 0.0f && vs < 0x1p126f;
   return Scales{good ? ks : 0.0f, good ? vs : 0.0f, good ? 0.0f : nan_f()};
 }
 
@@ -157,6 +161,7 @@ MD_DEV float advance(Column<D, ND>& o, float (&x)[N], const float (&f)[N / 16], 
 #pragma unroll
   for (int t = 0; t < N / 16; ++t) {
     if (cut) {
+      keep_branch();
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (first + 64 * t + i > o.hi || first + 64 * t + i < o.lo) x[16 * t + i] = -INFINITY;
@@ -356,8 +361,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 // they run on the f16 matrix cores, which accumulate in fp32 and need no joins:
 // the codes are exact in f16 (converted once per workgroup on their way to
 // LDS), a query row is scaled by a power of two to below 2^14 and rounded to
-// f16, and so is a weight p times 2^14 vs / R, R the largest value scale met so
-// far.  NS = 2 (fp32 outputs) takes a second f16 for what the first one leaves,
+// f16, and so is a weight p times 2^14 vs / R, R the power of two at or below
+// the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second f16 for what the first one leaves,
 // 22 bits together.  Per score that leaves half a maximum, one fma, one exp2
 // (a quarter of the rate), the sum and half a conversion on the vector ALU.
 //
@@ -406,8 +411,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   const int pshift = a.pshift;
   u32x4 kr[L], vr[L];
   float ks_n, vs_n;
-  auto load = [&](int t) {  // tile t's codes and scales; a page that is none is page 0 with a scale that is none
-    const int id = __builtin_amdgcn_readfirstlane(t < t_end ? q.table[t * kTile >> pshift] : 0);
+  auto page_at = [&](int t) { return t < t_end ? q.table[t * kTile >> pshift] : 0; };
+  int next = page_at(t_begin);  // the page of the tile that is loaded next, read a tile ahead
+  auto load = [&](int t) {      // tile t's codes and scales; a page that is none is page 0 with a scale that is none
+    const int id = __builtin_amdgcn_readfirstlane(next);
+    next = page_at(t + 1);
     const bool good = (unsigned)id < (unsigned)c.n_pages;
     const int page = good ? id : 0, sub = (t * kTile) & ((1 << pshift) - 1);
     const int64_t ph = (int64_t)page * c.Hkv + h;
@@ -421,7 +429,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
       vr[n] = *reinterpret_cast<const u32x4*>(vp + ((ch >> 2) << pshift) + 16 * (ch & 3));
     }
   };
-  auto kkey = [](int tok) { return (tok & 3) | ((tok >> 4) & 1) << 2; };
+  // sixteen lanes of a fragment read hit sixteen chunks of a 256-byte line: its
+  // tokens differ in bits 0, 1, 2 and 4, its channels in bits 0..3
+  auto kslot = [](int tok, int chunk) {
+    const int up = ((tok >> 4) & 1) | ((tok >> 2) & 1) << 1;
+    return tok * D + 8 * (chunk ^ (D == 64 ? ((tok >> 1) & 1) | up << 1 : (tok & 3) | up << 2));
+  };
+  auto vslot = [](int d, int chunk) { return d * kTile + 8 * (chunk ^ ((d >> 1) & 7)); };
   auto stage = [&](int buf) {
 #pragma unroll
     for (int n = 0; n < L; ++n) {
@@ -435,7 +449,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
         w[m >> 1][2 * (m & 1) + 1] = f.y;
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_k[buf][tok * D + 8 * ((kc + m) ^ kkey(tok))]) = w[m];
+      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_k[buf][kslot(tok, kc + m)]) = w[m];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const uint2 f = codes_f16(vr[n][m]);
@@ -443,7 +457,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
         w[m >> 1][2 * (m & 1) + 1] = f.y;
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_v[buf][d * kTile + 8 * ((vc + m) ^ (d & 7))]) = w[m];
+      for (int m = 0; m < 2; ++m) *reinterpret_cast<u32x4*>(&s_v[buf][vslot(d, vc + m)]) = w[m];
     }
   };
   if (t_begin < t_end) load(t_begin);
@@ -488,7 +502,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   for (int n = 0; n < DT; ++n)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[n][i] = 0.0f;
-  float R = 0.0f;  // the largest value scale so far; acc is in steps of R / 2^14
+  int ex_r = 1;  // acc is in steps of R / 2^14, R = 2^(ex_r - 127)
 
   Scales sc{};
   if (t_begin < t_end) {
@@ -508,13 +522,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
         for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][tok * D + 8 * ((2 * k + hh) ^ kkey(tok))]);
+          const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][kslot(tok, 2 * k + hh)]);
 #pragma unroll
           for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
         }
       }
       const int base = t * kTile, first = base + 16 * hh;
       if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
+        keep_branch();
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -533,8 +548,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
       const float m1 = fmaxf(m, raw), ref = m1 > -INFINITY ? m1 : 0.0f;
       const float alpha = __builtin_amdgcn_exp2f(m - ref);
       m = m1;
-      const float R1 = fmaxf(R, sc.vs), down = R1 > 0.0f ? R / R1 : 1.0f, w = R1 > 0.0f ? sc.vs / R1 * 16384.0f : 0.0f;
-      R = R1;
+      // R is a power of two, so both factors are exact
+      const int e1 = max(ex_r, (int)(__float_as_uint(sc.vs) >> 23));
+      const float down = __uint_as_float((uint32_t)max(127 + ex_r - e1, 0) << 23);
+      const float w = sc.vs * __uint_as_float((uint32_t)(254 - e1) << 23) * 16384.0f;
+      ex_r = e1;
       f16x8 pf[NS][4];
       float sum = 0.0f;
 #pragma unroll
@@ -550,6 +568,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
       l = fmaf(l, alpha, sum);
       const float scale = alpha * down;
       if (__builtin_amdgcn_ballot_w64(scale != 1.0f)) {
+        keep_branch();
 #pragma unroll
         for (int n = 0; n < DT; ++n)
 #pragma unroll
@@ -561,7 +580,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // block k / 2, step k % 2: tokens 32 (k / 2) + 16 hh + 8 (k % 2) ..
-          const f16x8 vf = *reinterpret_cast<const f16x8*>(&s_v[buf][d * kTile + 8 * ((4 * (k >> 1) + 2 * hh + (k & 1)) ^ (d & 7))]);
+          const f16x8 vf = *reinterpret_cast<const f16x8*>(&s_v[buf][vslot(d, 4 * (k >> 1) + 2 * hh + (k & 1))]);
 #pragma unroll
           for (int e = 0; e < NS; ++e) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[e][k], acc[n], 0, 0, 0);
         }
@@ -577,7 +596,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   l += xor_lanes<32>(l);
   if (c0 + col >= cols) return;
   const int64_t orow = (int64_t)q.row0 + qt;
-  const float unit = R * (1.0f / 16384.0f);
+  const float unit = __uint_as_float((uint32_t)ex_r << 23) * (1.0f / 16384.0f);
   if (active == 1) {
     const float inv = l == 0.0f ? 0.0f : unit / l;
 #pragma unroll

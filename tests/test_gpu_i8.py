@@ -85,9 +85,9 @@ def _product(x, w, ws, b, out):
 
 
 # the last token counts of a launch shape and the first of the next, and widths around a tile's
-SHAPES = [(1, 1, 256), (1, 256, 2048), (2, 17, 512), (15, 33, 1024), (16, 64, 1280), (17, 31, 256), (32, 100, 4352),
+SHAPES = [(1, 1, 256), (1, 256, 2048), (2, 17, 512), (3, 40, 16384), (4, 20, 16384), (4, 100, 6144), (5, 50, 16384), (15, 33, 1024), (16, 64, 1280), (17, 31, 256), (32, 100, 4352),
           (33, 48, 768), (64, 130, 2048), (65, 64, 512), (100, 200, 768), (127, 65, 256), (128, 1500, 256),
-          (129, 129, 1024), (300, 1000, 512), (1000, 1111, 256), (2100, 2049, 256)]
+          (129, 129, 1024), (300, 1000, 512), (70, 64, 4096), (500, 100, 2048), (1000, 1111, 256), (2100, 2049, 256)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)
@@ -162,7 +162,7 @@ def test_no_tokens_and_refused_tensors():
     with pytest.raises(ValueError):
         md.i8_linear(W, x.cpu())
     with pytest.raises(md.MDError) as e:
-        md.i8_linear(W, x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        md.i8_linear(W, torch.zeros(9, 256, device="cuda"), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.name == "MD_ERR_WORKSPACE"
 
 
