@@ -8,23 +8,55 @@ namespace md {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// rint(x / s) for finite x and s > 0 with |x / s| < 256, ties to even, clamped
-// to -127..127, exactly: a product with 1 / s gives the integer or its
-// neighbour, and the sign of the fused x - (n +- 1/2) s (one rounding, so never
-// wrong) says on which side of the two borders x lies.  s is at least 2^-100
-// here (tiny magnitudes are scaled up first), so nothing underflows.
-MD_DEV int code_of(float x, float s, float inv) {
-  float n = rintf(x * inv);
-  const float hi = fmaf(-(n + 0.5f), s, x), lo = fmaf(-(n - 0.5f), s, x);
-  const bool odd = ((int)n) & 1;
-  if (hi > 0.0f || (hi == 0.0f && odd)) n += 1.0f;
-  else if (lo < 0.0f || (lo == 0.0f && odd)) n -= 1.0f;
-  return (int)fminf(fmaxf(n, -127.0f), 127.0f);
-}
-
 // Values whose largest magnitude is below 2^-60 are scaled by 2^80 before
 // their codes are formed (their step may be subnormal).
 constexpr float kTiny = 0x1p-60f, kTinyUp = 0x1p80f;
+
+// A scale s as what turns values of magnitudes up to amax into codes.  s that
+// is zero or NaN gives codes 0.
+struct Step {
+  float up, s, inv;
+  bool none;
+};
+MD_DEV Step step_of(float s, float amax) {
+  Step o;
+  o.up = amax < kTiny && s < 1.0f ? kTinyUp : 1.0f;
+  o.none = !(s > 0.0f);
+  o.s = o.none ? 1.0f : s * o.up;
+  o.inv = 1.0f / o.s;
+  return o;
+}
+
+// x / s to the nearest integer, ties to even, clamped to -127..127, for eight
+// finite x with |x / s| < 256, exactly: x (1 / s) is within 2^-15 of the
+// quotient, so its integer is the one sought unless it lies next to a border
+// k + 1/2.  There (one value in 5000) the sign of the fused x - (n +- 1/2) s,
+// one rounding and so never wrong, says on which side of the borders x lies.
+// s is at least 2^-100 here, so nothing underflows.
+MD_DEV uint2 codes8(const float (&v)[8], const Step& s) {
+  uint32_t w[2] = {0, 0};
+  if (s.none) return make_uint2(0, 0);
+  float n[8], far = 0.0f;
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const float r = v[m] * s.up * s.inv;
+    n[m] = rintf(r);
+    far = fmaxf(far, fabsf(r - n[m]));
+  }
+  if (far > 0.4999f) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float x = v[m] * s.up, hi = fmaf(-(n[m] + 0.5f), s.s, x), lo = fmaf(-(n[m] - 0.5f), s.s, x);
+      const bool odd = ((int)n[m]) & 1;
+      if (hi > 0.0f || (hi == 0.0f && odd)) n[m] += 1.0f;
+      else if (lo < 0.0f || (lo == 0.0f && odd)) n[m] -= 1.0f;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+    w[m >> 2] |= (uint32_t)((int)fminf(fmaxf(n[m], -127.0f), 127.0f) & 255) << (8 * (m & 3));
+  return make_uint2(w[0], w[1]);
+}
 
 template <int XT>
 MD_DEV void load8(const void* x, int64_t i, float (&v)[8]) {

@@ -24,29 +24,13 @@ namespace md {
 // or a NaN gets the scale NaN and codes 0, so its products are NaN and no other
 // row's are.
 struct RowScale {
-  float s, up, ss, inv;
-  bool none;
+  float s;
+  Step step;
 };
 MD_DEV RowScale row_scale_of(uint32_t top) {
-  RowScale o;
-  const float amax = __uint_as_float(top);
-  const bool bad = top >= 0x7F800000u;
-  o.s = bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
-  o.up = amax < kTiny ? kTinyUp : 1.0f;
-  o.none = bad || !(o.s > 0.0f);
-  o.ss = o.none ? 1.0f : o.s * o.up;
-  o.inv = 1.0f / o.ss;
-  return o;
+  const float amax = __uint_as_float(top), s = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
+  return RowScale{s, step_of(s, amax)};
 }
-MD_DEV uint2 codes8(const float (&v)[8], const RowScale& s) {
-  uint32_t w[2] = {0, 0};
-  if (!s.none) {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) w[m >> 2] |= (uint32_t)(code_of(v[m] * s.up, s.ss, s.inv) & 255) << (8 * (m & 3));
-  }
-  return make_uint2(w[0], w[1]);
-}
-
 // One row per group of WPR waves (WPR 1: four rows a workgroup), the whole row
 // in registers between the maximum and the codes: x is read once.  Bound by
 // the read of x.
@@ -87,7 +71,7 @@ __global__ __launch_bounds__(256) void k_i8_quantize(const void* __restrict__ x,
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     const int c = at + i * kStep;
-    if (c < K) *reinterpret_cast<uint2*>(codes + base + c) = codes8(v[i], s);
+    if (c < K) *reinterpret_cast<uint2*>(codes + base + c) = codes8(v[i], s.step);
   }
 }
 
@@ -196,7 +180,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
       for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
         float v[8];
         load8<XT>(x, (int64_t)t * K + c, v);
-        *reinterpret_cast<uint2*>(codes + t * K + c) = codes8(v, s);
+        *reinterpret_cast<uint2*>(codes + t * K + c) = codes8(v, s.step);
       }
     }
     __syncthreads();

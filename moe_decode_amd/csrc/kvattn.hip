@@ -72,8 +72,9 @@ MD_DEV float join(const i32x4 (&a)[ND], int r) {
   else return fmaf((float)a[2][r], 65536.0f, (float)low);
 }
 
+template <int AUX>
 MD_DEV i32x4 load16(rsrc_t r, int off, int soff) {
-  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
+  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, AUX);
   return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 
@@ -211,7 +212,7 @@ MD_DEV float weights(const float* x, float f, float ref, float scale, i32x4 (&pd
 // while the next one's scores are.
 template <int D, int ND>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAttn a) {
-  constexpr int KS = D / 64, DT = D / 16;
+  constexpr int DT = D / 16;
   __shared__ __attribute__((aligned(16))) float s_acc[kWaves][16][D + 4];
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
   const KvCache& c = a.c;
@@ -227,18 +228,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
   if (split >= active) return;
   const int t_begin = sp.t0 + split * per, t_end = min(t_begin + per, sp.t1);
 
-  Column<D, ND> o;
-  column_init<D, ND>(o, a, q, h, ct * 16 + col, cols, g);
-  float acc[DT][4];
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][r] = 0.0f;
-
   const int pshift = a.pshift;
-  const int koff = (16 * (col >> 2) + (col & 3)) * D + 16 * g;  // this lane's A row of key tile 0
+  // Rows of 128 bytes and more are loaded eight lanes a row, a whole line each:
+  // lane (m, g) of load (i, k) takes token 16 (m / 4) + 2 i + (m / 2) % 2,
+  // chunk 8 k + 4 (m % 2) + g.  As an A operand its even rows hold a token's
+  // first 64 channels and its odd rows the next 64, so it is multiplied by both
+  // halves of the query and every result uses every other row of each product
+  // (the matrix cores have room; half-line loads cost 13% of the read rate).
+  constexpr bool kWide = D > 64;
+  constexpr int KI = kWide ? 8 : 4, KK = kWide ? D / 128 : 1;
+  const int koff = kWide ? (16 * (col >> 2) + ((col >> 1) & 1)) * D + 64 * (col & 1) + 16 * g
+                         : (16 * (col >> 2) + (col & 3)) * D + 16 * g;
   const int voff = (col << pshift) + 16 * g;
-  i32x4 kf[4][KS], vf[DT];
+  i32x4 kf[KI][KK], vf[DT];
   // a page that is none reads page 0 and counts as one with scale NaN
   auto page_at = [&](int t) { return t < t_end ? q.table[t * kTile >> pshift] : 0; };
   // buffer loads: past the last tile the resources are empty, and the same
@@ -247,24 +249,32 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     const int sub = (t * kTile) & ((1 << pshift) - 1);
     const rsrc_t r = make_res(c.k + ((((int64_t)page * c.Hkv + h) << pshift) + sub) * D, t < t_end ? kTile * D : 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < KI; ++i)
 #pragma unroll
-      for (int k = 0; k < KS; ++k) kf[j][k] = load16(r, koff + 4 * j * D + 64 * k, 0);
+      for (int k = 0; k < KK; ++k) kf[i][k] = load16<kAuxStream>(r, koff + (kWide ? 2 : 4) * i * D + 128 * k, 0);
   };
   auto load_v = [&](int t, int page) {
     const int sub = (t * kTile) & ((1 << pshift) - 1);
     const rsrc_t r = make_res(c.v + (((int64_t)page * c.Hkv + h) << pshift) * D + sub, t < t_end ? (D << pshift) - sub : 0);
 #pragma unroll
-    for (int i = 0; i < DT; ++i) vf[i] = load16(r, voff, (16 * i) << pshift);
+    for (int i = 0; i < DT; ++i) vf[i] = load16<0>(r, voff, (16 * i) << pshift);
   };
+  // the first tile is on its way while the queries are rounded
   int t = t_begin + wave;
+  int id = __builtin_amdgcn_readfirstlane(page_at(t)), next = page_at(t + kWaves);
+  bool good = (unsigned)id < (unsigned)c.n_pages;
+  int page = good ? id : 0;
+  load_k(t, page);
+  load_v(t, page);
+  float ks = c.k_scale[(int64_t)page * c.Hkv + h], vs = c.v_scale[(int64_t)page * c.Hkv + h];
+  Column<D, ND> o;
+  column_init<D, ND>(o, a, q, h, ct * 16 + col, cols, g);
+  float acc[DT][4];
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[i][r] = 0.0f;
   if (t < t_end) {
-    int id = __builtin_amdgcn_readfirstlane(page_at(t)), next = page_at(t + kWaves);
-    bool good = (unsigned)id < (unsigned)c.n_pages;
-    int page = good ? id : 0;
-    load_k(t, page);
-    load_v(t, page);
-    float ks = c.k_scale[(int64_t)page * c.Hkv + h], vs = c.v_scale[(int64_t)page * c.Hkv + h];
     for (; t < t_end; t += kWaves) {
       const Scales sc = scales_of(good ? ks : -1.0f, vs);
       id = __builtin_amdgcn_readfirstlane(next);
@@ -273,17 +283,28 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
       next = page_at(t + 2 * kWaves);
       float x[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int i = 0; i < KI; ++i) {
         i32x4 d[ND];
+        if constexpr (kWide) {
 #pragma unroll
-        for (int e = 0; e < ND; ++e) {
-          d[e] = i32x4{0, 0, 0, 0};
+          for (int e = 0; e < ND; ++e) {
+            i32x4 d0{0, 0, 0, 0}, d1{0, 0, 0, 0};
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][k], o.qd[e][k], d[e], 0, 0, 0);
+            for (int k = 0; k < KK; ++k) {
+              d0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[i][k], o.qd[e][2 * k], d0, 0, 0, 0);
+              d1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[i][k], o.qd[e][2 * k + 1], d1, 0, 0, 0);
+            }
+            d[e] = i32x4{d0[0] + d1[1], d0[2] + d1[3], 0, 0};
+          }
+          x[2 * i] = join<ND>(d, 0);
+          x[2 * i + 1] = join<ND>(d, 1);
+        } else {
+#pragma unroll
+          for (int e = 0; e < ND; ++e)
+            d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[i][0], o.qd[e][0], i32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[4 * i + r] = join<ND>(d, r);
         }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[4 * j + r] = join<ND>(d, r);
         __builtin_amdgcn_sched_barrier(0);
       }
       load_k(t + kWaves, page);

@@ -70,6 +70,8 @@ APPENDS = [  # heads, dim, page, (new, length) of each sequence
     (3, 64, 128, [(130, 200), (128, 256), (1, 129), (129, 129)]),
     (2, 256, 64, [(65, 128), (2, 130), (64, 127)]),
     (1, 128, 256, [(257, 300), (256, 256), (1, 512), (17, 33)]),
+    (2, 64, 64, [(1, 2), (1, 6), (1, 7), (1, 8), (2, 70), (1, 64)]),      # every place in a word, held tokens before it
+    (1, 256, 256, [(3, 35), (8, 30), (1, 131)]),
 ]
 
 
