@@ -223,11 +223,13 @@ struct KvAttn {
   float scale;
   int tile;                   // columns (query, head) of a workgroup
   int snake;                  // all workgroups run at once, two on a compute unit
-  int splits, chunk;          // a split covers chunk tiles of 64 positions
-  float *part, *part_m;       // [rows][Hq][splits][D], [rows][Hq][splits][2]
+  int splits, chunk;          // many columns: a split covers chunk tiles of 64 positions
+  int pieces;                 // few columns: workgroups that all tiles are dealt out to, or 0
+  float *part, *part_m;       // [rows][Hq][splits][D], [rows][Hq][splits][2]; [2 pieces][16][D], [2 pieces][16][2]
+  int4* shares;               // [pieces]: of the segment that begins there, how many shares, which one, first slot
 };
 struct KvPlan {
-  int tile, splits, chunk;
+  int tile, splits, chunk, pieces;
 };
 constexpr int kPairsPerLaunch = 448;  // page pairs that fit a launch's 4 KB of arguments
 struct PagePairs {

@@ -116,6 +116,13 @@ md::KvBatch dev(const md_kv_batch* b) {
   return md::KvBatch{b->n_seqs, b->rows, b->max_q, b->max_kv, b->table_stride, b->q_start, b->kv_len, b->table};
 }
 
+// Partial sums (one per row or column each) that the attention's workspace
+// holds, after its notes on them: maxima and totals, then vectors.
+size_t attn_slots(const md::KvPlan& p, const md_kv_batch* b, int32_t q_heads) {
+  if (p.pieces) return (size_t)2 * p.pieces * 16;
+  return p.splits > 1 ? (size_t)b->rows * q_heads * p.splits : 0;
+}
+
 // The attention's checks up to its pointers, and its launch geometry.
 md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal, int32_t window,
                     md::KvPlan* plan, size_t* bytes) {
@@ -131,8 +138,10 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
   *plan = md::kv_attn_plan(dev(c), dev(b), G, window, causal);
   const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
   if (groups > INT32_MAX) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
-  const size_t slots = plan->splits > 1 ? (size_t)b->rows * q_heads * plan->splits : 0;
-  *bytes = slots ? align256(slots * 2 * sizeof(float)) + align256(slots * c->head_dim * sizeof(float)) : 0;
+  const size_t slots = attn_slots(*plan, b, q_heads);
+  *bytes = slots ? align256(plan->pieces * sizeof(int4)) + align256(slots * 2 * sizeof(float)) +
+                       align256(slots * c->head_dim * sizeof(float))
+                 : 0;
   return MD_OK;
 }
 
@@ -348,10 +357,14 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
   a.tile = plan.tile;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
+  a.pieces = plan.pieces;
   if (need) {
-    const size_t slots = (size_t)b->rows * q_heads * plan.splits;
-    a.part_m = static_cast<float*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(slots * 2 * sizeof(float)));
+    char* at = static_cast<char*>(workspace);
+    a.shares = reinterpret_cast<int4*>(at);
+    at += align256(plan.pieces * sizeof(int4));
+    a.part_m = reinterpret_cast<float*>(at);
+    at += align256(attn_slots(plan, b, q_heads) * 2 * sizeof(float));
+    a.part = reinterpret_cast<float*>(at);
   }
   const hipError_t e = md::launch_kv_attn(a, c->head_dim, ytype, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "attention launch");

@@ -205,29 +205,53 @@ MD_DEV float weights(const float* x, float f, float ref, float scale, i32x4 (&pd
   return sum;
 }
 
-// Few columns (decode): a workgroup's four waves take turns at the tiles of one
-// column tile of 16 and meet in LDS.  Bound by the read of the cache: keys and
-// values go from HBM straight into the matrix cores' operand registers, the
-// next tile's keys while this one's weights are formed and summed, its values
-// while the next one's scores are.
+// Few columns (decode): four waves take turns at the tiles of one column tile
+// of 16 and meet in LDS.  Bound by the read of the cache: keys and values go
+// from HBM straight into the matrix cores' operand registers, the next tile's
+// keys while this one's weights are formed and summed, its values while the
+// next one's scores are.
+//
+// A segment is the tiles of one sequence, key head and column tile.  Where
+// segments are long (a.pieces > 0) the tiles of all of them, in order, are dealt
+// out in equal runs to as many workgroups as run at once: a ragged batch
+// leaves nobody waiting, whatever its lengths, which only the device knows.  A
+// segment that one workgroup covers is written out, of the others each
+// workgroup keeps at most its first and its last one's share in the workspace,
+// and the one where a segment begins notes how many shares there are for
+// k_kv_join_pieces.  Measured, with the join: 32 sequences of up to 8190 tokens,
+// 64 heads on 8 of 128 channels, 67 us (289 MB, 4.3 TB/s; fixed shares of max_kv
+// 76), two of up to 131071 on pages of 128 tokens 83 us (402 MB, 4.9 TB/s; 85).
+// A copy that only loads took 5% less than the kernel: it waits for memory.
+// Half, one and a half times and twice as many workgroups: 75, 77, 73 and 81,
+// 94, 89 us.
+constexpr int kMaxDealt = 1024;  // sequences, at most, that a workgroup sums up
+
+// The tiles that any column of a sequence sees, one at least where it has rows:
+// somebody has to write their zeros.
+MD_DEV int tiles_of(const KvAttn& a, const Seq& q, int cols, int& t0) {
+  const Span s = span_of(a, q, 0, cols);
+  t0 = s.t0;
+  return max(s.t1 - s.t0, 1);
+}
+
 template <int D, int ND>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAttn a) {
+struct FewLds {
+  float acc[kWaves][16][D + 4];
+  float m[kWaves][16], l[kWaves][16];
+};
+
+// Tiles [t_begin, t_end) of head h's column tile ct.  slot < 0: they are all
+// that it sees, and the outputs are written; else the sums go to that slot.
+template <int D, int ND>
+MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, const Span& sp, int t_begin, int t_end,
+                        int slot, FewLds<D, ND>& lds) {
   constexpr int DT = D / 16;
-  __shared__ __attribute__((aligned(16))) float s_acc[kWaves][16][D + 4];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+  auto& s_acc = lds.acc;
+  auto& s_m = lds.m;
+  auto& s_l = lds.l;
   const KvCache& c = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
-  const int h = rest % c.Hkv, ct = rest / c.Hkv, s = blockIdx.y;
-  const Seq q = seq_of(a.b, s, c.page);
-  const int cols = q.nq * a.G;
-  if (ct * 16 >= cols) return;
-  const Span sp = span_of(a, q, ct * 16, min(ct * 16 + 16, cols));
-  const int per = a.chunk, active = max(1, (sp.t1 - sp.t0 + per - 1) / per);
-  if (split >= active) return;
-  const int t_begin = sp.t0 + split * per, t_end = min(t_begin + per, sp.t1);
-
   const int pshift = a.pshift;
   // Rows of 128 bytes and more are loaded eight lanes a row, a whole line each:
   // lane (m, g) of load (i, k) takes token 16 (m / 4) + 2 i + (m / 2) % 2,
@@ -356,9 +380,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     ll = fmaf(w[i], s_l[i][oc], ll);  // 0 * NaN stays NaN
   }
   const int64_t orow = (int64_t)q.row0 + ot;
-  const bool direct = active == 1;
-  const float inv = direct ? (ll == 0.0f ? 0.0f : 1.0f / ll) : 1.0f;
-  const int64_t slot = (orow * (a.G * c.Hkv) + oh) * a.splits + split;
+  const float inv = slot < 0 ? (ll == 0.0f ? 0.0f : 1.0f / ll) : 1.0f;
+  const int64_t at = (int64_t)slot * 16 + oc;
 #pragma unroll
   for (int i = 0; i < DT / 4; ++i) {
     const int d = 4 * part + 64 * i;
@@ -367,12 +390,97 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     for (int k = 0; k < kWaves; ++k)
 #pragma unroll
       for (int r = 0; r < 4; ++r) y[r] = fmaf(w[k], s_acc[k][oc][d + r], y[r]);
-    if (direct) store_out4(a, orow, oh, D, d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    else *reinterpret_cast<float4*>(a.part + slot * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+    if (slot < 0) store_out4(a, orow, oh, D, d, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    else *reinterpret_cast<float4*>(a.part + at * D + d) = make_float4(y[0], y[1], y[2], y[3]);
   }
-  if (!direct && part == 0) {
-    a.part_m[2 * slot] = mm;
-    a.part_m[2 * slot + 1] = ll;
+  if (slot >= 0 && part == 0) reinterpret_cast<float2*>(a.part_m)[at] = make_float2(mm, ll);
+}
+
+template <int D, int ND>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAttn a) {
+  __shared__ __attribute__((aligned(16))) FewLds<D, ND> lds;
+  __shared__ int64_t first[kMaxDealt + 1], waves[kWaves];
+  const int Hkv = a.c.Hkv;
+  const int tid = threadIdx.x;
+  int s = blockIdx.y, plain_seg = blockIdx.x;  // without a deal: one segment a workgroup
+  int64_t u = 0, end = 1, total = 0, runs = 0;
+  if (a.pieces) {
+    // tiles before each sequence (rolled: code that runs once is fetched cold)
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < kMaxDealt / 256; ++i) {
+      const int e = tid * (kMaxDealt / 256) + i;
+      int64_t n = 0;
+      if (e < a.b.S) {
+        const Seq q = seq_of(a.b, e, a.c.page);
+        int t0;
+        if (q.nq) n = (int64_t)((q.nq * a.G + 15) / 16) * Hkv * tiles_of(a, q, q.nq * a.G, t0);
+      }
+      first[e] = sum;
+      sum += n;
+    }
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t v = __shfl_up(upto, o, 64);
+      if ((tid & 63) >= o) upto += v;
+    }
+    if ((tid & 63) == 63) waves[tid >> 6] = upto;
+    __syncthreads();
+    int64_t before = upto - sum;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < tid >> 6) before += waves[w];
+      total += waves[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxDealt / 256; ++i) first[tid * (kMaxDealt / 256) + i] += before;
+    if (tid == 0) first[kMaxDealt] = total;
+    __syncthreads();
+    // runs of four tiles at least: one a wave
+    runs = max(min((int64_t)a.pieces, total / kWaves), (int64_t)(total > 0));
+    if (tid == 0) a.shares[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (blockIdx.x >= runs) return;
+    u = blockIdx.x * total / runs;
+    end = (blockIdx.x + 1) * total / runs;
+    int lo = 0, hi = kMaxDealt;  // the sequence of tile u: first[lo] <= u < first[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    s = lo;
+  }
+  for (bool again = false; u < end; again = true) {
+    s = __builtin_amdgcn_readfirstlane(s);
+    const Seq q = seq_of(a.b, s, a.c.page);
+    const int cols = q.nq * a.G, cts = (cols + 15) / 16;
+    int t0, seg = plain_seg, from = 0;
+    const int n = cols ? tiles_of(a, q, cols, t0) : 0;
+    int to = n;
+    if (a.pieces) {
+      const int64_t in = u - first[s];
+      seg = __builtin_amdgcn_readfirstlane((int)(in / n));
+      from = __builtin_amdgcn_readfirstlane((int)(in - (int64_t)seg * n));
+      to = __builtin_amdgcn_readfirstlane((int)min((int64_t)n, from + (end - u)));
+    } else if (seg >= cts * Hkv) {
+      return;
+    }
+    const int h = __builtin_amdgcn_readfirstlane(seg / cts), ct = seg - h * cts;
+    const Span sp = span_of(a, q, ct * 16, min(ct * 16 + 16, cols));
+    // the first one's share of a workgroup goes to its slot 0, the last one's to 1
+    const int slot = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (again ? 1 : 0);
+    if (again) __syncthreads();  // the LDS of the one before
+    // (said to be the same in all lanes, or every load would ask each of them)
+    few_columns<D, ND>(a, q, h, ct, cols, sp, __builtin_amdgcn_readfirstlane(max(t0 + from, sp.t0)),
+                       __builtin_amdgcn_readfirstlane(min(t0 + to, sp.t1)), slot, lds);
+    if (!a.pieces) return;
+    if (from == 0 && to < n && tid == 0) {
+      const int64_t last = ((first[s] + (int64_t)(seg + 1) * n) * runs - 1) / total;  // the run with its last tile
+      a.shares[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, s, seg, slot);
+    }
+    u += to - from;
+    while (u < end && u >= first[s + 1]) ++s;  // u < end <= total: there is one that holds it
   }
 }
 
@@ -686,20 +794,70 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttn a) {
   store_out4(a, row, head, D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
+// The shares of a segment that several workgroups had: one workgroup for each
+// workgroup where one may begin and each of its columns.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join_pieces(KvAttn a) {
+  constexpr int L = D / 4, P = 256 / L;
+  __shared__ float s_l[P];
+  __shared__ __attribute__((aligned(16))) float s_o[P][D];
+  const int4 sh = a.shares[blockIdx.x];  // count, sequence, segment, first slot
+  if (sh.x <= 1) return;
+  const Seq q = seq_of(a.b, sh.y, a.c.page);
+  const int cols = q.nq * a.G, cts = (cols + 15) / 16, h = sh.z / cts, c = (sh.z - h * cts) * 16 + (int)blockIdx.y;
+  if (c >= cols) return;
+  const int part = threadIdx.x / L, d = 4 * ((int)threadIdx.x % L);
+  auto at = [&](int i) { return (int64_t)(i ? 2 * ((int)blockIdx.x + i) : sh.w) * 16 + blockIdx.y; };
+  const float2* ml = reinterpret_cast<const float2*>(a.part_m);
+  float m = -INFINITY;
+  for (int i = threadIdx.x & 63; i < sh.x; i += 64) m = fmaxf(m, ml[at(i)].x);
+  m = group_max<64>(m);
+  const float ref = m > -INFINITY ? m : 0.0f;
+  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = part; i < sh.x; i += P) {
+    const float2 x = ml[at(i)];
+    const float w = __builtin_amdgcn_exp2f(x.x - ref);
+    const float4 p = *reinterpret_cast<const float4*>(a.part + at(i) * D + d);
+    l = fmaf(w, x.y, l);
+    o[0] = fmaf(w, p.x, o[0]);
+    o[1] = fmaf(w, p.y, o[1]);
+    o[2] = fmaf(w, p.z, o[2]);
+    o[3] = fmaf(w, p.w, o[3]);
+  }
+  *reinterpret_cast<float4*>(&s_o[part][d]) = make_float4(o[0], o[1], o[2], o[3]);
+  if (d == 0) s_l[part] = l;
+  __syncthreads();
+  if (part) return;
+  for (int i = 1; i < P; ++i) {
+    l += s_l[i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += s_o[i][d + r];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int qt = c / a.G;
+  store_out4(a, (int64_t)q.row0 + qt, h * a.G + (c - qt * a.G), D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+}
+
 KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal) {
-  // enough workgroups to fill the chip several times over, of at least one
-  // tile a wave; a split is a fixed number of tiles, so that in a ragged batch
-  // every workgroup has the same work
   int64_t most = b.max_kv;
   if (causal && window && (int64_t)window + b.max_q < most) most = (int64_t)window + b.max_q;
   const int64_t tiles = (most + kTile - 1) / kTile + 1;
-  KvPlan p;
+  KvPlan p{};
   p.tile = (int64_t)b.max_q * G > 64 ? kRowCols : 16;
+  p.splits = 1;
+  p.chunk = (int)tiles;
+  if (p.tile == 16) {
+    // as many workgroups as run at once (registers: one, two or four on a
+    // compute unit); segments of up to two tiles a wave are not worth a second
+    // kernel
+    if (tiles > 2 * kWaves && b.S <= kMaxDealt) p.pieces = device_cus() * (c.D == 64 ? 4 : c.D == 128 ? 2 : 1);
+    return p;
+  }
+  // enough workgroups to fill the chip, a split a fixed number of tiles
   const int64_t base = (int64_t)b.S * c.Hkv * (((int64_t)b.max_q * G + p.tile - 1) / p.tile);
-  const int64_t want = p.tile == 16 ? 1024 : 512;
-  int64_t chunk = (tiles * base + want - 1) / want;
-  if (chunk < kWaves) chunk = kWaves;
-  chunk += chunk & 1;  // whole steps
+  int64_t chunk = (tiles * base + 511) / 512;
+  if (chunk < 4) chunk = 4;
   p.chunk = (int)(chunk < tiles ? chunk : tiles);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
   return p;
@@ -708,7 +866,7 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int c
 hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
   KvAttn a = a0;
   const int64_t cts = ((int64_t)a.b.max_q * a.G + a.tile - 1) / a.tile;
-  const dim3 grid((unsigned)(a.splits * cts * a.c.Hkv), a.b.S), block(64 * kWaves);
+  const dim3 grid = a.pieces ? dim3(a.pieces) : dim3((unsigned)(a.splits * cts * a.c.Hkv), a.b.S), block(64 * kWaves);
   const int64_t groups = (int64_t)grid.x * grid.y;
   a.snake = groups > device_cus() && groups <= 2 * device_cus();
 #define MD_ATT(D_, N_)                                                                     \
@@ -727,11 +885,16 @@ hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
   }
 #undef MD_ATT
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const dim3 jgrid(a.b.max_q, a.G * a.c.Hkv, a.b.S);
-  if (D == 64) hipLaunchKernelGGL((k_kv_join<64>), jgrid, dim3(256), 0, st, a);
-  else if (D == 128) hipLaunchKernelGGL((k_kv_join<128>), jgrid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((k_kv_join<256>), jgrid, dim3(256), 0, st, a);
+  if (e != hipSuccess || (a.splits == 1 && !a.pieces)) return e;
+#define MD_JOIN(D_)                                                                                                   \
+  do {                                                                                                                \
+    if (a.pieces) hipLaunchKernelGGL((k_kv_join_pieces<D_>), dim3(a.pieces, 16), dim3(256), 0, st, a);                \
+    else hipLaunchKernelGGL((k_kv_join<D_>), dim3(a.b.max_q, a.G * a.c.Hkv, a.b.S), dim3(256), 0, st, a);             \
+  } while (0)
+  if (D == 64) MD_JOIN(64);
+  else if (D == 128) MD_JOIN(128);
+  else MD_JOIN(256);
+#undef MD_JOIN
   return hipGetLastError();
 }
 

@@ -253,6 +253,42 @@ def test_attention(case, xt, out):
     assert bool((y[rows] == 5.0).all())     # the row behind the last sequence
 
 
+@pytest.mark.parametrize("S,Hkv,G,D,page,window,out", [
+    (700, 1, 2, 64, 64, 0, "f32"), (1024, 1, 1, 64, 64, 0, "bf16"), (1025, 1, 1, 64, 64, 0, "f32"),
+    (37, 2, 8, 128, 64, 0, "f32"), (37, 2, 8, 128, 128, 90, "bf16"), (5, 1, 3, 256, 256, 0, "f32"),
+    (3, 4, 5, 64, 64, 700, "f32")])
+def test_ragged_batches_dealt_out(S, Hkv, G, D, page, window, out):
+    """Sequences of 0 to 1500 positions with 0 to 3 new rows each, some without
+    rows, some that see nothing: every row against the definition; the same call
+    again gives the same bits."""
+    import moe_decode_amd as md
+    import torch
+    rng = np.random.default_rng(S + D)
+    nq = rng.integers(0, 4, S)
+    lens = np.where(rng.random(S) < 0.7, rng.integers(0, 40, S), rng.integers(0, 1500, S))
+    nq[-1], lens[-1], nq[0] = 0, 1500, 3
+    nq, lens = nq.tolist(), lens.tolist()
+    table, n = _tables(lens, page, rng)
+    m = Cache(n, Hkv, page, D, rng)
+    c = _to_gpu(m)
+    q, qn = _rn(rng, (sum(nq) + 1, Hkv * G, D), "f32")
+    b = _batch(nq, lens, table, max_q=3)
+    y = torch.full((sum(nq) + 1, Hkv * G, D), 5.0, dtype=_dt(out), device="cuda")
+    md.kv_attention(c, b, q, window=window, out=y)
+    got, at = y.double().cpu().numpy(), 0
+    for i, (a, L) in enumerate(zip(nq, lens)):
+        if a:
+            want, tol = attention(qn[at:at + a], m.values("k", table[i], L), m.values("v", table[i], L), D ** -0.5,
+                                  True, window, out)
+            assert (np.abs(got[at:at + a] - want) <= tol).all(), (i, a, L)
+        at += a
+    assert bool((y[-1] == 5.0).all())
+    for _ in range(3):
+        z = torch.full_like(y, 5.0)
+        md.kv_attention(c, b, q, window=window, out=z)
+        assert torch.equal(z, y)
+
+
 def test_long_context_split_over_workgroups():
     """131072 + 3 positions (offsets of a page past 2^31 bytes are not reached
     here, but every split is), against the sum in 64 bits on the GPU."""
@@ -565,3 +601,47 @@ def test_two_streams_at_once():
                 got.append(md.kv_attention(c, b, q))
         torch.cuda.synchronize()
         assert all(torch.equal(a, w) for a, w in zip(got, want))
+
+
+def test_a_captured_call_follows_the_lengths():
+    """One graph of append and attention over long contexts, its batch's arrays
+    and pages rewritten between the replays; every replay equals the eager call
+    (long and short sequences, one without rows)."""
+    import moe_decode_amd as md
+    import torch
+    Hkv, G, dim, page = 2, 4, 128, 64
+    rng = np.random.default_rng(21)
+    cases = [([1, 1, 1], [1900, 3, 700]), ([1, 0, 2], [64, 500, 2000]), ([2, 1, 0], [129, 1999, 0])]
+    tables = [_tables(l, page, rng) for _, l in cases]
+    n = max(t[1] for t in tables)
+    m = Cache(n, Hkv, page, dim, rng)
+    live, ref = _to_gpu(m), _to_gpu(m)
+    rows = 3
+    b = md.KVBatch(_i32([0, 0, 0, 0]), _i32([0, 0, 0]), _i32(np.zeros((3, 32))), 2, 2000)
+    q, k, v = (torch.zeros(rows, h, dim, device="cuda") for h in (Hkv * G, Hkv, Hkv))
+    out = torch.empty(rows, Hkv * G, dim, device="cuda")
+    ws = torch.empty(md.kv_attention_workspace_size(live, b, rows, Hkv * G), dtype=torch.uint8, device="cuda")
+
+    def call(c, o, w=None):
+        md.kv_append(c, b, k, v)
+        md.kv_attention(c, b, q, out=o, workspace=w)
+    call(live, out, ws)                     # (no rows: writes nothing)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(live, out, ws)
+    for turn in range(6):
+        (nq, lens), (table, _) = cases[turn % 3], tables[turn % 3]
+        b.q_start.copy_(_i32(np.concatenate([[0], np.cumsum(nq)])))
+        b.kv_len.copy_(_i32(lens))
+        b.table.zero_()
+        b.table[:, :table.shape[1]].copy_(_i32(np.maximum(table, 0)))
+        for t in (q, k, v):
+            t.copy_(torch.from_numpy(rng.standard_normal(t.shape).astype(np.float32)))
+        g.replay()
+        want = torch.empty_like(out)
+        call(ref, want)
+        r = sum(nq)
+        assert torch.equal(out[:r], want[:r]), turn
+        assert torch.equal(live.k, ref.k) and torch.equal(live.v, ref.v) and torch.equal(live.k_scale, ref.k_scale)
+        torch.cuda.synchronize()
