@@ -690,7 +690,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
         for (int i = 0; i < 16; ++i) {
           const float p = __builtin_amdgcn_exp2f(fmaf(x[b][i], f, -ref));
           sum += p;
-          const float pw = p * w;
+          float pw = p * w;
+          // both parts from one rounded product: fused into the first conversion and not into the second, a
+          // tie could round two ways and leave a weight 2^-11 off
+          if constexpr (NS == 2) asm volatile("" : "+v"(pw));
           pf[0][2 * b + (i >> 3)][i & 7] = (_Float16)pw;
           if constexpr (NS == 2) pf[1][2 * b + (i >> 3)][i & 7] = (_Float16)(pw - (float)pf[0][2 * b + (i >> 3)][i & 7]);
         }

@@ -253,6 +253,26 @@ def test_attention(case, xt, out):
     assert bool((y[rows] == 5.0).all())     # the row behind the last sequence
 
 
+@pytest.mark.parametrize("max_q", [4, 300])
+def test_every_weight_is_right(max_q):
+    """Values of which each channel holds one token: the outputs are the softmax
+    weights, each within the bound by itself (4 rows of 4 heads: the form for
+    few columns; 300 of them: the one for many, whose weights are two f16)."""
+    import moe_decode_amd as md
+    Hkv, G, dim, page = 1, 4, 64, 64
+    rng = np.random.default_rng(77)
+    m = Cache(1, Hkv, page, dim, rng)
+    m.c["v"][:] = (127 * np.eye(64)).astype(np.int8)
+    m.s["v"][:] = 1 / 127
+    c = _to_gpu(m)
+    q, qn = _rn(rng, (max_q, G, dim), "f32")
+    q, qn = q * 0.25, qn * np.float32(0.25)
+    y = md.kv_attention(c, _batch([max_q], [64], [[0]]), q, causal=False).double().cpu().numpy()
+    want, tol = attention(qn, m.values("k", [0], 64), m.values("v", [0], 64), 0.125, False, 0, "f32", many=max_q > 16)
+    assert (tol <= 1e-4 * want).all()
+    assert (np.abs(y - want) <= tol).all(), float((np.abs(y - want) / want).max())
+
+
 @pytest.mark.parametrize("S,Hkv,G,D,page,window,out", [
     (700, 1, 2, 64, 64, 0, "f32"), (1024, 1, 1, 64, 64, 0, "bf16"), (1025, 1, 1, 64, 64, 0, "f32"),
     (37, 2, 8, 128, 64, 0, "f32"), (37, 2, 8, 128, 128, 90, "bf16"), (5, 1, 3, 256, 256, 0, "f32"),
