@@ -506,17 +506,18 @@ md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*hos
  * q_heads x head_dim, fp32 or bf16 (xtype, ytype), row strides in values, a
  * multiple of 16 bytes; out must not overlap q.
  * Accuracy: the cache's codes enter exactly, sums of integers are exact or in
- * fp32, and everything else is fp32.  Up to 64 columns a query row (one head)
- * is rounded to integers of its largest magnitude / 8355704 (bf16 out:
+ * fp32, and everything else is fp32.  In the form for few columns a query row (one
+ * head) is rounded to integers of its largest magnitude / 8355704 (bf16 out:
  * / 32638), a softmax weight to integers of 1 / 8355711 (1 / 32639) of the
- * largest weight among its workgroup's tokens so far.  Over 64 columns a
- * query's channel and a weight (times its page's value scale) are rounded to 22
+ * largest weight among its workgroup's tokens so far.  In the form for many (over
+ * 64 columns, max_q * q_heads / kv_heads; fp32 out of 256 channels: over 512 on
+ * at most 2560 positions) a query's channel and a weight (times its page's value scale) are rounded to 22
  * bits (bf16 out: 11).  A non-finite q makes its own row and head NaN; so does a
  * page whose scale is not in 0..2^126 for the rows that see it.
- * Long sequences are split over workgroups and joined by a second kernel (up
- * to 64 columns, max_q * q_heads / kv_heads: all tiles of the batch are dealt
- * out evenly, following the lengths on the device); the order of every sum is
- * fixed, so the same batch gives the same bits.
+ * Long sequences are split over workgroups and joined by a second kernel (few
+ * columns: all tiles of the batch are dealt out evenly, following the lengths on
+ * the device); the order of every sum is fixed, so the same batch gives the same
+ * bits.
  * Errors: a null pointer, an unknown type, causal not 0 or 1, window < 0 or
  * without causal, a scale that is not finite, out == q -> MD_ERR_INVALID_ARG;
  * sizes that are not positive, a stride below its row, q_heads no multiple of
@@ -525,7 +526,7 @@ md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*hos
  * -> MD_ERR_ALIGNMENT; a workspace below md_kv_attention_workspace_size ->
  * MD_ERR_WORKSPACE. */
 md_status md_kv_attention_workspace_size(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, int32_t q_heads,
-                                         int32_t causal, int32_t window, size_t *bytes /*host*/);
+                                         int32_t causal, int32_t window, int32_t ytype, size_t *bytes /*host*/);
 md_status md_kv_attention(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, const void *q, int32_t xtype,
                           int32_t q_heads, int64_t q_stride, float scale, int32_t causal, int32_t window, void *out,
                           int32_t ytype, int64_t out_stride, void *workspace, size_t workspace_bytes,

@@ -105,7 +105,7 @@ def lib():
             "md_i8_linear_workspace_size": (i32, [vp, i32, psz]),
             "md_i8_linear": (i32, [vp, vp, i32, i32, vp, vp, i32, vp, sz, vp]),
             "md_kv_append": (i32, [vp, vp, vp, i64, vp, i64, i32, vp]),
-            "md_kv_attention_workspace_size": (i32, [vp, vp, i32, i32, i32, psz]),
+            "md_kv_attention_workspace_size": (i32, [vp, vp, i32, i32, i32, i32, psz]),
             "md_kv_attention": (i32, [vp, vp, vp, i32, i32, i64, ctypes.c_float, i32, i32, vp, i32, i64, vp, sz, vp]),
             "md_kv_read_pages": (i32, [vp, vp, i32, vp, vp, i32, vp]),
             "md_kv_copy_pages": (i32, [vp, vp, vp, i32, vp]),
@@ -696,10 +696,11 @@ def kv_append(cache, batch, k, v, stream=None):
                                   vs, _xtype(k.dtype), st))
 
 
-def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0):
+def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0, out_dtype=None):
+    import torch
     need = ctypes.c_size_t(0)
     _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads,
-                                                int(causal), window, ctypes.byref(need)))
+                                                int(causal), window, _xtype(out_dtype or torch.float32), ctypes.byref(need)))
     return need.value
 
 
@@ -724,13 +725,13 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         if out.shape[0] != rows:
             raise ValueError(f"out has {out.shape[0]} rows, q {rows}")
         os_ = _rows("out", out, heads, cache.head_dim, cache.device)
-        L, d = lib(), batch.desc(rows)
+        L, d, yt = lib(), batch.desc(rows), _xtype(out.dtype)
         need = ctypes.c_size_t(0)
-        _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, ctypes.byref(need)))
+        _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
+                                                ctypes.byref(need)))
         ws, wsb = _workspace(need.value, cache.device, workspace)
         _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
-                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out),
-                                 _xtype(out.dtype), os_, _ptr(ws), wsb, st))
+                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws), wsb, st))
     return out
 
 

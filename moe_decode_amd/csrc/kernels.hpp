@@ -239,7 +239,7 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const void* k, i
                             int64_t v_stride, int xt, hipStream_t st);
 hipError_t launch_kv_read(const KvCache& c, const int* pages, int n, void* k, void* v, int yt, hipStream_t st);
 hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int n, hipStream_t st);
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal);
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal, int yt);
 hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st);
 
 }  // namespace md

@@ -125,7 +125,7 @@ size_t attn_slots(const md::KvPlan& p, const md_kv_batch* b, int32_t q_heads) {
 
 // The attention's checks up to its pointers, and its launch geometry.
 md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal, int32_t window,
-                    md::KvPlan* plan, size_t* bytes) {
+                    int32_t ytype, md::KvPlan* plan, size_t* bytes) {
   md_status s;
   if ((s = check_cache(c)) != MD_OK || (s = check_batch(c, b)) != MD_OK) return s;
   if (q_heads <= 0 || q_heads % c->kv_heads)
@@ -134,8 +134,9 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
   if (causal != 0 && causal != 1) return fail(MD_ERR_INVALID_ARG, "attention: causal = %d", causal);
   if (window < 0 || (window > 0 && !causal))
     return fail(MD_ERR_INVALID_ARG, "attention: window %d%s", window, causal ? "" : " without causal");
+  if (!valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown ytype %d", ytype);
   const int G = q_heads / c->kv_heads;
-  *plan = md::kv_attn_plan(dev(c), dev(b), G, window, causal);
+  *plan = md::kv_attn_plan(dev(c), dev(b), G, window, causal, ytype);
   const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
   if (groups > INT32_MAX) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
   const size_t slots = attn_slots(*plan, b, q_heads);
@@ -310,10 +311,10 @@ md_status md_kv_copy_pages(const md_kv_cache* c, const int32_t* src, const int32
 }
 
 md_status md_kv_attention_workspace_size(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal,
-                                         int32_t window, size_t* bytes) {
+                                         int32_t window, int32_t ytype, size_t* bytes) {
   md::KvPlan plan;
   size_t need = 0;
-  const md_status s = attn_plan(c, b, q_heads, causal, window, &plan, &need);
+  const md_status s = attn_plan(c, b, q_heads, causal, window, ytype, &plan, &need);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
   *bytes = need;
@@ -325,9 +326,9 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
                           int64_t out_stride, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   md::KvPlan plan;
   size_t need = 0;
-  md_status s = attn_plan(c, b, q_heads, causal, window, &plan, &need);
+  md_status s = attn_plan(c, b, q_heads, causal, window, ytype, &plan, &need);
   if (s != MD_OK) return s;
-  if (!valid_xtype(xtype) || !valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown xtype %d or ytype %d", xtype, ytype);
+  if (!valid_xtype(xtype)) return fail(MD_ERR_INVALID_ARG, "unknown xtype %d", xtype);
   if (!std::isfinite(scale)) return fail(MD_ERR_INVALID_ARG, "attention: scale %g", scale);
   if (b->rows == 0) return ok();
   const int64_t width = (int64_t)q_heads * c->head_dim;

@@ -405,18 +405,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
   int s = blockIdx.y, plain_seg = blockIdx.x;  // without a deal: one segment a workgroup
   int64_t u = 0, end = 1, total = 0, runs = 0;
   if (a.pieces) {
-    // tiles before each sequence (rolled: code that runs once is fetched cold)
+    // tiles before each sequence; a thread takes `per` neighbouring ones
+    const int per = (a.b.S + 255) >> 8;
     int64_t sum = 0;
 #pragma unroll 1
-    for (int i = 0; i < kMaxDealt / 256; ++i) {
-      const int e = tid * (kMaxDealt / 256) + i;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
       int64_t n = 0;
       if (e < a.b.S) {
         const Seq q = seq_of(a.b, e, a.c.page);
         int t0;
         if (q.nq) n = (int64_t)((q.nq * a.G + 15) / 16) * Hkv * tiles_of(a, q, q.nq * a.G, t0);
+        first[e] = sum;
       }
-      first[e] = sum;
       sum += n;
     }
     int64_t upto = sum;
@@ -433,9 +434,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
       if (w < tid >> 6) before += waves[w];
       total += waves[w];
     }
-#pragma unroll
-    for (int i = 0; i < kMaxDealt / 256; ++i) first[tid * (kMaxDealt / 256) + i] += before;
-    if (tid == 0) first[kMaxDealt] = total;
+    for (int e = tid * per; e < min(tid * per + per, a.b.S); ++e) first[e] += before;
+    if (tid == 0) first[a.b.S] = total;
     __syncthreads();
     // runs of four tiles at least: one a wave
     runs = max(min((int64_t)a.pieces, total / kWaves), (int64_t)(total > 0));
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     if (blockIdx.x >= runs) return;
     u = blockIdx.x * total / runs;
     end = (blockIdx.x + 1) * total / runs;
-    int lo = 0, hi = kMaxDealt;  // the sequence of tile u: first[lo] <= u < first[lo + 1]
+    int lo = 0, hi = a.b.S;  // the sequence of tile u: first[lo] <= u < first[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (first[mid] <= u) lo = mid;
@@ -842,12 +842,19 @@ __global__ __launch_bounds__(256) void k_kv_join_pieces(KvAttn a) {
   store_out4(a, (int64_t)q.row0 + qt, h * a.G + (c - qt * a.G), D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal) {
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal, int yt) {
   int64_t most = b.max_kv;
   if (causal && window && (int64_t)window + b.max_q < most) most = (int64_t)window + b.max_q;
   const int64_t tiles = (most + kTile - 1) / kTile + 1;
   KvPlan p{};
-  p.tile = (int64_t)b.max_q * G > 64 ? kRowCols : 16;
+  // More than four column tiles: the form that shares its loads among 128
+  // columns (80 columns, 16 sequences of 4000: 41 us, 51 in the other one; 64:
+  // 41 both).  fp32 outputs of 256 channels do not fit its registers, so there
+  // it is kept for columns by the hundreds on short sequences (8 of 256 new in
+  // 2048 tokens: 357 us against 412; 2048 in 4096: 747 against 480).
+  const int64_t cols = (int64_t)b.max_q * G;
+  const bool tight = c.D == 256 && yt == XF32;
+  p.tile = cols > (tight ? 512 : 64) && !(tight && most > 2560) ? kRowCols : 16;
   p.splits = 1;
   p.chunk = (int)tiles;
   if (p.tile == 16) {
@@ -857,9 +864,14 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int c
     if (tiles > 2 * kWaves && b.S <= kMaxDealt) p.pieces = device_cus() * (c.D == 64 ? 4 : c.D == 128 ? 2 : 1);
     return p;
   }
-  // enough workgroups to fill the chip, a split a fixed number of tiles
+  // where the columns alone give most compute units a workgroup, sequences stay
+  // whole (8 of 256 new in 2048 tokens, 16 heads on 4 of 128: 63 us, in two
+  // parts 91; 2048 new in 4096: 123, 152); else two workgroups a unit, a split a
+  // fixed number of tiles (1024 new in 8192: 126 us; one a unit 146)
   const int64_t base = (int64_t)b.S * c.Hkv * (((int64_t)b.max_q * G + p.tile - 1) / p.tile);
-  int64_t chunk = (tiles * base + 511) / 512;
+  if (4 * base >= 3 * (int64_t)device_cus()) return p;
+  const int64_t want = 2 * device_cus();
+  int64_t chunk = (tiles * base + want - 1) / want;
   if (chunk < 4) chunk = 4;
   p.chunk = (int)(chunk < tiles ? chunk : tiles);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);

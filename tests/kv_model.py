@@ -126,6 +126,15 @@ def attention(q, k, v, scale, causal, window, out, many=False):
     return o, tol
 
 
+def many_columns(max_q, G, D, max_kv, window, out):
+    """Which of the two forms a call takes (causal, where a window is given)."""
+    if window:
+        max_kv = min(max_kv, window + max_q)
+    if D == 256 and out == "f32":
+        return max_q * G > 512 and max_kv <= 2560
+    return max_q * G > 64
+
+
 class Pages:
     """The page bookkeeping by plain sets: which table names which page."""
 

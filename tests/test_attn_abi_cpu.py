@@ -78,7 +78,7 @@ def test_bad_caches(kw, want):
     L, sz, n = md.lib(), ctypes.c_size_t(0), (ctypes.c_int32 * 1)(0)
     c, b = ctypes.byref(_c(**kw)), ctypes.byref(_b())
     assert _st(L.md_kv_append(c, b, FAKE, 256, FAKE, 256, 0, None)) == want
-    assert _st(L.md_kv_attention_workspace_size(c, b, 4, 1, 0, ctypes.byref(sz))) == want
+    assert _st(L.md_kv_attention_workspace_size(c, b, 4, 1, 0, 0, ctypes.byref(sz))) == want
     assert _st(L.md_kv_read_pages(c, FAKE, 1, FAKE, FAKE, 0, None)) == want
     assert _st(L.md_kv_copy_pages(c, n, n, 1, None)) == want
 
@@ -116,11 +116,12 @@ def test_attention_and_append_errors():
     assert att(out=FAKE) == "MD_ERR_INVALID_ARG"        # in place
     assert att(os_=500) == "MD_ERR_SHAPE"
     wide = ctypes.byref(_b(S=1, max_kv=100000, stride=1563))
-    assert L.md_kv_attention_workspace_size(c, wide, 4, 1, 0, ctypes.byref(sz)) == 0 and sz.value > 0
+    assert L.md_kv_attention_workspace_size(c, wide, 4, 1, 0, 0, ctypes.byref(sz)) == 0 and sz.value > 0
     assert att(bb=wide, wsb=sz.value - 1) == "MD_ERR_WORKSPACE"
     assert att(bb=wide, ws=None) == "MD_ERR_WORKSPACE"
     assert att(bb=wide, ws=ODD) == "MD_ERR_ALIGNMENT"
-    assert _st(L.md_kv_attention_workspace_size(c, wide, 4, 1, 0, None)) == "MD_ERR_INVALID_ARG"
+    assert _st(L.md_kv_attention_workspace_size(c, wide, 4, 1, 0, 0, None)) == "MD_ERR_INVALID_ARG"
+    assert _st(L.md_kv_attention_workspace_size(c, wide, 4, 1, 0, 2, ctypes.byref(sz))) == "MD_ERR_INVALID_ARG"
     none = ctypes.byref(_b(rows=0, q_start=None, kv_len=None, table=None))
     assert L.md_kv_attention(c, none, None, 0, 4, 512, 0.1, 1, 0, None, 0, 512, None, 0, None) == 0
     assert L.md_kv_append(c, none, None, 256, None, 256, 0, None) == 0

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from .gpu_common import require_gpu, say
-from .kv_model import Cache, attention
+from .kv_model import Cache, attention, many_columns
 
 pytestmark = pytest.mark.gpu
 
@@ -219,6 +219,7 @@ ATTN = [  # key heads, group, dim, page, (new, length) of each sequence, causal,
     (2, 4, 128, 64, [(40, 1500), (3, 50), (17, 17)], True, 0),
     (1, 16, 64, 128, [(4, 900), (5, 1000)], False, 0),
     (1, 5, 256, 64, [(13, 700), (20, 90)], True, 200),
+    (1, 8, 256, 64, [(70, 700), (3, 90)], True, 0),
 ]
 
 
@@ -244,7 +245,7 @@ def test_attention(case, xt, out):
     worst = 0.0
     for i, (a, b) in enumerate(seqs):
         want, tol = attention(qn[at:at + a], m.values("k", table[i], b), m.values("v", table[i], b), scale, causal,
-                              window, out, many=max(nq) * G > 64)
+                              window, out, many=many_columns(max(nq), G, dim, max(lens), window, out))
         err = np.abs(got[at:at + a] - want)
         assert (err <= tol).all(), (i, float((err / tol).max()))
         worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()) if a else 0.0)
