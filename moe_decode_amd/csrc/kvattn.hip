@@ -858,10 +858,15 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int c
   p.splits = 1;
   p.chunk = (int)tiles;
   if (p.tile == 16) {
-    // as many workgroups as run at once (registers: one, two or four on a
-    // compute unit); segments of up to two tiles a wave are not worth a second
-    // kernel
-    if (tiles > 2 * kWaves && b.S <= kMaxDealt) p.pieces = device_cus() * (c.D == 64 ? 4 : c.D == 128 ? 2 : 1);
+    // A segment each where they are short, or middling and enough of them: the
+    // deal and its join cost some 8 us (64 channels x 2, us without and with:
+    // 16 new in 1000 tokens of 4 sequences 12 and 20, 1 in 2000 of 64: 21 and 33,
+    // 1 in 2000 of one: 16 and 12, 1 in 4000 of 64: 33 and 41, of one: 26 and 17).
+    // Else as many workgroups as run at once (registers: one, two or four on a
+    // compute unit).
+    const int64_t segments = (int64_t)b.S * c.Hkv * ((cols + 15) / 16);
+    const bool whole = tiles <= 17 || (tiles <= 33 && segments >= 16) || (tiles <= 65 && segments >= device_cus());
+    if (!whole && b.S <= kMaxDealt) p.pieces = device_cus() * (c.D == 64 ? 4 : c.D == 128 ? 2 : 1);
     return p;
   }
   // where the columns alone give most compute units a workgroup, sequences stay

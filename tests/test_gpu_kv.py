@@ -279,7 +279,7 @@ def test_every_weight_is_right(max_q):
     (37, 2, 8, 128, 64, 0, "f32"), (37, 2, 8, 128, 128, 90, "bf16"), (5, 1, 3, 256, 256, 0, "f32"),
     (3, 4, 5, 64, 64, 700, "f32")])
 def test_ragged_batches_dealt_out(S, Hkv, G, D, page, window, out):
-    """Sequences of 0 to 1500 positions with 0 to 3 new rows each, some without
+    """Sequences of 0 to 4500 positions with 0 to 3 new rows each, some without
     rows, some that see nothing: every row against the definition; the same call
     again gives the same bits."""
     import moe_decode_amd as md
@@ -287,7 +287,7 @@ def test_ragged_batches_dealt_out(S, Hkv, G, D, page, window, out):
     rng = np.random.default_rng(S + D)
     nq = rng.integers(0, 4, S)
     lens = np.where(rng.random(S) < 0.7, rng.integers(0, 40, S), rng.integers(0, 1500, S))
-    nq[-1], lens[-1], nq[0] = 0, 1500, 3
+    nq[-1], lens[-1], nq[0], lens[1] = 0, 4500, 3, 4300
     nq, lens = nq.tolist(), lens.tolist()
     table, n = _tables(lens, page, rng)
     m = Cache(n, Hkv, page, D, rng)
@@ -632,13 +632,13 @@ def test_a_captured_call_follows_the_lengths():
     import torch
     Hkv, G, dim, page = 2, 4, 128, 64
     rng = np.random.default_rng(21)
-    cases = [([1, 1, 1], [1900, 3, 700]), ([1, 0, 2], [64, 500, 2000]), ([2, 1, 0], [129, 1999, 0])]
+    cases = [([1, 1, 1], [1900, 3, 700]), ([1, 0, 2], [64, 500, 2000]), ([2, 1, 0], [129, 4999, 0])]
     tables = [_tables(l, page, rng) for _, l in cases]
     n = max(t[1] for t in tables)
     m = Cache(n, Hkv, page, dim, rng)
     live, ref = _to_gpu(m), _to_gpu(m)
     rows = 3
-    b = md.KVBatch(_i32([0, 0, 0, 0]), _i32([0, 0, 0]), _i32(np.zeros((3, 32))), 2, 2000)
+    b = md.KVBatch(_i32([0, 0, 0, 0]), _i32([0, 0, 0]), _i32(np.zeros((3, 80))), 2, 5000)
     q, k, v = (torch.zeros(rows, h, dim, device="cuda") for h in (Hkv * G, Hkv, Hkv))
     out = torch.empty(rows, Hkv * G, dim, device="cuda")
     ws = torch.empty(md.kv_attention_workspace_size(live, b, rows, Hkv * G), dtype=torch.uint8, device="cuda")
