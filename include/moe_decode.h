@@ -470,7 +470,7 @@ typedef struct md_kv_cache {
 typedef struct md_kv_batch {
     int32_t n_seqs;            /* 1..65535                                    */
     int32_t rows;              /* rows of the call's tensors, 0..2^20         */
-    int32_t max_q, max_kv;     /* bounds of the runs and of kv_len, >= 1      */
+    int32_t max_q, max_kv;     /* bounds of the runs (to 2^20) and of kv_len (to 2^30), >= 1 */
     int32_t table_stride;      /* entries per sequence, * page >= max_kv      */
     const int32_t *q_start;    /* [n_seqs + 1]                                */
     const int32_t *kv_len;     /* [n_seqs]                                    */
@@ -535,7 +535,7 @@ md_status md_kv_attention(const md_kv_cache *c /*host*/, const md_kv_batch *b /*
 /* The values that n pages hold (pages: device, n int32): k and v as
  * [n][kv_heads][page][head_dim] in ytype, both with the token before the
  * channel.  Slots that no token has reached give what their codes stand for; a
- * page number outside the cache gives NaN.  n = 0: nothing to do. */
+ * page number outside the cache gives NaN.  n: 0 (nothing to do) .. 2^24 - 1. */
 md_status md_kv_read_pages(const md_kv_cache *c /*host*/, const int32_t *pages, int32_t n, void *k, void *v,
                            int32_t ytype, hipStream_t stream);
 

@@ -541,14 +541,26 @@ class _on:
             torch.cuda.set_device(self.back)
 
 
-def _i8_desc(W):
-    """The C descriptor of an int8 matrix, made once while its tensors stay."""
+def _i8_desc(W, device=None):
+    """The C descriptor of an int8 matrix, made once while its tensors stay;
+    they have to hold the matrix and lie on `device`."""
+    import torch
     d, q, sc = W.__dict__.get("_i8"), W.q.data_ptr(), _ptr(W.row_scale)
     if d is None or d.q != q or d.row_scale != sc:
         if W.count != 1:
             raise ValueError(f"one matrix wanted, got a stack of {W.count}")
+        if W.type == I8_ROW:
+            r = W.row_scale
+            if not W.q.is_contiguous() or W.q.numel() * W.q.element_size() < W.rows * W.cols:
+                raise ValueError(f"W.q: {W.rows} x {W.cols} bytes wanted, got {tuple(W.q.shape)} of {W.q.dtype}")
+            if r is not None and (r.dtype != torch.float32 or not r.is_contiguous() or r.numel() < W.rows
+                                  or r.device != W.q.device):
+                raise ValueError(f"W.row_scale: {W.rows} float32 values on {W.q.device} wanted, got "
+                                 f"{tuple(r.shape)} of {r.dtype} on {r.device}")
         d = W._i8 = W.desc()
-        W._i8_ref = ctypes.byref(d)
+        W._i8_ref, W._i8_dev = ctypes.byref(d), W.q.device
+    if device is not None and W._i8_dev != device:
+        raise ValueError(f"W is on {W._i8_dev}, the call's tensors on {device}")
     return W._i8_ref
 
 
@@ -587,7 +599,7 @@ def i8_matmul(W, codes, scales, bias=None, y=None, out_dtype=None, stream=None):
     _dense("scales", scales, (T,), torch.float32, dev)
     with _on(dev, stream) as st:
         y = _i8_args(W, T, bias, y, out_dtype, dev)
-        _check(lib().md_i8_matmul(_i8_desc(W), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
+        _check(lib().md_i8_matmul(_i8_desc(W, dev), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
                                   _xtype(y.dtype), st))
     return y
 
@@ -604,7 +616,7 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
     _dense("x", x, (T, W.cols), x.dtype, dev)
     with _on(dev, stream) as st:
         y = _i8_args(W, T, bias, y, out_dtype, dev)
-        L, d = lib(), _i8_desc(W)
+        L, d = lib(), _i8_desc(W, dev)
         ws, wsb = None, 0
         if T > 1:
             need = ctypes.c_size_t(0)
@@ -700,7 +712,8 @@ def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window
     import torch
     need = ctypes.c_size_t(0)
     _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads,
-                                                int(causal), window, _xtype(out_dtype or torch.float32), ctypes.byref(need)))
+                                                int(causal), window, _xtype(out_dtype or torch.float32),
+                                                ctypes.byref(need)))
     return need.value
 
 
@@ -731,7 +744,8 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
                                                 ctypes.byref(need)))
         ws, wsb = _workspace(need.value, cache.device, workspace)
         _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
-                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws), wsb, st))
+                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws),
+                                 wsb, st))
     return out
 
 

@@ -31,9 +31,10 @@ MD_DEV RowScale row_scale_of(uint32_t top) {
   const float amax = __uint_as_float(top), s = top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
   return RowScale{s, step_of(s, amax)};
 }
+
 // One row per group of WPR waves (WPR 1: four rows a workgroup), the whole row
 // in registers between the maximum and the codes: x is read once.  Bound by
-// the read of x.
+// the read of x (8191 x 6144 bf16: 28 us, 5.4 TB/s read and written together).
 template <int XT, int WPR, int STEPS>
 __global__ __launch_bounds__(256) void k_i8_quantize(const void* __restrict__ x, int T, int K,
                                                      int8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -134,9 +135,12 @@ MD_DEV void put4(void* y, int64_t row, int N, int n, const i32x4& a, float xs, c
 // its waves split the sum and meet in LDS.  Weights go from HBM straight into
 // the matrix cores' operand registers (lane l: row l % 16, 16 bytes at
 // 64 step + 16 (l / 16)), codes of x from the L2.
-// OWN (one token; four took longer, 12.8 -> 21.7 us at 6144 x 6144): x itself comes in, and every workgroup
-// rounds the whole rows to codes in its LDS while its first weights are on
-// their way: one launch less, which is half of a small call.
+// Bound by the read of W (6144 x 6144, 4 tokens: 12.8 us for 37.7 MB, the
+// quantizer's launch included).
+// OWN (one token; four took 21.7 us there): x itself comes in, and every
+// workgroup rounds the whole row to codes in its LDS while its first weights are
+// on their way: one launch less, which is half of a small call (256 x 2048: 7.9
+// -> 4.7 us).
 template <int YT, int NT, bool OWN, int XT>
 __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, const float* __restrict__ ws, int N,
                                                  int K, const void* __restrict__ x, const float* __restrict__ xs_in,
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
 // unrolled over them: the compiler waits for all direct loads in flight before
 // an LDS read that might touch what they fill, and can only tell variables
 // apart (404 -> 326 us for 8191 tokens, 5632 channels, 6144 terms with the
-// quantizer's 35).  The large tile is bound by LDS reads, which deliver 64
+// quantizer, which was 35 of them then and is 28 now: 320).  The large tile is bound by LDS reads, which deliver 64
 // bytes a clock here: 24 of 1 KB per wave and step against 64 products of 16
 // clocks, 1.95 Pop/s of 2.35 that a large library product reaches.  Measured
 // and dropped: fragments read half a step ahead (332), 64-byte steps in four
@@ -231,11 +235,12 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
 // straight from L1 into registers (451 to 488).
 constexpr int kBK = 128;
 
-// All but the n youngest of this wave's loads have landed, and all waves are here.
+// All but the N youngest of this wave's loads have landed, its LDS reads are
+// done (the next load may overwrite what they read), and all waves are here.
 template <int N>
 MD_DEV void landed() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }

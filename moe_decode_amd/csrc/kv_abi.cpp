@@ -25,6 +25,8 @@ constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxKvHeads = 256;
+constexpr int kMaxPositions = 1 << 30;  // tiles' borders and windows before position 0 stay in 32 bits
+constexpr int kMaxGrid = (1 << 24) - 1;  // workgroups of 256 along x: below 2^32 threads
 
 bool valid_xtype(int32_t t) { return t == MD_X_F32 || t == MD_X_BF16; }
 int elem(int32_t t) { return t == MD_X_F32 ? 4 : 2; }
@@ -88,6 +90,8 @@ md_status check_batch(const md_kv_cache* c, const md_kv_batch* b) {
   if (b->n_seqs > kMaxSeqs || b->rows > kMaxTokens || b->max_q > kMaxTokens)
     return fail(MD_ERR_UNSUPPORTED, "batch: n_seqs %d (at most %d), rows %d, max_q %d (at most %d)", b->n_seqs, kMaxSeqs,
                 b->rows, b->max_q, kMaxTokens);
+  if (b->max_kv > kMaxPositions)
+    return fail(MD_ERR_UNSUPPORTED, "batch: max_kv %d > %d", b->max_kv, kMaxPositions);
   if ((int64_t)b->table_stride * c->page < b->max_kv)
     return fail(MD_ERR_SHAPE, "batch: %d pages of %d tokens hold no %d tokens", b->table_stride, c->page, b->max_kv);
   return MD_OK;
@@ -123,6 +127,9 @@ size_t attn_slots(const md::KvPlan& p, const md_kv_batch* b, int32_t q_heads) {
   return p.splits > 1 ? (size_t)b->rows * q_heads * p.splits : 0;
 }
 
+// A window that reaches past every position is none.
+int seen(const md_kv_batch* b, int32_t window) { return window >= b->max_kv ? 0 : window; }
+
 // The attention's checks up to its pointers, and its launch geometry.
 md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal, int32_t window,
                     int32_t ytype, md::KvPlan* plan, size_t* bytes) {
@@ -136,9 +143,9 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
     return fail(MD_ERR_INVALID_ARG, "attention: window %d%s", window, causal ? "" : " without causal");
   if (!valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown ytype %d", ytype);
   const int G = q_heads / c->kv_heads;
-  *plan = md::kv_attn_plan(dev(c), dev(b), G, window, causal, ytype);
+  *plan = md::kv_attn_plan(dev(c), dev(b), G, seen(b, window), causal, ytype);
   const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
-  if (groups > INT32_MAX) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
+  if (groups > kMaxGrid) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
   const size_t slots = attn_slots(*plan, b, q_heads);
   *bytes = slots ? align256(plan->pieces * sizeof(int4)) + align256(slots * 2 * sizeof(float)) +
                        align256(slots * c->head_dim * sizeof(float))
@@ -271,6 +278,7 @@ md_status md_kv_read_pages(const md_kv_cache* c, const int32_t* pages, int32_t n
   if ((s = check_cache(c)) != MD_OK) return s;
   if (!valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown ytype %d", ytype);
   if (n < 0) return fail(MD_ERR_SHAPE, "n = %d must not be negative", n);
+  if (n > kMaxGrid) return fail(MD_ERR_UNSUPPORTED, "n = %d pages > %d", n, kMaxGrid);
   if (n == 0) return ok();
   if (!pages) return fail(MD_ERR_INVALID_ARG, "pages: null pointer");
   if (!aligned4(pages)) return fail(MD_ERR_ALIGNMENT, "pages: not 4-byte aligned");
@@ -352,7 +360,7 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
   a.yt = ytype;
   a.G = q_heads / c->kv_heads;
   a.causal = causal;
-  a.window = window;
+  a.window = seen(b, window);
   a.pshift = c->page == 64 ? 6 : c->page == 128 ? 7 : 8;
   a.scale = scale;
   a.tile = plan.tile;

@@ -3,8 +3,9 @@
 //
 //   o = softmax(scale * q k^T + mask) v,   k = ks[page, head] K,  v = vs[page, head] V
 //
-// Both products run on the int8 matrix cores with the cache's codes as they
-// lie in memory.  The other operand is split into balanced base-256 digits: a
+// Two forms, by the number of (query, head) columns that share a key head: for
+// many of them see k_kv_attn_rows; for few, both products run on the int8 matrix
+// cores with the cache's codes as they lie in memory.  The other operand is split into balanced base-256 digits: a
 // query row (one token, one head) as integers of 2^-23 of its largest
 // magnitude (three digits; two for bf16 outputs: 2^-15), a softmax weight
 // p in [0, 1] as integers of 2^-23 (2^-15).  Every digit's sum is exact in
@@ -14,9 +15,9 @@
 // Operand layout.  Keys enter as the A operand (rows = tokens), queries as B
 // (columns = (query, head) pairs that share the key head), so the scores come
 // out with a column's tokens in one lane: lane l holds column l % 16 and the
-// rows 4 g + r, g = l / 16.  Row m of key tile j is token
-// 16 (m / 4) + 4 j + m % 4 of the 64, which makes lane group g's sixteen scores
-// the tokens 16 g .. 16 g + 15 -- exactly the 16 bytes of the contraction that
+// rows 4 g + r, g = l / 16.  Of 64 tokens, rows 4 g .. 4 g + 3 of every key tile
+// are some of 16 g .. 16 g + 15 (which: at the loads), so lane group g's sixteen
+// scores are those tokens' -- exactly the 16 bytes of the contraction that
 // the same lane feeds as the B operand of the second product, whose A operand
 // is 16 consecutive tokens of a channel of the transposed values.  The weights
 // never leave their lane: no LDS, no lane exchange but the row maximum's.
@@ -219,11 +220,11 @@ MD_DEV float weights(const float* x, float f, float ref, float scale, i32x4 (&pd
 // workgroup keeps at most its first and its last one's share in the workspace,
 // and the one where a segment begins notes how many shares there are for
 // k_kv_join_pieces.  Measured, with the join: 32 sequences of up to 8190 tokens,
-// 64 heads on 8 of 128 channels, 67 us (289 MB, 4.3 TB/s; fixed shares of max_kv
-// 76), two of up to 131071 on pages of 128 tokens 83 us (402 MB, 4.9 TB/s; 85).
-// A copy that only loads took 5% less than the kernel: it waits for memory.
-// Half, one and a half times and twice as many workgroups: 75, 77, 73 and 81,
-// 94, 89 us.
+// 64 heads on 8 of 128 channels, 65 us (289 MB, 4.4 TB/s; fixed shares of max_kv
+// 76), two of up to 131071 on pages of 128 tokens 81 us (402 MB, 5.0 TB/s; 85).
+// A form that only loaded took 5% less: it waits for memory.  Half, one and a
+// half times and twice as many workgroups, when it took 67 and 83: 75, 77, 73
+// and 81, 94, 89 us.
 constexpr int kMaxDealt = 1024;  // sequences, at most, that a workgroup sums up
 
 // The tiles that any column of a sequence sees, one at least where it has rows:
@@ -491,9 +492,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 // the codes are exact in f16 (converted once per workgroup on their way to
 // LDS), a query row is scaled by a power of two to below 2^14 and rounded to
 // f16, and so is a weight p times 2^14 vs / R, R the power of two at or below
-// the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second f16 for what the first one leaves,
-// 22 bits together.  Per score that leaves half a maximum, one fma, one exp2
-// (a quarter of the rate), the sum and half a conversion on the vector ALU.
+// the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second f16
+// for what the first one leaves, 22 bits together.  Per score that leaves half a
+// maximum, one fma, one exp2 (a quarter of the rate), the sum and half a
+// conversion on the vector ALU.
+//
+// Measured: 4096 new of 5003 tokens, 16 heads on 4 of 128 channels, bf16 out,
+// 157 us (99 GFlop, 0.63 Pflop/s; the int8 form's digits and joins 296).  Every
+// wave reads all of a tile's 32 KB from LDS, at 64 bytes a clock and compute
+// unit half of that time and twice what the products take; the softmax's vector
+// work stands between the two products, and two waves a SIMD overlap the rest
+// only in part.  Measured
+// and dropped: the next tile's first product beside this one's softmax (187 to
+// 196, registers), one wave a SIMD (307), wave priorities (162 to 164).
 //
 // 32 x 32 tiles: score row 8 a + 4 hh + b of a 32-token block is its token
 // 16 hh + 4 a + b, so lane half hh holds tokens 16 hh .. 16 hh + 15 and feeds

@@ -68,6 +68,7 @@ BAD_CACHE = [(dict(n=0), "MD_ERR_SHAPE"), (dict(heads=0), "MD_ERR_SHAPE"), (dict
              (dict(v=ODD), "MD_ERR_ALIGNMENT"), (dict(ks=None), "MD_ERR_INVALID_ARG"), (dict(vs=ODD), "MD_ERR_ALIGNMENT")]
 BAD_BATCH = [(dict(S=0), "MD_ERR_SHAPE"), (dict(S=65536), "MD_ERR_UNSUPPORTED"), (dict(rows=-1), "MD_ERR_SHAPE"),
              (dict(max_q=0), "MD_ERR_SHAPE"), (dict(max_kv=0), "MD_ERR_SHAPE"), (dict(max_kv=129), "MD_ERR_SHAPE"),
+             (dict(max_kv=(1 << 30) + 1, stride=1 << 25), "MD_ERR_UNSUPPORTED"),
              (dict(stride=0), "MD_ERR_SHAPE"), (dict(rows=(1 << 20) + 1), "MD_ERR_UNSUPPORTED"),
              (dict(q_start=None), "MD_ERR_INVALID_ARG"), (dict(kv_len=FAKE + 2), "MD_ERR_ALIGNMENT"),
              (dict(table=None), "MD_ERR_INVALID_ARG")]
@@ -132,6 +133,7 @@ def test_attention_and_append_errors():
     assert _st(ap(c, b, None, 256, FAKE, 256, 0, None)) == "MD_ERR_INVALID_ARG"
     assert _st(ap(c, b, FAKE, 256, FAKE, 256, 7, None)) == "MD_ERR_INVALID_ARG"
     rd = L.md_kv_read_pages
+    assert _st(rd(c, FAKE, 1 << 24, FAKE, FAKE, 0, None)) == "MD_ERR_UNSUPPORTED"
     assert _st(rd(c, None, 2, FAKE, FAKE, 0, None)) == "MD_ERR_INVALID_ARG"
     assert _st(rd(c, FAKE + 2, 2, FAKE, FAKE, 0, None)) == "MD_ERR_ALIGNMENT"
     assert _st(rd(c, FAKE, -2, FAKE, FAKE, 0, None)) == "MD_ERR_SHAPE"
@@ -149,3 +151,18 @@ def test_copy_pairs_that_meet_are_refused(src, dst):
     assert _st(L.md_kv_copy_pages(c, None, a(*dst), n, None)) == "MD_ERR_INVALID_ARG"
     assert _st(L.md_kv_copy_pages(c, a(*src), a(*dst), -1, None)) == "MD_ERR_SHAPE"
     assert L.md_kv_copy_pages(c, None, None, 0, None) == 0
+
+
+def test_matrices_that_do_not_hold_what_they_say():
+    """The binding refuses what the C call cannot see: a matrix on another
+    device than the call's tensors, too short, or with scales of another type."""
+    import torch
+    q, s = torch.zeros(64 * 256, dtype=torch.int8), torch.zeros(64)
+    ok = md.DevQMatrix("i8_row", 64, 256, q, s)
+    md._i8_desc(ok, torch.device("cpu"))
+    with pytest.raises(ValueError):
+        md._i8_desc(ok, torch.device("cuda:0"))
+    for bad in (md.DevQMatrix("i8_row", 64, 512, q, s), md.DevQMatrix("i8_row", 64, 256, q, s.double()),
+                md.DevQMatrix("i8_row", 64, 256, q, s[:63]), md.DevQMatrix("i8_row", 64, 256, q.view(64, 256).t(), s)):
+        with pytest.raises(ValueError):
+            md._i8_desc(bad, torch.device("cpu"))

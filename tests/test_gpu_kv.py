@@ -72,6 +72,7 @@ APPENDS = [  # heads, dim, page, (new, length) of each sequence
     (1, 128, 256, [(257, 300), (256, 256), (1, 512), (17, 33)]),
     (2, 64, 64, [(1, 2), (1, 6), (1, 7), (1, 8), (2, 70), (1, 64)]),      # every place in a word, held tokens before it
     (1, 256, 256, [(3, 35), (8, 30), (1, 131)]),
+    (1, 256, 256, [(256, 256), (300, 400), (1, 700)]),                     # whole pages of 64 KB
 ]
 
 
@@ -220,6 +221,9 @@ ATTN = [  # key heads, group, dim, page, (new, length) of each sequence, causal,
     (1, 16, 64, 128, [(4, 900), (5, 1000)], False, 0),
     (1, 5, 256, 64, [(13, 700), (20, 90)], True, 200),
     (1, 8, 256, 64, [(70, 700), (3, 90)], True, 0),
+    (2, 4, 128, 64, [(12, 5), (5, 300)], True, 2 ** 31 - 1),                # windows past every position, and runs
+    (1, 4, 64, 64, [(200, 90), (3, 64)], True, 2 ** 31 - 1),                # that begin before the first one
+    (2, 4, 64, 64, [(9, 100), (2, 100)], True, 100),
 ]
 
 
