@@ -434,8 +434,8 @@ md_status md_i8_quantize(const void *x, int32_t xtype, int32_t T, int32_t K, int
 /* y from codes and scales; bias: device, W->rows fp32, or NULL; ytype: md_xtype. */
 md_status md_i8_matmul(const md_qmatrix *W /*host*/, const int8_t *codes, const float *scales, int32_t T,
                        const float *bias, void *y, int32_t ytype, hipStream_t stream);
-/* Both: y = W Q(x) (+ bias), the codes in the workspace (one token needs
- * none: then the size is 0 and workspace may be NULL). */
+/* Both: y = W Q(x) (+ bias), the codes in the workspace (one token and some
+ * small calls need none: then the size is 0 and workspace may be NULL). */
 md_status md_i8_linear_workspace_size(const md_qmatrix *W /*host*/, int32_t T, size_t *bytes /*host*/);
 md_status md_i8_linear(const md_qmatrix *W /*host*/, const void *x, int32_t xtype, int32_t T, const float *bias,
                        void *y, int32_t ytype, void *workspace, size_t workspace_bytes, hipStream_t stream);

@@ -621,7 +621,8 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
         if T > 1:
             need = ctypes.c_size_t(0)
             _check(L.md_i8_linear_workspace_size(d, T, ctypes.byref(need)))
-            ws, wsb = _workspace(need.value, dev, workspace)
+            if need.value:
+                ws, wsb = _workspace(need.value, dev, workspace)
         _check(L.md_i8_linear(d, x.data_ptr(), _xtype(x.dtype), T, _ptr(bias), y.data_ptr(), _xtype(y.dtype), _ptr(ws),
                               wsb, st))
     return y

@@ -96,7 +96,8 @@ hipError_t launch_i8_quantize(const void* x, int xt, int T, int K, int8_t* codes
 
 // ---- products ------------------------------------------------------------
 
-constexpr int kOwnTokens = 1;      // up to these: each workgroup forms the codes itself
+constexpr int kOwnTokens = 8;      // up to these each workgroup may form the codes itself
+constexpr int kOwnSteps = 4;       // ... of rows of up to 512 times this, one wave a row
 constexpr int kFewTokens = 32;     // up to these: k_i8_few
 constexpr int kSplitTokens = 512;  // up to these the sum may be split
 
@@ -137,16 +138,16 @@ MD_DEV void put4(void* y, int64_t row, int N, int n, const i32x4& a, float xs, c
 // 64 step + 16 (l / 16)), codes of x from the L2.
 // Bound by the read of W (6144 x 6144, 4 tokens: 12.8 us for 37.7 MB, the
 // quantizer's launch included).
-// OWN (one token; four took 21.7 us there): x itself comes in, and every
-// workgroup rounds the whole row to codes in its LDS while its first weights are
-// on their way: one launch less, which is half of a small call (256 x 2048: 7.9
-// -> 4.7 us).
-template <int YT, int NT, bool OWN, int XT>
+// OWN: x itself comes in, and every workgroup rounds all of it to codes in its
+// LDS while its first weights are on their way: one launch less, which is half
+// of a small call (i8_own_codes).
+enum Own { kNoOwn, kOwnRow, kOwnRows };
+template <int YT, int NT, Own OWN, int XT>
 __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, const float* __restrict__ ws, int N,
                                                  int K, const void* __restrict__ x, const float* __restrict__ xs_in,
                                                  int T, const float* __restrict__ bias, void* __restrict__ y) {
   extern __shared__ __attribute__((aligned(16))) int8_t few_lds[];  // shares of the sum; OWN: then T rows of codes
-  __shared__ uint32_t red[kOwnTokens][16];
+  __shared__ uint32_t red[16];                                      // OWN: the waves' maxima, or the rows' scales
   int* part = reinterpret_cast<int*>(few_lds);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
   const int n0 = blockIdx.x * 16, r = lane & 15, g = lane >> 4;
@@ -160,35 +161,53 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
   if (wave * 256 < K) weights(wave * 256);
   const int8_t* xp[NT];
   float own = 0.0f;  // OWN: the scale of this lane's token
-  if constexpr (OWN) {
+  if constexpr (OWN == kOwnRow) {
     int8_t* codes = few_lds + nw * 1024;
-    uint32_t top[kOwnTokens] = {};
-    for (int t = 0; t < T; ++t)
-      for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
-        float v[8];
-        load8<XT>(x, (int64_t)t * K + c, v);
+    uint32_t top = 0;
+    for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
+      float v[8];
+      load8<XT>(x, c, v);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) top[t] = max(top[t], __float_as_uint(v[m]) & 0x7FFFFFFFu);
-      }
-#pragma unroll
-    for (int t = 0; t < kOwnTokens; ++t) {
-      const uint32_t w = wave_max_u32(top[t]);
-      if (lane == 0) red[t][wave] = w;
+      for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(v[m]) & 0x7FFFFFFFu);
+    }
+    top = wave_max_u32(top);
+    if (lane == 0) red[wave] = top;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) top = max(top, red[w]);
+    const RowScale s = row_scale_of(top);
+    own = s.s;
+    for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
+      float v[8];
+      load8<XT>(x, c, v);
+      *reinterpret_cast<uint2*>(codes + c) = codes8(v, s.step);
     }
     __syncthreads();
-    for (int t = 0; t < T; ++t) {
-      uint32_t m = 0;
-      for (int w = 0; w < nw; ++w) m = max(m, red[t][w]);
-      const RowScale s = row_scale_of(m);
-      if (t == min(r, T - 1)) own = s.s;
-      for (int c = 8 * tid; c < K; c += 8 * (int)blockDim.x) {
-        float v[8];
-        load8<XT>(x, (int64_t)t * K + c, v);
-        *reinterpret_cast<uint2*>(codes + t * K + c) = codes8(v, s.step);
+    xp[0] = codes + 16 * g;
+  } else if constexpr (OWN == kOwnRows) {
+    int8_t* codes = few_lds + nw * 1024;  // rows K + 16 bytes apart: the sixteen of a fragment in different banks
+    for (int t = wave; t < T; t += nw) {
+      float v[kOwnSteps][8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kOwnSteps; ++i) {
+        const int c = 8 * lane + 512 * i;
+        if (c < K) {
+          load8<XT>(x, (int64_t)t * K + c, v[i]);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(v[i][m]) & 0x7FFFFFFFu);
+        }
+      }
+      const RowScale s = row_scale_of(wave_max_u32(top));
+      if (lane == 0) red[t] = __float_as_uint(s.s);
+#pragma unroll
+      for (int i = 0; i < kOwnSteps; ++i) {
+        const int c = 8 * lane + 512 * i;
+        if (c < K) *reinterpret_cast<uint2*>(codes + t * (K + 16) + c) = codes8(v[i], s.step);
       }
     }
     __syncthreads();
-    xp[0] = codes + min(r, T - 1) * K + 16 * g;
+    own = __uint_as_float(red[min(r, T - 1)]);
+    xp[0] = codes + min(r, T - 1) * (K + 16) + 16 * g;
   } else {
 #pragma unroll
     for (int t = 0; t < NT; ++t) xp[t] = static_cast<const int8_t*>(x) + (int64_t)min(t * 16 + r, T - 1) * K + 16 * g;
@@ -215,7 +234,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const int8_t* __restrict__ W, c
     i32x4 sum{0, 0, 0, 0};
     for (int w = 0; w < nw; ++w) sum += *reinterpret_cast<const i32x4*>(part + ((w * NT + t) * 64 + lane) * 4);
     const int tok = t * 16 + r, n = n0 + 4 * g;
-    if (tok < T && n < N) put4<YT>(y, tok, N, n, sum, OWN ? own : xs_in[tok], ws, bias);
+    if (tok < T && n < N) put4<YT>(y, tok, N, n, sum, OWN != kNoOwn ? own : xs_in[tok], ws, bias);
   }
 }
 
@@ -382,15 +401,27 @@ int i8_shares(int N, int K, int T) {
 
 static int few_waves(int K) { return K <= 1024 ? 4 : K <= 4096 ? 8 : 16; }
 
-bool i8_own_codes(int T) { return T <= kOwnTokens; }
+// One token (256 channels of 2048 terms: 7.9 -> 4.7 us), or a few of rows that a
+// wave holds, where all workgroups together do not round too much (bf16 in, us
+// with the quantizer's launch and without: 2 x 256 x 256 5.5 and 3.7, 4 x 2048 x
+// 1024 6.8 and 5.1, 8 x 6144 x 2048 11.0 and 10.3; but 8 x 16384 x 2048 14.4 and
+// 18.7, 12 x 2048 x 1024 7.4 and 8.2).
+bool i8_own_codes(int N, int K, int T) {
+  return T == 1 || (T <= kOwnTokens && K <= 512 * kOwnSteps && (int64_t)N * T * K <= 1 << 27);
+}
 
 hipError_t launch_i8_own(const int8_t* W, const float* ws, int N, int K, const void* x, int xt, int T,
                          const float* bias, void* y, int yt, hipStream_t st) {
   const int nw = few_waves(K);
   const dim3 grid((N + 15) / 16), block(64 * nw);
-  const size_t lds = (size_t)nw * 1024 + (size_t)T * K;
-#define MD_OWN(Y_, X_)                                                                                             \
-  hipLaunchKernelGGL((k_i8_few<Y_, 1, true, X_>), grid, block, lds, st, W, ws, N, K, x, (const float*)nullptr, T, bias, y)
+  const size_t lds = (size_t)nw * 1024 + (T == 1 ? (size_t)K : (size_t)T * (K + 16));
+#define MD_OWNS(Y_, X_, O_)                                                                                       \
+  hipLaunchKernelGGL((k_i8_few<Y_, 1, O_, X_>), grid, block, lds, st, W, ws, N, K, x, (const float*)nullptr, T, bias, y)
+#define MD_OWN(Y_, X_)                    \
+  do {                                    \
+    if (T == 1) MD_OWNS(Y_, X_, kOwnRow); \
+    else MD_OWNS(Y_, X_, kOwnRows);       \
+  } while (0)
   if (yt == XF32) {
     if (xt == XF32) MD_OWN(XF32, XF32);
     else MD_OWN(XF32, XBF16);
@@ -399,6 +430,7 @@ hipError_t launch_i8_own(const int8_t* W, const float* ws, int N, int K, const v
     else MD_OWN(XBF16, XBF16);
   }
 #undef MD_OWN
+#undef MD_OWNS
   return hipGetLastError();
 }
 
@@ -409,9 +441,9 @@ static hipError_t matmul(const int8_t* W, const float* ws, int N, int K, const i
     const int nw = few_waves(K);
     const dim3 grid((N + 15) / 16), block(64 * nw);
     if (T <= 16)
-      hipLaunchKernelGGL((k_i8_few<YT, 1, false, XF32>), grid, block, (size_t)nw * 1024, st, W, ws, N, K, xq, xs, T, bias, y);
+      hipLaunchKernelGGL((k_i8_few<YT, 1, kNoOwn, XF32>), grid, block, (size_t)nw * 1024, st, W, ws, N, K, xq, xs, T, bias, y);
     else
-      hipLaunchKernelGGL((k_i8_few<YT, 2, false, XF32>), grid, block, (size_t)nw * 2048, st, W, ws, N, K, xq, xs, T, bias, y);
+      hipLaunchKernelGGL((k_i8_few<YT, 2, kNoOwn, XF32>), grid, block, (size_t)nw * 2048, st, W, ws, N, K, xq, xs, T, bias, y);
     return hipGetLastError();
   }
   auto tiles = [&](int bn, int bt) { return (int64_t)((N + bn - 1) / bn) * ((T + bt - 1) / bt); };

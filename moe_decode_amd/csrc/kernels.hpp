@@ -196,7 +196,7 @@ hipError_t launch_combine(const float* o, const int* pos_of_pair, const float* g
 hipError_t launch_i8_quantize(const void* x, int xt, int T, int K, int8_t* codes, float* scales, hipStream_t st);
 hipError_t launch_i8_matmul(const int8_t* W, const float* ws, int N, int K, const int8_t* xq, const float* xs, int T,
                             const float* bias, void* y, int yt, int* part, hipStream_t st);
-bool i8_own_codes(int T);  // so few tokens that launch_i8_own takes x itself
+bool i8_own_codes(int N, int K, int T);  // so few tokens that launch_i8_own takes x itself
 hipError_t launch_i8_own(const int8_t* W, const float* ws, int N, int K, const void* x, int xt, int T,
                          const float* bias, void* y, int yt, hipStream_t st);
 int i8_shares(int N, int K, int T);  // shares of the sum: part holds shares * T * (N rounded up to 4) int32

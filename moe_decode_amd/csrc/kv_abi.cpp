@@ -226,7 +226,7 @@ md_status md_i8_linear_workspace_size(const md_qmatrix* W, int32_t T, size_t* by
   const md_status s = check_i8(W, T);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
-  *bytes = T && !md::i8_own_codes(T) ? codes_bytes(T, W->cols) + scales_bytes(T) + shares_bytes(W, T) : 0;
+  *bytes = T && !md::i8_own_codes(W->rows, W->cols, T) ? codes_bytes(T, W->cols) + scales_bytes(T) + shares_bytes(W, T) : 0;
   return ok();
 }
 
@@ -240,7 +240,7 @@ md_status md_i8_linear(const md_qmatrix* W, const void* x, int32_t xtype, int32_
   if ((s = check_device("x", x)) != MD_OK || (s = check_device("y", y)) != MD_OK ||
       (bias && (s = check_device("bias", bias)) != MD_OK))
     return s;
-  if (md::i8_own_codes(T)) {
+  if (md::i8_own_codes(W->rows, W->cols, T)) {
     const hipError_t e = md::launch_i8_own(static_cast<const int8_t*>(W->q), W->row_scale, W->rows, W->cols, x, xtype, T,
                                            bias, y, ytype, stream);
     return e == hipSuccess ? ok() : hip_fail(e, "i8 linear launch");

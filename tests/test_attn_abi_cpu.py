@@ -46,12 +46,13 @@ def test_i8_errors():
     ws, lin = L.md_i8_linear_workspace_size, L.md_i8_linear
     assert _st(ws(_w(), 4, None)) == "MD_ERR_INVALID_ARG"
     assert ws(_w(), 0, ctypes.byref(sz)) == 0 and sz.value == 0
-    assert ws(_w(), 5, ctypes.byref(sz)) == 0 and sz.value == 5 * 256 + 256
-    assert _st(lin(_w(), FAKE, 0, 5, None, FAKE, 0, FAKE, sz.value - 1, None)) == "MD_ERR_WORKSPACE"
-    assert _st(lin(_w(), FAKE, 0, 5, None, FAKE, 0, None, sz.value, None)) == "MD_ERR_WORKSPACE"
-    assert _st(lin(_w(), FAKE, 0, 5, None, FAKE, 0, ODD, sz.value, None)) == "MD_ERR_ALIGNMENT"
-    assert _st(lin(_w(), FAKE, 5, 5, None, FAKE, 0, FAKE, sz.value, None)) == "MD_ERR_INVALID_ARG"
-    assert _st(lin(_w(), None, 0, 5, None, FAKE, 0, FAKE, sz.value, None)) == "MD_ERR_INVALID_ARG"
+    assert ws(_w(), 5, ctypes.byref(sz)) == 0 and sz.value == 0          # the codes stay in the workgroups
+    assert ws(_w(), 17, ctypes.byref(sz)) == 0 and sz.value == 17 * 256 + 256
+    assert _st(lin(_w(), FAKE, 0, 17, None, FAKE, 0, FAKE, sz.value - 1, None)) == "MD_ERR_WORKSPACE"
+    assert _st(lin(_w(), FAKE, 0, 17, None, FAKE, 0, None, sz.value, None)) == "MD_ERR_WORKSPACE"
+    assert _st(lin(_w(), FAKE, 0, 17, None, FAKE, 0, ODD, sz.value, None)) == "MD_ERR_ALIGNMENT"
+    assert _st(lin(_w(), FAKE, 5, 17, None, FAKE, 0, FAKE, sz.value, None)) == "MD_ERR_INVALID_ARG"
+    assert _st(lin(_w(), None, 0, 17, None, FAKE, 0, FAKE, sz.value, None)) == "MD_ERR_INVALID_ARG"
 
 
 def _c(n=8, page=64, heads=2, dim=128, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE):

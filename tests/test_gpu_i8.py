@@ -87,6 +87,7 @@ def _product(x, w, ws, b, out):
 # the last token counts of a launch shape and the first of the next, and widths around a tile's
 SHAPES = [(1, 1, 256), (1, 256, 2048), (2, 17, 512), (3, 40, 16384), (4, 20, 16384), (4, 100, 6144), (5, 50, 16384), (15, 33, 1024), (16, 64, 1280), (17, 31, 256), (32, 100, 4352),
           (33, 48, 768), (64, 130, 2048), (65, 64, 512), (100, 200, 768), (127, 65, 256), (128, 1500, 256),
+          (2, 15, 256), (7, 33, 768), (8, 70, 2048), (9, 40, 2048), (8, 90, 2304), (8, 8192, 2048), (8, 8193, 2048),
           (129, 129, 1024), (300, 1000, 512), (70, 64, 4096), (500, 100, 2048), (1000, 1111, 256), (2100, 2049, 256)]
 
 
