@@ -510,9 +510,10 @@ md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*hos
  * head) is rounded to integers of its largest magnitude / 8355704 (bf16 out:
  * / 32638), a softmax weight to integers of 1 / 8355711 (1 / 32639) of the
  * largest weight among its workgroup's tokens so far.  In the form for many (over
- * 64 columns, max_q * q_heads / kv_heads; fp32 out of 256 channels: over 512 on
- * at most 2560 positions) a query's channel and a weight (times its page's value scale) are rounded to 22
- * bits (bf16 out: 11).  A non-finite q makes its own row and head NaN; so does a
+ * 64 columns, max_q * q_heads / kv_heads; fp32 out of 256 channels: over 768) a
+ * query's channel and a weight (times its page's value scale) are rounded to 22
+ * bits (bf16 out: 11, and weights below 2^-21 of the row's largest to steps of
+ * 2^-31 of it).  A non-finite q makes its own row and head NaN; so does a
  * page whose scale is not in 0..2^126 for the rows that see it.
  * Long sequences are split over workgroups and joined by a second kernel (few
  * columns: all tiles of the batch are dealt out evenly, following the lengths on

@@ -64,7 +64,7 @@ MD_DEV Span span_of(const KvAttn& a, const Seq& q, int c0, int c1) {
 // at once, two on a compute unit, the second half goes the other way round and
 // each unit gets a heavy and a light one (4096 new of 5003 tokens, 16 heads on 4
 // of 128 channels: 165 us against 166 heaviest first throughout and 187 in the
-// heads' order, on a kernel that takes 157 now).
+// heads' order, on a kernel that takes 149 now).
 MD_DEV int column_tile(const KvAttn& a, int b, int n) {
   if (!a.causal) return b;
   const int half = (n + 1) / 2;

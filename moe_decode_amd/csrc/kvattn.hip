@@ -491,20 +491,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 // they run on the f16 matrix cores, which accumulate in fp32 and need no joins:
 // the codes are exact in f16 (converted once per workgroup on their way to
 // LDS), a query row is scaled by a power of two to below 2^14 and rounded to
-// f16, and so is a weight p times 2^14 vs / R, R the power of two at or below
-// the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second f16
-// for what the first one leaves, 22 bits together.  Per score that leaves half a
+// f16, and so is a weight p times a unit times vs / R, R the power of two at or
+// below the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second
+// f16 for what the first one leaves, 22 bits together, and the unit 2^14, which
+// keeps both parts of weights down to 2^-18 whole.  NS = 1: a row's reference
+// follows its maximum only where that has grown by 2^7, so p stays below 2^7 and
+// the unit is 2^7 (a weight below 2^-21 loses bits, 2^-32 at most); without that
+// some column's maximum moves in most tiles and the sums are rescaled there
+// (4096 new of 5003 tokens: 160 us, 156).  Per score that leaves half a
 // maximum, one fma, one exp2 (a quarter of the rate), the sum and half a
 // conversion on the vector ALU.
 //
 // Measured: 4096 new of 5003 tokens, 16 heads on 4 of 128 channels, bf16 out,
-// 157 us (99 GFlop, 0.63 Pflop/s; the int8 form's digits and joins 296).  Every
+// 149 us (99 GFlop, 0.66 Pflop/s; the int8 form's digits and joins 296).  Every
 // wave reads all of a tile's 32 KB from LDS, at 64 bytes a clock and compute
 // unit half of that time and twice what the products take; the softmax's vector
-// work stands between the two products, and two waves a SIMD overlap the rest
-// only in part.  Measured
-// and dropped: the next tile's first product beside this one's softmax (187 to
-// 196, registers), one wave a SIMD (307), wave priorities (162 to 164).
+// work (a third of the waves' time) stands between the two products, and two waves
+// a SIMD overlap these only in part.  Measured
+// and dropped, when it took 157: the next tile's first product beside this one's
+// softmax (187 to 196, registers), one wave a SIMD (307), wave priorities (162 to
+// 164).
 //
 // 32 x 32 tiles: score row 8 a + 4 hh + b of a 32-token block is its token
 // 16 hh + 4 a + b, so lane half hh holds tokens 16 hh .. 16 hh + 15 and feeds
@@ -526,9 +532,26 @@ MD_DEV uint2 codes_f16(uint32_t w) {
 
 constexpr int kRowCols = 128;  // columns of a workgroup
 
+// Schedules a block of N LDS reads that feed NS matrix instructions each with
+// four reads in flight; left to itself the compiler waits for every read right
+// after it (4096 new of 5003 tokens, 128 channels: 152 -> 149 us, 2048 of 2048 of
+// 4 sequences, 64 channels: 67 -> 62).
+template <int N, int NS, int GROUP>
+MD_DEV void paced() {
+  constexpr int kAhead = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, GROUP);
+#pragma unroll
+  for (int i = 0; i < N - kAhead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, NS, GROUP);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, GROUP);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kAhead * NS, GROUP);
+}
+
 template <int D, int NS>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a) {
   constexpr int KS = D / 16, DT = D / 32;
+  constexpr float kLag = NS == 1 ? 7.0f : 0.0f, kUnit = NS == 1 ? 128.0f : 16384.0f;
   constexpr int L = kTile * D / 16 / 256;  // 16-byte chunks of codes per thread, keys or values
   __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kTile * D], s_v[2][kTile * D];
   const KvCache& c = a.c;
@@ -642,7 +665,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   for (int n = 0; n < DT; ++n)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[n][i] = 0.0f;
-  int ex_r = 1;  // acc is in steps of R / 2^14, R = 2^(ex_r - 127)
+  int ex_r = 1;  // acc is in steps of R / kUnit, R = 2^(ex_r - 127)
 
   Scales sc{};
   if (t_begin < t_end) {
@@ -656,17 +679,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
     if (any && t < mine.t1 && t >= mine.t0) {
       f32x16 x[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int tok = 32 * b + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int tok = 32 * b + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
           const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][kslot(tok, 2 * k + hh)]);
 #pragma unroll
           for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
         }
-      }
+      paced<2 * KS, NS, 0>();
       const int base = t * kTile, first = base + 16 * hh;
       if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
         keep_branch();
@@ -685,13 +710,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
       if (raw > -INFINITY) l += sc.off;
       raw = fmaxf(raw, xor_lanes<32>(raw)) * f;
       if (raw == INFINITY) l = nan_f();
-      const float m1 = fmaxf(m, raw), ref = m1 > -INFINITY ? m1 : 0.0f;
+      const float m1 = raw > m + kLag ? raw : m, ref = m1 > -INFINITY ? m1 : 0.0f;
       const float alpha = __builtin_amdgcn_exp2f(m - ref);
       m = m1;
       // R is a power of two, so both factors are exact
       const int e1 = max(ex_r, (int)(__float_as_uint(sc.vs) >> 23));
       const float down = __uint_as_float((uint32_t)max(127 + ex_r - e1, 0) << 23);
-      const float w = sc.vs * __uint_as_float((uint32_t)(254 - e1) << 23) * 16384.0f;
+      const float w = sc.vs * __uint_as_float((uint32_t)(254 - e1) << 23) * kUnit;
       ex_r = e1;
       f16x8 pf[NS][4];
       float sum = 0.0f;
@@ -728,6 +753,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
           for (int e = 0; e < NS; ++e) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[e][k], acc[n], 0, 0, 0);
         }
       }
+      paced<4 * DT, NS, 1>();
     }
     if (t + 1 < t_end) {
       stage(buf ^ 1);
@@ -739,7 +765,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   l += xor_lanes<32>(l);
   if (c0 + col >= cols) return;
   const int64_t orow = (int64_t)q.row0 + qt;
-  const float unit = __uint_as_float((uint32_t)ex_r << 23) * (1.0f / 16384.0f);
+  const float unit = __uint_as_float((uint32_t)ex_r << 23) * (1.0f / kUnit);
   if (active == 1) {
     const float inv = l == 0.0f ? 0.0f : unit / l;
 #pragma unroll
@@ -861,11 +887,11 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int c
   // More than four column tiles: the form that shares its loads among 128
   // columns (80 columns, 16 sequences of 4000: 41 us, 51 in the other one; 64:
   // 41 both).  fp32 outputs of 256 channels do not fit its registers, so there
-  // it is kept for columns by the hundreds on short sequences (8 of 256 new in
-  // 2048 tokens: 357 us against 412; 2048 in 4096: 747 against 480).
+  // it is kept for columns by the hundreds (us here and in the other one: 240
+  // columns, 4 sequences of 1000: 53 and 26; 600, 4 of 8000: 197 and 167; 1000,
+  // one of 30000: 235 and 308; 8192, one of 4096: 405 and 446).
   const int64_t cols = (int64_t)b.max_q * G;
-  const bool tight = c.D == 256 && yt == XF32;
-  p.tile = cols > (tight ? 512 : 64) && !(tight && most > 2560) ? kRowCols : 16;
+  p.tile = cols > (c.D == 256 && yt == XF32 ? 768 : 64) ? kRowCols : 16;
   p.splits = 1;
   p.chunk = (int)tiles;
   if (p.tile == 16) {

@@ -94,7 +94,7 @@ def attention(q, k, v, scale, causal, window, out, many=False):
     sums.  A query's channel and a weight are off relatively by c = 2^-12 (bf16
     outputs), or 2^-23 where a second f16 holds the first one's remainder (13 of
     24 bits, rounded to 11), with floors (2^-25 of 2^14) that the weights show
-    as n 2^-38 max |v|; a sum of D products is off by D u of its terms' sizes, one
+    as n 2^-38 max |v| (bf16 outputs: of 2^7, n 2^-31 max |v|); a sum of D products is off by D u of its terms' sizes, one
     of n weights by n u."""
     n, Hq, D = q.shape
     L, Hkv = k.shape[0], k.shape[1]
@@ -121,18 +121,14 @@ def attention(q, k, v, scale, causal, window, out, many=False):
                 c = 2.0 ** -12 if out == "bf16" else 2.0 ** -23
                 ds = A * (c + D * u) + 24 * u * np.abs(s).max()
                 chain += c + (hi - lo) * u
-                grid = (hi - lo) * 2.0 ** -38 * np.abs(vv).max(0) / e.sum()
+                grid = (hi - lo) * 2.0 ** (-31 if out == "bf16" else -38) * np.abs(vv).max(0) / e.sum()
             tol[i, h] = 1.05 * (2 * (ds + 4 * u + chain) * V + grid) + HALF[out] * np.abs(o[i, h]) + 1e-37
     return o, tol
 
 
-def many_columns(max_q, G, D, max_kv, window, out):
-    """Which of the two forms a call takes (causal, where a window is given)."""
-    if window:
-        max_kv = min(max_kv, window + max_q)
-    if D == 256 and out == "f32":
-        return max_q * G > 512 and max_kv <= 2560
-    return max_q * G > 64
+def many_columns(max_q, G, D, out):
+    """Which of the two forms a call takes."""
+    return max_q * G > (768 if D == 256 and out == "f32" else 64)
 
 
 class Pages:

@@ -224,6 +224,8 @@ ATTN = [  # key heads, group, dim, page, (new, length) of each sequence, causal,
     (2, 4, 128, 64, [(12, 5), (5, 300)], True, 2 ** 31 - 1),                # windows past every position, and runs
     (1, 4, 64, 64, [(200, 90), (3, 64)], True, 2 ** 31 - 1),                # that begin before the first one
     (2, 4, 64, 64, [(9, 100), (2, 100)], True, 100),
+    (1, 8, 256, 64, [(100, 700), (3, 90)], True, 0),
+    (1, 8, 256, 128, [(110, 3000)], True, 500),
 ]
 
 
@@ -249,7 +251,7 @@ def test_attention(case, xt, out):
     worst = 0.0
     for i, (a, b) in enumerate(seqs):
         want, tol = attention(qn[at:at + a], m.values("k", table[i], b), m.values("v", table[i], b), scale, causal,
-                              window, out, many=many_columns(max(nq), G, dim, max(lens), window, out))
+                              window, out, many=many_columns(max(nq), G, dim, out))
         err = np.abs(got[at:at + a] - want)
         assert (err <= tol).all(), (i, float((err / tol).max()))
         worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()) if a else 0.0)
@@ -423,6 +425,28 @@ def test_scales_far_apart_and_large_scores():
             want, tol = attention(qn, m.values("k", table[0], 300), m.values("v", table[0], 300), scale, True, 0,
                                   "f32", many=max_q == 40)
             assert (np.abs(y - want) <= tol).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("grow", [0.3, 2.0, 30.0])
+def test_maxima_that_grow(out, many, grow):
+    """Keys that get larger from page to page, so that a row's largest score keeps
+    rising by a little or a lot, and then smaller again."""
+    import moe_decode_amd as md
+    Hkv, G, dim, page, n = 2, 2, 64, 64, 12
+    rng = np.random.default_rng(91)
+    m = Cache(n, Hkv, page, dim, rng)
+    up = np.minimum(np.arange(n), 16 - np.arange(n)) + 1
+    m.s["k"][:] = (grow / 127 * up)[:, None].astype(np.float32)
+    m.s["v"][:] = np.float32(0.01)
+    c = _to_gpu(m)
+    q, qn = _rn(rng, (5, Hkv * G, dim), "bf16")
+    got = md.kv_attention(c, _batch([5], [n * page - 3], [list(range(n))], max_q=40 if many else 5), q, out_dtype=_dt(out))
+    want, tol = attention(qn, m.values("k", range(n), n * page - 3), m.values("v", range(n), n * page - 3), dim ** -0.5,
+                          True, 0, out, many=many)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
 
 
 # ---- copies, and all of it together --------------------------------------------
