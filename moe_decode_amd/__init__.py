@@ -516,17 +516,26 @@ def _raw_stream(index):
     return _raw_stream(index)
 
 
+def _current_device():
+    """torch.cuda.current_device(), less its check that the GPU is initialised
+    (the tensors are there)."""
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
+
+
 class _on:
     """The device of a call's tensors made current, and its stream's handle."""
     __slots__ = ("back", "stream")
 
     def __init__(self, device, stream):
-        import torch
         if device.type != "cuda":
             raise ValueError(f"tensors on a GPU wanted, got {device}")
-        now, want = torch.cuda.current_device(), device.index
+        now, want = _current_device(), device.index
         self.back = None
         if want is not None and want != now:
+            import torch
             self.back = now
             torch.cuda.set_device(want)
             now = want
@@ -544,24 +553,23 @@ class _on:
 def _i8_desc(W, device=None):
     """The C descriptor of an int8 matrix, made once while its tensors stay;
     they have to hold the matrix and lie on `device`."""
-    import torch
-    d, q, sc = W.__dict__.get("_i8"), W.q.data_ptr(), _ptr(W.row_scale)
-    if d is None or d.q != q or d.row_scale != sc:
+    made, r = W.__dict__.get("_i8"), W.row_scale
+    key = (W.q.data_ptr(), None if r is None else r.data_ptr(), W.rows, W.cols, W.type, W.count)
+    if made is None or made[0] != key:
+        import torch
         if W.count != 1:
             raise ValueError(f"one matrix wanted, got a stack of {W.count}")
         if W.type == I8_ROW:
-            r = W.row_scale
             if not W.q.is_contiguous() or W.q.numel() * W.q.element_size() < W.rows * W.cols:
                 raise ValueError(f"W.q: {W.rows} x {W.cols} bytes wanted, got {tuple(W.q.shape)} of {W.q.dtype}")
             if r is not None and (r.dtype != torch.float32 or not r.is_contiguous() or r.numel() < W.rows
                                   or r.device != W.q.device):
                 raise ValueError(f"W.row_scale: {W.rows} float32 values on {W.q.device} wanted, got "
                                  f"{tuple(r.shape)} of {r.dtype} on {r.device}")
-        d = W._i8 = W.desc()
-        W._i8_ref, W._i8_dev = ctypes.byref(d), W.q.device
-    if device is not None and W._i8_dev != device:
-        raise ValueError(f"W is on {W._i8_dev}, the call's tensors on {device}")
-    return W._i8_ref
+        made = W._i8 = (key, ctypes.byref(W.desc()), W.q.device)
+    if device is not None and made[2] != device:
+        raise ValueError(f"W is on {made[2]}, the call's tensors on {device}")
+    return made[1]
 
 
 def i8_quantize(x, codes=None, scales=None, stream=None):
@@ -619,10 +627,10 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
         L, d = lib(), _i8_desc(W, dev)
         ws, wsb = None, 0
         if T > 1:
-            need = ctypes.c_size_t(0)
-            _check(L.md_i8_linear_workspace_size(d, T, ctypes.byref(need)))
-            if need.value:
-                ws, wsb = _workspace(need.value, dev, workspace)
+            made, key = W.__dict__.get("_i8_need"), (W.rows, W.cols, T)
+            if made is None or made[0] != key:  # the last call's answer: the size follows from these alone
+                made = W._i8_need = (key, i8_linear_workspace_size(W, T))
+            ws, wsb = _workspace(made[1], dev, workspace)
         _check(L.md_i8_linear(d, x.data_ptr(), _xtype(x.dtype), T, _ptr(bias), y.data_ptr(), _xtype(y.dtype), _ptr(ws),
                               wsb, st))
     return y
@@ -684,7 +692,7 @@ class KVBatch:
         self.max_q, self.max_kv, self.device = max_q, max_kv, dev
         self._desc = KVBatchDesc(S, 0, max_q, max_kv, table.shape[1], q_start.data_ptr(), kv_len.data_ptr(),
                                  table.data_ptr())
-        self._made = (-1, None)
+        self._made, self._need = (-1, None), (None, 0)
 
     def desc(self, rows):
         """The C descriptor for a call on `rows` rows: the last one again, or a
@@ -740,10 +748,14 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
             raise ValueError(f"out has {out.shape[0]} rows, q {rows}")
         os_ = _rows("out", out, heads, cache.head_dim, cache.device)
         L, d, yt = lib(), batch.desc(rows), _xtype(out.dtype)
-        need = ctypes.c_size_t(0)
-        _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
-                                                ctypes.byref(need)))
-        ws, wsb = _workspace(need.value, cache.device, workspace)
+        key = (cache.page, cache.kv_heads, cache.head_dim, rows, heads, causal, window, yt)
+        made = batch._need  # the last call's answer: the size follows from these alone
+        if made[0] != key:
+            need = ctypes.c_size_t(0)
+            _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
+                                                    ctypes.byref(need)))
+            made = batch._need = (key, need.value)
+        ws, wsb = _workspace(made[1], cache.device, workspace)
         _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
                                  dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws),
                                  wsb, st))
