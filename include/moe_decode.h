@@ -508,13 +508,17 @@ md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*hos
  * Accuracy: the cache's codes enter exactly, sums of integers are exact or in
  * fp32, and everything else is fp32.  In the form for few columns a query row (one
  * head) is rounded to integers of its largest magnitude / 8355704 (bf16 out:
- * / 32638), a softmax weight to integers of 1 / 8355711 (1 / 32639) of the
- * largest weight among its workgroup's tokens so far.  In the form for many (over
- * 64 columns, max_q * q_heads / kv_heads; fp32 out of 256 channels: over 768) a
- * query's channel and a weight (times its page's value scale) are rounded to 22
- * bits (bf16 out: 11, and weights below 2^-21 of the row's largest to steps of
- * 2^-31 of it).  A non-finite q makes its own row and head NaN; so does a
- * page whose scale is not in 0..2^126 for the rows that see it.
+ * / 32638), a softmax weight to integers of 1 / 8355711 of the largest weight
+ * among its tile (the row's tokens at positions 64 n .. 64 n + 63); the weights'
+ * total is taken before that.  The weights' rounding moves an output by at most
+ * 4e-6 of the largest magnitude among the values that the row sees, however long
+ * the context is.  In the form for many (over 64 columns, max_q * q_heads /
+ * kv_heads; fp32 out of 256 channels: over 768) a query's channel and a weight
+ * (times its page's value scale) are rounded to 22 bits (bf16 out: 11, and weights
+ * below 2^-21 of the row's largest to steps of 2^-31 of it).  A non-finite q makes
+ * its own row and head NaN; so does a page whose scale is not in 0..2^126 for the
+ * rows that see it.  Scores have to stay within fp32's range: those past it give
+ * NaN, or weights of 0.
  * Long sequences are split over workgroups and joined by a second kernel (few
  * columns: all tiles of the batch are dealt out evenly, following the lengths on
  * the device); the order of every sum is fixed, so the same batch gives the same

@@ -5,12 +5,20 @@
 //
 // Two forms, by the number of (query, head) columns that share a key head: for
 // many of them see k_kv_attn_rows; for few, both products run on the int8 matrix
-// cores with the cache's codes as they lie in memory.  The other operand is split into balanced base-256 digits: a
-// query row (one token, one head) as integers of 2^-23 of its largest
-// magnitude (three digits; two for bf16 outputs: 2^-15), a softmax weight
-// p in [0, 1] as integers of 2^-23 (2^-15).  Every digit's sum is exact in
-// int32, so what is rounded is q, p, the joins of the digits and the softmax's
-// fp32 arithmetic.
+// cores with the cache's codes as they lie in memory.  The other operand is split
+// into balanced base-256 digits: a query row (one token, one head) as integers of
+// 2^-23 of its largest magnitude (three digits; two for bf16 outputs: 2^-15), a
+// softmax weight as integers of 2^-23 of the largest one among its tile of 64
+// tokens.  Every digit's sum is exact in int32, so what is rounded is q, p, the
+// joins of the digits and the softmax's fp32 arithmetic.
+//
+// The weights' reference is the tile's own maximum, brought to the running one by
+// a factor in fp32, and they have three digits whatever the output's type: the
+// integers are steps of one size, so a weight far below the reference loses its
+// bits, and where one key holds most of a row's weight (the first token, often)
+// the rest of it is a long tail of such weights.  A tail of 2047 tokens beside a
+// key of 0.97 of the weight, bf16 out: 0.2% off the definition (the output's
+// rounding); 5% against the running maximum with two digits, one of 8191 24%.
 //
 // Operand layout.  Keys enter as the A operand (rows = tokens), queries as B
 // (columns = (query, head) pairs that share the key head), so the scores come
@@ -39,7 +47,7 @@ template <int ND>
 struct Digits;
 // q: |n| <= top, n + bias in bytes, digit = byte ^ 0x80; rows are scaled to
 // qtop, since the fp32 factor and product may come out up to one integer
-// higher, and one past top would wrap every digit.  p: 0 <= n <= top,
+// higher, and one past top would wrap every digit.  p (kWeightDigits): 0 <= n <= top,
 // top + pbias = 2^(8 ND - 1) - 1, so that one fma with 2^23 + pbias leaves the
 // biased digits in the low bytes of the sum's bit pattern (the highest digit
 // unbiased, 0..127).
@@ -50,9 +58,10 @@ struct Digits<3> {
 };
 template <>
 struct Digits<2> {
-  static constexpr float top = 32639.0f, qtop = 32638.0f;
-  static constexpr int bias = 0x8080, pbias = 0x80;
+  static constexpr float qtop = 32638.0f;
+  static constexpr int bias = 0x8080;
 };
+constexpr int kWeightDigits = 3;
 
 // Byte k of four integers, as one dword, for every digit k < ND.
 template <int ND>
@@ -154,54 +163,51 @@ MD_DEV Scales scales_of(float ks, float vs) {
 }
 
 // One tile's raw scores masked (where it is cut), the running maximum moved:
-// returns the factor of a raw score and the reference, and alpha for what has
-// been summed so far.
-template <int D, int ND, int N>
-MD_DEV float advance(Column<D, ND>& o, float (&x)[N], const float (&f)[N / 16], const float (&off)[N / 16], bool cut,
-                     int first, float& ref) {
-  float top = -INFINITY;
+// returns alpha for what has been summed so far, beta for what the tile's weights
+// give, and ref, the tile's own maximum, which they are relative to.
+template <int D, int ND>
+MD_DEV float advance(Column<D, ND>& o, float (&x)[16], float f, float off, bool cut, int first, float& ref,
+                     float& beta) {
+  if (cut) {
+    keep_branch();
 #pragma unroll
-  for (int t = 0; t < N / 16; ++t) {
-    if (cut) {
-      keep_branch();
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (first + 64 * t + i > o.hi || first + 64 * t + i < o.lo) x[16 * t + i] = -INFINITY;
-    }
-    float raw = x[16 * t];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) raw = fmaxf(raw, x[16 * t + i]);
-    if (raw > -INFINITY) o.l += off[t];
-    top = fmaxf(top, raw * f[t]);
+    for (int i = 0; i < 16; ++i)
+      if (first + i > o.hi || first + i < o.lo) x[i] = -INFINITY;
   }
+  float raw = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) raw = fmaxf(raw, x[i]);
+  if (raw > -INFINITY) o.l += off;
+  float top = raw * f;
   top = fmaxf(top, xor_lanes<16>(top));
   top = fmaxf(top, xor_lanes<32>(top));
   if (top == INFINITY) o.l = nan_f();
-  const float m1 = fmaxf(o.m, top);
-  ref = m1 > -INFINITY ? m1 : 0.0f;
-  const float alpha = __builtin_amdgcn_exp2f(o.m - ref);
+  ref = top > -INFINITY ? top : 0.0f;  // a tile that the column does not see: weights of 0
+  const float m1 = fmaxf(o.m, top), run = m1 > -INFINITY ? m1 : 0.0f;
+  const float alpha = __builtin_amdgcn_exp2f(o.m - run);
+  beta = __builtin_amdgcn_exp2f(top - run);
   o.m = m1;
   return alpha;
 }
 
-// Sixteen raw scores to softmax weights and their digits.  The fused product
-// and subtraction may leave the largest one just above 0, so the weight is
-// clamped to 1 (a digit past the top would wrap).
-template <int ND>
-MD_DEV float weights(const float* x, float f, float ref, float scale, i32x4 (&pd)[ND]) {
+// Sixteen raw scores to softmax weights and their digits, and the weights' sum.
+// The fused product and subtraction may leave the largest one just above 0, so the
+// weight is clamped to 1 (a digit past the top would wrap).
+MD_DEV float weights(const float (&x)[16], float f, float ref, i32x4 (&pd)[kWeightDigits]) {
+  using P = Digits<kWeightDigits>;
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t n[4], d[ND];
+    uint32_t n[4], d[kWeightDigits];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float p = __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(fmaf(x[4 * j + r], f, -ref)), 0.0f, 1.0f);
       sum += p;
-      n[r] = __float_as_uint(fmaf(p, scale, 8388608.0f + (float)Digits<ND>::pbias));
+      n[r] = __float_as_uint(fmaf(p, P::top, 8388608.0f + (float)P::pbias));
     }
-    bytes4<ND>(n[0], n[1], n[2], n[3], d);
+    bytes4<kWeightDigits>(n[0], n[1], n[2], n[3], d);
 #pragma unroll
-    for (int e = 0; e < ND; ++e) pd[e][j] = (int)(e < ND - 1 ? d[e] ^ 0x80808080u : d[e]);
+    for (int e = 0; e < kWeightDigits; ++e) pd[e][j] = (int)(e < kWeightDigits - 1 ? d[e] ^ 0x80808080u : d[e]);
   }
   return sum;
 }
@@ -335,22 +341,22 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
       load_k(t + kWaves, page);
       ks = c.k_scale[(int64_t)page * c.Hkv + h];
       vs = c.v_scale[(int64_t)page * c.Hkv + h];
-      const float f[1] = {fmaxf(o.qscale * sc.ks, 1e-37f)}, off[1] = {sc.off};
-      float ref;
+      const float f = fmaxf(o.qscale * sc.ks, 1e-37f);
+      float ref, beta;
       const int base = t * kTile;
-      const float alpha = advance<D, ND, 16>(o, x, f, off, base + kTile - 1 > sp.full_hi || base < sp.full_lo,
-                                             base + 16 * g, ref);
-      i32x4 pd[ND];
-      o.l = fmaf(o.l, alpha, weights<ND>(x, f[0], ref, Digits<ND>::top, pd));
-      const float fv = sc.vs * (1.0f / Digits<ND>::top);
+      const float alpha = advance<D, ND>(o, x, f, sc.off, base + kTile - 1 > sp.full_hi || base < sp.full_lo,
+                                         base + 16 * g, ref, beta);
+      i32x4 pd[kWeightDigits];
+      o.l = fmaf(beta, weights(x, f, ref, pd), o.l * alpha);
+      const float fv = sc.vs * (1.0f / Digits<kWeightDigits>::top) * beta;
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        i32x4 d[ND];
+        i32x4 d[kWeightDigits];
 #pragma unroll
-        for (int e = 0; e < ND; ++e)
+        for (int e = 0; e < kWeightDigits; ++e)
           d[e] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vf[i], pd[e], i32x4{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(join<ND>(d, r), fv, acc[i][r] * alpha);
+        for (int r = 0; r < 4; ++r) acc[i][r] = fmaf(join<kWeightDigits>(d, r), fv, acc[i][r] * alpha);
         if (i & 1) __builtin_amdgcn_sched_barrier(0);
       }
       load_v(t + kWaves, page);
