@@ -4,6 +4,10 @@ Every computation runs in the HIP library.  PyTorch supplies device memory
 and the current stream; this module only packs descriptors, allocates
 workspaces with torch, and turns error codes into exceptions.  There is no
 fallback: if the library is missing, importing the binding's functions raises.
+
+A call runs on the current stream, or on `stream`: then what it allocates is
+that stream's memory, and the caller has other streams wait for it before they
+read its outputs.
 """
 import ctypes
 import os
@@ -138,14 +142,36 @@ def _stream(stream):
     return s.cuda_stream
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, stream=None):
+    """The workspace of a call on `stream` (None: the current one).  One made
+    here is released when the call returns, while its kernels still run, so it
+    has to be of their stream's memory: what is made there next runs after them."""
     import torch
     if nbytes == 0:
         return None, 0
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws, nbytes
+
+
+def _result(stream, make, *args, **kw):
+    """make(*args, **kw): an output of a call on `stream` (None: the current
+    one), of that stream's memory like the workspace.  The caller has the stream
+    that is current now wait for the call and reads the output there, so its
+    memory is not given out again before what that stream holds when it is
+    released."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def row_bytes(type_, cols):
@@ -198,10 +224,10 @@ def qgemv(W, x, y=None, workspace=None, stream=None):
     batch = x.shape[0] if x.dim() == 2 else 1
     xt = X_BF16 if x.dtype == torch.bfloat16 else X_F32
     if y is None:
-        y = torch.empty(batch, W.rows, dtype=torch.float32, device=x.device)
+        y = _result(stream, torch.empty, batch, W.rows, dtype=torch.float32, device=x.device)
     need = ctypes.c_size_t(0)
     _check(L.md_qgemv_workspace_size(ctypes.byref(d), batch, ctypes.byref(need)))
-    ws, wsb = _workspace(need.value, x.device, workspace)
+    ws, wsb = _workspace(need.value, x.device, workspace, stream)
     _check(L.md_qgemv(ctypes.byref(d), _ptr(x), xt, batch, _ptr(y), _ptr(ws), wsb, _stream(stream)))
     return y
 
@@ -217,9 +243,9 @@ def moe_route_topk(x, Wr, bias, k, idx=None, gates=None, logits=None, workspace=
     T, H = x.shape
     E = Wr.shape[0]
     dev = x.device
-    idx = torch.empty(T, k, dtype=torch.int32, device=dev) if idx is None else idx
-    gates = torch.empty(T, k, dtype=torch.float32, device=dev) if gates is None else gates
-    ws, wsb = _workspace(route_workspace_size(T, H, E, k), dev, workspace)
+    idx = _result(stream, torch.empty, T, k, dtype=torch.int32, device=dev) if idx is None else idx
+    gates = _result(stream, torch.empty, T, k, dtype=torch.float32, device=dev) if gates is None else gates
+    ws, wsb = _workspace(route_workspace_size(T, H, E, k), dev, workspace, stream)
     _check(lib().md_moe_route_topk(_ptr(x), T, H, _ptr(Wr), _ptr(bias), E, k, _ptr(idx), _ptr(gates), _ptr(logits),
                                    _ptr(ws), wsb, _stream(stream)))
     return idx, gates
@@ -245,8 +271,8 @@ def ffn_forward(ffn, x, y=None, workspace=None, stream=None):
     T = x.shape[0]
     d = ffn.desc()
     if y is None:
-        y = torch.empty(T, ffn.down.rows, dtype=torch.float32, device=x.device)
-    ws, wsb = _workspace(ffn_workspace_size(ffn, T), x.device, workspace)
+        y = _result(stream, torch.empty, T, ffn.down.rows, dtype=torch.float32, device=x.device)
+    ws, wsb = _workspace(ffn_workspace_size(ffn, T), x.device, workspace, stream)
     _check(lib().md_ffn_forward(ctypes.byref(d), _ptr(x), T, _ptr(y), _ptr(ws), wsb, _stream(stream)))
     return y
 
@@ -299,8 +325,8 @@ def moe_layer_forward(layer, x, y=None, idx=None, gates=None, workspace=None, st
     dev = x.device
     d = layer.desc()
     if y is None:
-        y = torch.empty(T, layer.H, dtype=torch.float32, device=dev)
-    ws, wsb = _workspace(moe_workspace_size(layer, T), dev, workspace)
+        y = _result(stream, torch.empty, T, layer.H, dtype=torch.float32, device=dev)
+    ws, wsb = _workspace(moe_workspace_size(layer, T), dev, workspace, stream)
     if residual is None:
         _check(lib().md_moe_layer_forward(ctypes.byref(d), _ptr(x), T, _ptr(y), _ptr(idx), _ptr(gates), _ptr(ws), wsb,
                                           _stream(stream)))
@@ -339,8 +365,8 @@ def moe_layer_forward_timed(layer, x, stage, start, stop, y=None, idx=None, gate
     dev = x.device
     d = layer.desc()
     if y is None:
-        y = torch.empty(T, layer.H, dtype=torch.float32, device=dev)
-    ws, wsb = _workspace(moe_workspace_size(layer, T), dev, workspace)
+        y = _result(stream, torch.empty, T, layer.H, dtype=torch.float32, device=dev)
+    ws, wsb = _workspace(moe_workspace_size(layer, T), dev, workspace, stream)
     _check(lib().md_moe_layer_forward_timed(ctypes.byref(d), _ptr(x), T, _ptr(y), _ptr(idx), _ptr(gates), _ptr(ws),
                                             wsb, _stream(stream), STAGES.get(stage, stage), start.cuda_event,
                                             stop.cuda_event))
@@ -352,7 +378,7 @@ def add(a, b, out=None, stream=None):
     add between stacked layers."""
     import torch
     if out is None:
-        out = torch.empty_like(a)
+        out = _result(stream, torch.empty_like, a)
     _check(lib().md_add(_ptr(a), _ptr(b), _ptr(out), a.numel(), _stream(stream)))
     return out
 
@@ -373,8 +399,8 @@ def moe_experts_forward(layer, x, idx, gates, y=None, workspace=None, stream=Non
     T = x.shape[0]
     d = layer.desc()
     if y is None:
-        y = torch.empty(T, layer.H, dtype=torch.float32, device=x.device)
-    ws, wsb = _workspace(moe_workspace_size(layer, T), x.device, workspace)
+        y = _result(stream, torch.empty, T, layer.H, dtype=torch.float32, device=x.device)
+    ws, wsb = _workspace(moe_workspace_size(layer, T), x.device, workspace, stream)
     _check(lib().md_moe_experts_forward(ctypes.byref(d), _ptr(x), T, _ptr(idx), _ptr(gates), _ptr(y), _ptr(ws), wsb,
                                         _stream(stream)))
     return y
@@ -464,8 +490,8 @@ class ExpertTier:
         import torch
         T = x.shape[0]
         if y is None:
-            y = torch.empty(T, self.host.H, dtype=torch.float32, device=x.device)
-        ws, wsb = _workspace(self.workspace_size(T), x.device, workspace)
+            y = _result(stream, torch.empty, T, self.host.H, dtype=torch.float32, device=x.device)
+        ws, wsb = _workspace(self.workspace_size(T), x.device, workspace, stream)
         cs = self.copy_stream.cuda_stream if self.copy_stream is not None else None
         ev = self.copy_done.cuda_event if self.copy_done is not None else None
         _check(lib().md_moe_cached_forward(ctypes.byref(self.host.desc()), ctypes.byref(self.slots.desc()),
@@ -579,20 +605,20 @@ def i8_quantize(x, codes=None, scales=None, stream=None):
     dev = x.device
     _dense("x", x, (T, K), x.dtype, dev)
     with _on(dev, stream) as st:
-        codes = torch.empty(T, K, dtype=torch.int8, device=dev) if codes is None else \
+        codes = _result(stream, torch.empty, T, K, dtype=torch.int8, device=dev) if codes is None else \
             _dense("codes", codes, (T, K), torch.int8, dev)
-        scales = torch.empty(T, dtype=torch.float32, device=dev) if scales is None else \
+        scales = _result(stream, torch.empty, T, dtype=torch.float32, device=dev) if scales is None else \
             _dense("scales", scales, (T,), torch.float32, dev)
         _check(lib().md_i8_quantize(_ptr(x), _xtype(x.dtype), T, K, _ptr(codes), _ptr(scales), st))
     return codes, scales
 
 
-def _i8_args(W, T, bias, y, out_dtype, device):
+def _i8_args(W, T, bias, y, out_dtype, device, stream):
     import torch
     if bias is not None:
         _dense("bias", bias, (W.rows,), torch.float32, device)
     if y is None:
-        return torch.empty(T, W.rows, dtype=out_dtype or torch.float32, device=device)
+        return _result(stream, torch.empty, T, W.rows, dtype=out_dtype or torch.float32, device=device)
     if out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
     return _dense("y", y, (T, W.rows), y.dtype, device)
@@ -606,7 +632,7 @@ def i8_matmul(W, codes, scales, bias=None, y=None, out_dtype=None, stream=None):
     _dense("codes", codes, (T, W.cols), torch.int8, dev)
     _dense("scales", scales, (T,), torch.float32, dev)
     with _on(dev, stream) as st:
-        y = _i8_args(W, T, bias, y, out_dtype, dev)
+        y = _i8_args(W, T, bias, y, out_dtype, dev, stream)
         _check(lib().md_i8_matmul(_i8_desc(W, dev), _ptr(codes), _ptr(scales), T, _ptr(bias), _ptr(y),
                                   _xtype(y.dtype), st))
     return y
@@ -623,14 +649,14 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
     T, dev = x.shape[0], x.device
     _dense("x", x, (T, W.cols), x.dtype, dev)
     with _on(dev, stream) as st:
-        y = _i8_args(W, T, bias, y, out_dtype, dev)
+        y = _i8_args(W, T, bias, y, out_dtype, dev, stream)
         L, d = lib(), _i8_desc(W, dev)
         ws, wsb = None, 0
         if T > 1:
             made, key = W.__dict__.get("_i8_need"), (W.rows, W.cols, T)
             if made is None or made[0] != key:  # the last call's answer: the size follows from these alone
                 made = W._i8_need = (key, i8_linear_workspace_size(W, T))
-            ws, wsb = _workspace(made[1], dev, workspace)
+            ws, wsb = _workspace(made[1], dev, workspace, stream)
         _check(L.md_i8_linear(d, x.data_ptr(), _xtype(x.dtype), T, _ptr(bias), y.data_ptr(), _xtype(y.dtype), _ptr(ws),
                               wsb, st))
     return y
@@ -741,7 +767,8 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
     qs = _rows("q", q, heads, cache.head_dim, cache.device)
     with _on(cache.device, stream) as st:
         if out is None:
-            out = torch.empty(rows, heads, dim, dtype=out_dtype or torch.float32, device=cache.device)
+            out = _result(stream, torch.empty, rows, heads, dim, dtype=out_dtype or torch.float32,
+                          device=cache.device)
         elif out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
         if out.shape[0] != rows:
@@ -755,7 +782,7 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
             _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
                                                     ctypes.byref(need)))
             made = batch._need = (key, need.value)
-        ws, wsb = _workspace(made[1], cache.device, workspace)
+        ws, wsb = _workspace(made[1], cache.device, workspace, stream)
         _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
                                  dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws),
                                  wsb, st))
@@ -771,8 +798,10 @@ def kv_read_pages(cache, pages, k=None, v=None, out_dtype=None, stream=None):
     shape = (n, cache.kv_heads, cache.page, cache.head_dim)
     with _on(dev, stream) as st:
         dt = out_dtype or (k.dtype if k is not None else torch.float32)
-        k = torch.empty(shape, dtype=dt, device=dev) if k is None else _dense("k", k, shape, dt, dev)
-        v = torch.empty(shape, dtype=dt, device=dev) if v is None else _dense("v", v, shape, dt, dev)
+        k = _result(stream, torch.empty, shape, dtype=dt, device=dev) if k is None else \
+            _dense("k", k, shape, dt, dev)
+        v = _result(stream, torch.empty, shape, dtype=dt, device=dev) if v is None else \
+            _dense("v", v, shape, dt, dev)
         _check(lib().md_kv_read_pages(cache._ref, _ptr(pages), n, _ptr(k), _ptr(v), _xtype(dt), st))
     return k, v
 
