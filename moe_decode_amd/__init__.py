@@ -187,6 +187,11 @@ class DevQMatrix:
         self.rows, self.cols, self.count = rows, cols, count
         self.q, self.row_scale = q, row_scale
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if not name.startswith("_i8"):      # what _i8_desc has checked and packed
+            object.__setattr__(self, "_i8", None)
+
     def desc(self, expert=0):
         rb = row_bytes(self.type, self.cols)
         off = expert * self.rows * rb
@@ -577,22 +582,24 @@ class _on:
 
 
 def _i8_desc(W, device=None):
-    """The C descriptor of an int8 matrix, made once while its tensors stay;
-    they have to hold the matrix and lie on `device`."""
-    made, r = W.__dict__.get("_i8"), W.row_scale
-    key = (W.q.data_ptr(), None if r is None else r.data_ptr(), W.rows, W.cols, W.type, W.count)
-    if made is None or made[0] != key:
+    """The C descriptor of an int8 matrix, packed once while its attributes stay
+    (DevQMatrix drops it when one is set); its tensors have to hold the matrix
+    and lie on `device`."""
+    q, r = W.q, W.row_scale
+    made, at = W._i8, (q.data_ptr(), None if r is None else r.data_ptr())
+    if made is None or made[0] != at:
         import torch
         if W.count != 1:
             raise ValueError(f"one matrix wanted, got a stack of {W.count}")
         if W.type == I8_ROW:
-            if not W.q.is_contiguous() or W.q.numel() * W.q.element_size() < W.rows * W.cols:
-                raise ValueError(f"W.q: {W.rows} x {W.cols} bytes wanted, got {tuple(W.q.shape)} of {W.q.dtype}")
+            if not q.is_contiguous() or q.nbytes < W.rows * W.cols:
+                raise ValueError(f"W.q: {W.rows} x {W.cols} bytes wanted, got {tuple(q.shape)} of {q.dtype}, strides "
+                                 f"{q.stride()}")
             if r is not None and (r.dtype != torch.float32 or not r.is_contiguous() or r.numel() < W.rows
-                                  or r.device != W.q.device):
-                raise ValueError(f"W.row_scale: {W.rows} float32 values on {W.q.device} wanted, got "
-                                 f"{tuple(r.shape)} of {r.dtype} on {r.device}")
-        made = W._i8 = (key, ctypes.byref(W.desc()), W.q.device)
+                                  or r.device != q.device):
+                raise ValueError(f"W.row_scale: {W.rows} float32 values on {q.device} wanted, got {tuple(r.shape)} of "
+                                 f"{r.dtype} on {r.device}, strides {r.stride()}")
+        made = W._i8 = (at, ctypes.byref(W.desc()), q.device)
     if device is not None and made[2] != device:
         raise ValueError(f"W is on {made[2]}, the call's tensors on {device}")
     return made[1]
