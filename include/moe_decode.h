@@ -520,9 +520,10 @@ md_status md_kv_append(const md_kv_cache *c /*host*/, const md_kv_batch *b /*hos
  * rows that see it.  Scores have to stay within fp32's range: those past it give
  * NaN, or weights of 0.
  * Long sequences are split over workgroups and joined by a second kernel (few
- * columns: all tiles of the batch are dealt out evenly, following the lengths on
- * the device); the order of every sum is fixed, so the same batch gives the same
- * bits.
+ * columns: all tiles of a batch of up to 1024 sequences are dealt out evenly,
+ * following the lengths on the device; in a larger one each sequence's heads have a
+ * workgroup each, however long it is); the order of every sum is fixed, so the same
+ * batch gives the same bits.
  * Errors: a null pointer, an unknown type, causal not 0 or 1, window < 0 or
  * without causal, a scale that is not finite, out == q -> MD_ERR_INVALID_ARG;
  * sizes that are not positive, a stride below its row, q_heads no multiple of

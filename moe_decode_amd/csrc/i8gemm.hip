@@ -136,8 +136,9 @@ MD_DEV void put4(void* y, int64_t row, int N, int n, const i32x4& a, float xs, c
 // its waves split the sum and meet in LDS.  Weights go from HBM straight into
 // the matrix cores' operand registers (lane l: row l % 16, 16 bytes at
 // 64 step + 16 (l / 16)), codes of x from the L2.
-// Bound by the read of W (6144 x 6144, 4 tokens: 12.8 us for 37.7 MB, the
-// quantizer's launch included).
+// Reads W once (6144 x 6144, 37.7 MB from HBM, us a call: 4 tokens 11.1, with the
+// quantizer's launch 14.6; 32 tokens 21.9 and 25.8): 3.4 TB/s at 4 tokens, half of
+// what a plain read reaches.
 // OWN: x itself comes in, and every workgroup rounds all of it to codes in its
 // LDS while its first weights are on their way: one launch less, which is half
 // of a small call (i8_own_codes).

@@ -231,7 +231,10 @@ MD_DEV float weights(const float (&x)[16], float f, float ref, i32x4 (&pd)[kWeig
 // A form that only loaded took 5% less: it waits for memory.  Half, one and a
 // half times and twice as many workgroups, when it took 67 and 83: 75, 77, 73
 // and 81, 94, 89 us.
-constexpr int kMaxDealt = 1024;  // sequences, at most, that a workgroup sums up
+// Sequences, at most, that a workgroup sums up (8 bytes of LDS each).  In a larger
+// batch every segment stays whole (one of 32768 tokens among 1024 sequences, 8
+// heads on 1 of 64: 34 us; among 1025: 137).
+constexpr int kMaxDealt = 1024;
 
 // The tiles that any column of a sequence sees, one at least where it has rows:
 // somebody has to write their zeros.
@@ -500,7 +503,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 // f16, and so is a weight p times a unit times vs / R, R the power of two at or
 // below the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second
 // f16 for what the first one leaves, 22 bits together, and the unit 2^14, which
-// keeps both parts of weights down to 2^-18 whole.  NS = 1: a row's reference
+// keeps both parts of weights down to 2^-18 whole; it does not fit the registers at
+// 128 channels (22 spilled) and 256 (89).  NS = 1: a row's reference
 // follows its maximum only where that has grown by 2^7, so p stays below 2^7 and
 // the unit is 2^7 (a weight below 2^-21 loses bits, 2^-32 at most); without that
 // some column's maximum moves in most tiles and the sums are rescaled there
