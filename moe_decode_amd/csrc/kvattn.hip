@@ -231,6 +231,7 @@ MD_DEV float weights(const float (&x)[16], float f, float ref, i32x4 (&pd)[kWeig
 // A form that only loaded took 5% less: it waits for memory.  Half, one and a
 // half times and twice as many workgroups, when it took 67 and 83: 75, 77, 73
 // and 81, 94, 89 us.
+
 // Sequences, at most, that a workgroup sums up (8 bytes of LDS each).  In a larger
 // batch every segment stays whole (one of 32768 tokens among 1024 sequences, 8
 // heads on 1 of 64: 34 us; among 1025: 137).
