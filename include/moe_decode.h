@@ -24,7 +24,10 @@
  *   - the attention block beside it in 8-bit integers: the linear layers with a
  *     scale for each token and output channel (int8 rows, any number of
  *     tokens), a paged cache of keys and values with a scale for each page and
- *     head, the attention that reads it, and the bookkeeping of its pages.
+ *     head, the attention that reads it, and the bookkeeping of its pages;
+ *   - what a step that checks drafted tokens needs around them: norms and
+ *     rotation of queries and keys, attention over a tree of drafts and over a
+ *     window with sinks, routing with balance and groups, log probabilities.
  *
  * Conventions (every entry point):
  *   - Pointers marked "device" are HIP device pointers, "host" are host
@@ -47,7 +50,8 @@
  * Supported shapes: hidden / input widths (cols) are multiples of 256 and at
  * most 16384; rows 1..65536; E <= 256; 1 <= k <= 8; T <= 128 tokens per
  * layer call (longer prompts are split by the caller into chunks of at most
- * 128 tokens); batch <= 8 for md_qgemv; md_i8_* and md_kv_*: see there.
+ * 128 tokens); batch <= 8 for md_qgemv; md_i8_*, md_kv_*, md_qk_norm_rope,
+ * md_moe_route and md_token_logprobs: see there.
  *
  * Accuracy contract.  Weights are decoded exactly (scale times code) and
  * every contraction y = sum_c w_c x_c is accumulated in fp32 or exactly in
@@ -538,6 +542,50 @@ md_status md_kv_attention(const md_kv_cache *c /*host*/, const md_kv_batch *b /*
                           int32_t ytype, int64_t out_stride, void *workspace, size_t workspace_bytes,
                           hipStream_t stream);
 
+/* md_kv_attention, causal, with what a row sees set by more than its position.
+ *   window > 0 with sinks: the last `window` positions up to the row's own and,
+ *   of those before them, the first `sinks` of the sequence.  sinks without a
+ *   window change nothing: every position up to the row's own is seen.
+ *   tree (device, uint64 [rows][words], 64 * words >= max_q): the run's tokens
+ *   are the nodes of a tree of drafts.  Row i of a run sees the run's token j
+ *   where bit j % 64 of its word j / 64 is set (its own too only then; bits
+ *   past the run are not read), and every position before the run; with window
+ *   > 0, of a of the run's tokens seen, the last max(window - a, 0) of those
+ *   positions, and the first `sinks`.  NULL: no tree (words is not read).
+ * A row that sees nothing gives zeros.  Everything else as md_kv_attention with
+ * causal 1.  Errors: as there; a null mask -> MD_ERR_INVALID_ARG; sinks < 0 ->
+ * MD_ERR_INVALID_ARG; words < 1 or 64 * words < max_q -> MD_ERR_SHAPE; a tree
+ * off 8 bytes -> MD_ERR_ALIGNMENT; words > 16384 -> MD_ERR_UNSUPPORTED. */
+typedef struct md_kv_mask {
+    int32_t window;            /* 0: none                                     */
+    int32_t sinks;             /* first positions that stay visible           */
+    int32_t words;             /* words of a row of tree                      */
+    const uint64_t *tree;      /* device [rows][words], or NULL               */
+} md_kv_mask;
+md_status md_kv_attention_masked_workspace_size(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/,
+                                                int32_t q_heads, const md_kv_mask *mask /*host*/, int32_t ytype,
+                                                size_t *bytes /*host*/);
+md_status md_kv_attention_masked(const md_kv_cache *c /*host*/, const md_kv_batch *b /*host*/, const void *q,
+                                 int32_t xtype, int32_t q_heads, int64_t q_stride, float scale,
+                                 const md_kv_mask *mask /*host*/, void *out, int32_t ytype, int64_t out_stride,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The masks of a batch's trees of drafts from their parents: parents (device,
+ * int32 [rows]) holds each token's parent, as its number within the sequence's
+ * run (below the token's own), or -1 for one that follows the cached tokens
+ * directly.  masks (device, uint64 [rows][words]) receives a bit for the token
+ * and for each of its ancestors, positions (device, int32 [rows], may be NULL)
+ * the place in the text: kv_len - n of the run's n tokens, plus the number of
+ * ancestors.  A token whose chain of parents leaves the run, or does not
+ * descend, gets no bits and position -1.  Runs of up to 1024 tokens.  Rows
+ * behind the last sequence are left as they are, as are those of a sequence
+ * whose q_start is not ascending within 0..rows; of one with more than max_q
+ * rows the first max_q are written.  Only q_start and kv_len of the batch are
+ * read.  Errors: as md_kv_append's for the batch; max_q > 1024 ->
+ * MD_ERR_UNSUPPORTED; 64 * words < max_q -> MD_ERR_SHAPE. */
+md_status md_kv_tree(const md_kv_batch *b /*host*/, const int32_t *parents, uint64_t *masks, int32_t words,
+                     int32_t *positions, hipStream_t stream);
+
 /* The values that n pages hold (pages: device, n int32): k and v as
  * [n][kv_heads][page][head_dim] in ytype, both with the token before the
  * channel.  Slots that no token has reached give what their codes stand for; a
@@ -599,6 +647,109 @@ md_status md_kv_pages_truncate(md_kv_pages *p /*host*/, const int32_t *table /*h
 md_status md_kv_pages_compact(md_kv_pages *p /*host*/, int32_t *tables /*host*/, int32_t table_stride,
                               const int32_t *lens /*host*/, int32_t n_seqs, int32_t *copy_src /*host*/,
                               int32_t *copy_dst /*host*/, int32_t *n_copy /*host*/);
+
+/* ---- around the attention and the experts -------------------------------- */
+
+/* Norms of queries and keys for each head, and their rotation by position, in
+ * one pass (before md_kv_append and md_kv_attention).  For each row and head
+ *     z = x / sqrt(mean_c x_c^2 + eps) * weight        (no weight: z = x)
+ *     y = z, but for the pairs (a, b) of its first `rot` channels:
+ *     y_a = f (z_a cos t - z_b sin t),   y_b = f (z_b cos t + z_a sin t),
+ *     t = positions[row] * inv_freq[p] of pair p,  f = factor,
+ * p pairing channel p with p + rot / 2, or with `interleaved` 2 p with 2 p + 1.
+ * x and y are fp32 or bf16 (xtype, ytype); sums and products are fp32, the
+ * angle and what is left of it after whole turns fp64, so that far positions
+ * keep their accuracy.  head_dim: a multiple of 8 up to 256; rot: a multiple of
+ * 8, 0..head_dim.  q: rows x q_heads x head_dim, row strides in values, a
+ * multiple of 16 bytes; k likewise, or k_heads 0 (k is not read then).  An
+ * output may be its input (same address, type and row stride); otherwise
+ * nothing may overlap.  rows: 0..2^20 (0: nothing to do).  An infinity or a NaN
+ * reaches the outputs of its own row and head only.  Errors: a null pointer, an
+ * unknown type, a factor or eps that is not finite, eps < 0 ->
+ * MD_ERR_INVALID_ARG; rows, heads or a head_dim that are not positive, rot outside 0..head_dim,
+ * a stride below its row -> MD_ERR_SHAPE; sizes outside the sets, more than
+ * 1024 heads of either -> MD_ERR_UNSUPPORTED; a pointer or row stride off 16
+ * bytes (positions: 4) -> MD_ERR_ALIGNMENT. */
+typedef struct md_rope {
+    int32_t head_dim, rot;
+    int32_t interleaved;       /* 0: channel p with p + rot / 2; 1: 2 p with 2 p + 1 */
+    const float *inv_freq;     /* device [rot / 2]                            */
+    float factor;              /* 1 for none                                  */
+    float eps;
+    const float *q_weight;     /* device [head_dim], or NULL: no norm         */
+    const float *k_weight;
+} md_rope;
+md_status md_qk_norm_rope(const md_rope *r /*host*/, const int32_t *positions, int32_t rows, const void *q,
+                          int32_t q_heads, int64_t q_stride, const void *k, int32_t k_heads, int64_t k_stride,
+                          int32_t xtype, void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                          int32_t ytype, hipStream_t stream);
+
+/* Routing to experts for any number of tokens (idx and gates as
+ * md_moe_experts_forward takes them, 128 tokens a call there):
+ *     l_e = sum_c W_r[e][c] x[c] (+ router_bias[e]), in fp64, rounded once to fp32
+ *     s_e = 1 / (1 + exp(-l_e)), or exp(l_e) / sum_i exp(l_i)
+ *     c_e = s_e + balance_e            (what chooses; balance NULL: s_e)
+ * With groups > 1 the E experts are `groups` equal runs; a run's value is its
+ * largest c (best_two: the sum of its two largest), and only the experts of the
+ * groups_kept runs of the largest values may be chosen.  idx: the k largest c in
+ * descending order, gates: their s (not c), with renorm divided by the chosen
+ * ones' sum, times scale.  Equal values go to the lower run and expert.  Scores,
+ * values and gates are fp64 until a gate is rounded to fp32, so that the choice
+ * is the definition's.  x: T x H fp32 or bf16; logits (T x E fp32, may be NULL).
+ * T: 0..2^20 (0: nothing to do); H, E, k as md_moe_route_topk.  A NaN is the
+ * smallest of all; idx then still names k different experts.  Errors: null
+ * pointers, unknown xtype or score, a flag that is not 0 or 1, a scale that is
+ * not finite -> MD_ERR_INVALID_ARG; T < 0, k > E, groups that do not divide E,
+ * groups_kept outside 1..groups, fewer experts in them than k, best_two with runs of one
+ * expert -> MD_ERR_SHAPE; sizes outside the sets -> MD_ERR_UNSUPPORTED; pointers
+ * off 16 bytes -> MD_ERR_ALIGNMENT; the workspace -> MD_ERR_WORKSPACE. */
+typedef enum md_score { MD_SCORE_SOFTMAX = 0, MD_SCORE_SIGMOID = 1 } md_score;
+typedef struct md_routing {
+    int32_t k;
+    int32_t score;             /* md_score                                    */
+    int32_t groups, groups_kept, best_two;
+    int32_t renorm;
+    float scale;
+    const float *balance;      /* device [E], or NULL                         */
+} md_routing;
+md_status md_moe_route_workspace_size(int32_t T, int32_t H, int32_t E, size_t *bytes /*host*/);
+md_status md_moe_route(const md_routing *r /*host*/, const void *x, int32_t xtype, int32_t T, int32_t H,
+                       const float *W_r, const float *router_bias, int32_t E, int32_t *idx, float *gates, float *logits,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The layer forward with such a routing in place of the layer's own top-k
+ * (W_r and router_bias are the layer's; routing->k = L->k): md_moe_route, then
+ * md_moe_experts_forward.  T, y, idx_out, gates_out as md_moe_layer_forward. */
+md_status md_moe_routed_workspace_size(const md_moe_layer *L /*host*/, int32_t T, size_t *bytes /*host*/);
+md_status md_moe_layer_forward_routed(const md_moe_layer *L /*host*/, const md_routing *routing /*host*/, const float *x,
+                                      int32_t T, float *y, int32_t *idx_out, float *gates_out, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* Log probabilities from rows of logits: with z_v = scale * logits[row][v] and
+ * Z = sum_v exp(z_v),
+ *     logprobs[row][i] = z_t - log Z,  t = tokens[row][i]      (n_tokens of them)
+ *     entropy[row]     = log Z - sum_v z_v exp(z_v) / Z
+ *     top_ids[row][j], top_logprobs[row][j]: the `top` largest logits in
+ *     descending order (equal ones: the lower id first), and z - log Z of each.
+ * logits: rows x vocab fp32 or bf16, any row stride (in values) from vocab on;
+ * rows may begin at any value (an odd vocabulary).  A logit of -inf has
+ * probability 0 and adds nothing to the entropy.  A row with a NaN or +inf, or
+ * of -inf alone, has NaN in all its values; top_ids then still are the order's,
+ * a NaN taken as the smallest.  A token outside 0..vocab-1 gives NaN.  Sums of a
+ * row's parts are fp32, their joins fp64.
+ * rows: 0..2^20 (0: nothing to do), vocab: 1..2^20, n_tokens: 0..64, top: 0..32,
+ * at most vocab.  tokens, logprobs: [rows][n_tokens], entropy: [rows] or NULL,
+ * top_ids, top_logprobs: [rows][top]; those of n_tokens or top 0 are not read.
+ * Errors: null pointers, an unknown type, a scale that is not finite and
+ * positive -> MD_ERR_INVALID_ARG; negative sizes, top > vocab, a stride below
+ * vocab -> MD_ERR_SHAPE; sizes past the above -> MD_ERR_UNSUPPORTED; logits off
+ * their own size, the others off 4 bytes (workspace: 16) -> MD_ERR_ALIGNMENT;
+ * the workspace -> MD_ERR_WORKSPACE. */
+md_status md_token_logprobs_workspace_size(int32_t rows, int32_t vocab, int32_t top, size_t *bytes /*host*/);
+md_status md_token_logprobs(const void *logits, int32_t xtype, int64_t stride, int32_t rows, int32_t vocab,
+                            const int32_t *tokens, int32_t n_tokens, float scale, int32_t top, float *logprobs,
+                            float *entropy, int32_t *top_ids, float *top_logprobs, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 /* Measurement aid: reads nbytes of device memory at src once, in address
  * order, with every compute unit busy, and writes nothing unless some lane's

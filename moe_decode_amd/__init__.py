@@ -9,6 +9,7 @@ A call runs on the current stream, or on `stream`: then what it allocates is
 that stream's memory, and the caller has other streams wait for it before they
 read its outputs.
 """
+import collections
 import ctypes
 import os
 
@@ -34,7 +35,10 @@ EXPORTS = ("md_abi_version", "md_status_string", "md_last_error_detail", "md_row
            "md_i8_quantize", "md_i8_matmul", "md_i8_linear_workspace_size", "md_i8_linear",
            "md_kv_append", "md_kv_attention_workspace_size", "md_kv_attention", "md_kv_read_pages",
            "md_kv_copy_pages", "md_kv_pages_reset", "md_kv_pages_extend", "md_kv_pages_fork",
-           "md_kv_pages_truncate", "md_kv_pages_compact")
+           "md_kv_pages_truncate", "md_kv_pages_compact",
+           "md_kv_attention_masked_workspace_size", "md_kv_attention_masked", "md_kv_tree", "md_qk_norm_rope",
+           "md_moe_route_workspace_size", "md_moe_route", "md_moe_routed_workspace_size",
+           "md_moe_layer_forward_routed", "md_token_logprobs_workspace_size", "md_token_logprobs")
 STAGES = {"shared": 0, "router": 1, "select": 2, "gateup": 3, "down": 4, "combine": 5}
 
 
@@ -118,6 +122,17 @@ def lib():
             "md_kv_pages_fork": (i32, [vp, vp, i32, vp, i32]),
             "md_kv_pages_truncate": (i32, [vp, vp, i32, i32]),
             "md_kv_pages_compact": (i32, [vp, vp, i32, vp, i32, vp, vp, vp]),
+            "md_kv_attention_masked_workspace_size": (i32, [vp, vp, i32, vp, i32, psz]),
+            "md_kv_attention_masked": (i32, [vp, vp, vp, i32, i32, i64, ctypes.c_float, vp, vp, i32, i64, vp, sz, vp]),
+            "md_kv_tree": (i32, [vp, vp, vp, i32, vp, vp]),
+            "md_qk_norm_rope": (i32, [vp, vp, i32, vp, i32, i64, vp, i32, i64, i32, vp, i64, vp, i64, i32, vp]),
+            "md_moe_route_workspace_size": (i32, [i32, i32, i32, psz]),
+            "md_moe_route": (i32, [vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+            "md_moe_routed_workspace_size": (i32, [vp, i32, psz]),
+            "md_moe_layer_forward_routed": (i32, [vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+            "md_token_logprobs_workspace_size": (i32, [i32, i32, i32, psz]),
+            "md_token_logprobs": (i32, [vp, i32, i64, i32, i32, vp, i32, ctypes.c_float, i32, vp, vp, vp, vp, vp, sz,
+                                        vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -322,13 +337,33 @@ def moe_workspace_size(layer, T):
     return need.value
 
 
-def moe_layer_forward(layer, x, y=None, idx=None, gates=None, workspace=None, stream=None, residual=None):
+def moe_layer_forward(layer, x, y=None, idx=None, gates=None, workspace=None, stream=None, residual=None,
+                      routing=None):
     """y = layer(x), or residual + layer(x) when a residual ([T][H] fp32,
-    possibly x or y) is given."""
+    possibly x or y) is given.  routing (a Routing): in place of the layer's own
+    top-k; a residual is then added by the caller (add)."""
     import torch
     T = x.shape[0]
     dev = x.device
     d = layer.desc()
+    if routing is not None:
+        if residual is not None:
+            raise ValueError("a layer with a routing takes no residual")
+        _dense("x", x, (T, layer.H), torch.float32, dev)
+        with _on(dev, stream) as st:
+            r = routing.desc(layer.E, dev)
+            y = _result(stream, torch.empty, T, layer.H, dtype=torch.float32, device=dev) if y is None else \
+                _dense("y", y, (T, layer.H), torch.float32, dev)
+            if idx is not None:
+                _dense("idx", idx, (T, layer.k), torch.int32, dev)
+            if gates is not None:
+                _dense("gates", gates, (T, layer.k), torch.float32, dev)
+            need = ctypes.c_size_t(0)
+            _check(lib().md_moe_routed_workspace_size(ctypes.byref(d), T, ctypes.byref(need)))
+            ws, wsb = _workspace(need.value, dev, workspace, stream)
+            _check(lib().md_moe_layer_forward_routed(ctypes.byref(d), r, _ptr(x), T, _ptr(y), _ptr(idx), _ptr(gates),
+                                                     _ptr(ws), wsb, st))
+        return y
     if y is None:
         y = _result(stream, torch.empty, T, layer.H, dtype=torch.float32, device=dev)
     ws, wsb = _workspace(moe_workspace_size(layer, T), dev, workspace, stream)
@@ -669,6 +704,11 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
     return y
 
 
+class KVMaskDesc(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("words", ctypes.c_int32),
+                ("tree", ctypes.c_void_p)]
+
+
 class KVCacheDesc(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int32), ("page", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -760,18 +800,29 @@ def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window
 
 
 def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, out_dtype=None, workspace=None,
-                 stream=None):
+                 stream=None, sinks=0, tree=None):
     """Attention of the batch's new rows q ([rows][q_heads][head_dim], fp32 or
     bf16, rows may be strided) over the cache; scale 1 / sqrt(head_dim) by
     default.  causal: a row sees the positions up to its own (window > 0: the
-    last `window` of them); else every position of its sequence.  out: fp32 or
-    bf16 (out_dtype, fp32 by default); rows behind the last sequence are left as
-    they are."""
+    last `window` of them, and with sinks the first `sinks` of the sequence);
+    else every position of its sequence.  tree (int64 [rows][words], as kv_tree
+    makes them): the run's tokens are the nodes of a tree, a row sees those whose
+    bits are set and the positions before the run.  out: fp32 or bf16 (out_dtype,
+    fp32 by default); rows behind the last sequence are left as they are."""
     import torch
     if q.dim() != 3 or batch.device != cache.device:
         raise ValueError(f"q [rows][q_heads][head_dim] and the batch on {cache.device} wanted")
     rows, heads, dim = q.shape
     qs = _rows("q", q, heads, cache.head_dim, cache.device)
+    mask = None
+    if tree is not None or sinks:
+        if not causal:
+            raise ValueError("a tree or sinks without causal")
+        words = 0
+        if tree is not None:
+            words = tree.shape[1] if tree.dim() == 2 else 0
+            _dense("tree", tree, (rows, words), torch.int64, cache.device)
+        mask = KVMaskDesc(window, sinks, words, _ptr(tree))
     with _on(cache.device, stream) as st:
         if out is None:
             out = _result(stream, torch.empty, rows, heads, dim, dtype=out_dtype or torch.float32,
@@ -783,17 +834,46 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         os_ = _rows("out", out, heads, cache.head_dim, cache.device)
         L, d, yt = lib(), batch.desc(rows), _xtype(out.dtype)
         key = (cache.page, cache.kv_heads, cache.head_dim, rows, heads, causal, window, yt)
+        if mask is not None:
+            key += (sinks, mask.words)
         made = batch._need  # the last call's answer: the size follows from these alone
         if made[0] != key:
             need = ctypes.c_size_t(0)
-            _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
-                                                    ctypes.byref(need)))
+            if mask is None:
+                _check(L.md_kv_attention_workspace_size(cache._ref, d, heads, int(causal), window, yt,
+                                                        ctypes.byref(need)))
+            else:
+                _check(L.md_kv_attention_masked_workspace_size(cache._ref, d, heads, ctypes.byref(mask), yt,
+                                                               ctypes.byref(need)))
             made = batch._need = (key, need.value)
         ws, wsb = _workspace(made[1], cache.device, workspace, stream)
-        _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs,
-                                 dim ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), yt, os_, _ptr(ws),
-                                 wsb, st))
+        scale = dim ** -0.5 if scale is None else scale
+        if mask is None:
+            _check(L.md_kv_attention(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs, scale, int(causal), window,
+                                     _ptr(out), yt, os_, _ptr(ws), wsb, st))
+        else:
+            _check(L.md_kv_attention_masked(cache._ref, d, _ptr(q), _xtype(q.dtype), heads, qs, scale,
+                                            ctypes.byref(mask), _ptr(out), yt, os_, _ptr(ws), wsb, st))
     return out
+
+
+def kv_tree(batch, parents, masks=None, positions=None, stream=None):
+    """The masks of the batch's trees of drafts, and their tokens' positions in
+    the text, from each token's parent (int32 [rows] on the GPU: its number
+    within the run, or -1).  Returns masks (int64 [rows][max_q / 64 rounded up],
+    for kv_attention) and positions (int32 [rows], for qk_norm_rope)."""
+    import torch
+    rows, dev = parents.shape[0], batch.device
+    _dense("parents", parents, (rows,), torch.int32, dev)
+    with _on(dev, stream) as st:
+        if masks is None:
+            masks = _result(stream, torch.empty, rows, -(-batch.max_q // 64), dtype=torch.int64, device=dev)
+        else:
+            _dense("masks", masks, (rows, masks.shape[1]), torch.int64, dev)
+        positions = _result(stream, torch.empty, rows, dtype=torch.int32, device=dev) if positions is None else \
+            _dense("positions", positions, (rows,), torch.int32, dev)
+        _check(lib().md_kv_tree(batch.desc(rows), _ptr(parents), _ptr(masks), masks.shape[1], _ptr(positions), st))
+    return masks, positions
 
 
 def kv_read_pages(cache, pages, k=None, v=None, out_dtype=None, stream=None):
@@ -892,3 +972,164 @@ class KVPages:
                                          self.lens.ctypes.data, len(self.lens), self._src.ctypes.data,
                                          self._dst.ctypes.data, ctypes.byref(n)))
         return self._pairs(n.value)
+
+
+# ---- around the attention and the experts --------------------------------------
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("factor", ctypes.c_float), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, factor=1.0,
+                 q_out=None, k_out=None, out_dtype=None, stream=None):
+    """The heads of q ([rows][q_heads][head_dim], fp32 or bf16, rows may be
+    strided: a slice of a projection's output) and of k (likewise, or None) with
+    their norms (over a head's channels, times weight fp32 [head_dim]; None: no
+    norm), and their first 2 * len(inv_freq) channels turned by positions[row] *
+    inv_freq (int32 [rows], fp32): channel p with p + len(inv_freq), interleaved:
+    2 p with 2 p + 1; cosines and sines times factor.  q_out, k_out may be q and k
+    themselves; out_dtype: the inputs' type by default.  Returns both."""
+    import torch
+    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.dtype != q.dtype)):
+        raise ValueError("q and k [rows][heads][head_dim] of one length and type wanted")
+    rows, heads, dim = q.shape
+    dev = q.device
+    kh = 0 if k is None else k.shape[1]
+    qs, ks = _rows("q", q, heads, dim, dev), 0 if k is None else _rows("k", k, kh, dim, dev)
+    _dense("positions", positions, (rows,), torch.int32, dev)
+    _dense("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32, dev)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dense(name, w, (dim,), torch.float32, dev)
+    given = q_out if q_out is not None else k_out
+    dt = out_dtype or (q.dtype if given is None else given.dtype)
+
+    def out(name, t, n):
+        if t is None:
+            return _result(stream, torch.empty, rows, n, dim, dtype=dt, device=dev)
+        if t.dtype != dt or t.shape[0] != rows:
+            raise ValueError(f"{name}: {rows} rows of {dt} wanted, got {tuple(t.shape)} of {t.dtype}")
+        return t
+    with _on(dev, stream) as st:
+        q_out = out("q_out", q_out, heads)
+        qo = _rows("q_out", q_out, heads, dim, dev)
+        ko = 0
+        if k is not None:
+            k_out = out("k_out", k_out, kh)
+            ko = _rows("k_out", k_out, kh, dim, dev)
+        d = RopeDesc(dim, 2 * inv_freq.numel(), int(interleaved), inv_freq.data_ptr(), factor, eps, _ptr(q_weight),
+                     _ptr(k_weight))
+        _check(lib().md_qk_norm_rope(ctypes.byref(d), positions.data_ptr(), rows, q.data_ptr(), heads, qs, _ptr(k), kh,
+                                     ks, _xtype(q.dtype), q_out.data_ptr(), qo, _ptr(k_out), ko, _xtype(dt), st))
+    return q_out, k_out
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class RoutingDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("groups_kept", ctypes.c_int32), ("best_two", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("balance", ctypes.c_void_p)]
+
+
+class Routing:
+    """How tokens are routed: k experts by "softmax" or "sigmoid" scores, chosen
+    by score + balance (fp32 [E] on the GPU, or None) among the groups_kept best
+    of `groups` equal runs of experts (by their largest, best_two: the sum of
+    their two largest), with gates = scores (renorm: over their sum) times scale."""
+
+    def __init__(self, k, score="softmax", balance=None, groups=1, groups_kept=1, best_two=False, renorm=True,
+                 scale=1.0):
+        self.k, self.score, self.balance = k, SCORES.get(score, score), balance
+        self.groups, self.groups_kept, self.best_two = groups, groups_kept, bool(best_two)
+        self.renorm, self.scale = bool(renorm), scale
+
+    def desc(self, E, device):
+        """The C descriptor for a call on E experts."""
+        import torch
+        b = self.balance
+        if b is not None:
+            _dense("balance", b, (E,), torch.float32, device)
+        return ctypes.byref(RoutingDesc(self.k, self.score, self.groups, self.groups_kept, int(self.best_two),
+                                        int(self.renorm), self.scale, _ptr(b)))
+
+
+def moe_route_workspace_size(T, H, E):
+    need = ctypes.c_size_t(0)
+    _check(lib().md_moe_route_workspace_size(T, H, E, ctypes.byref(need)))
+    return need.value
+
+
+def moe_route(x, Wr, routing, bias=None, idx=None, gates=None, logits=None, workspace=None, stream=None):
+    """The experts of each row of x ([T][H] fp32 or bf16, any T) and their gates
+    ([T][k], int32 and fp32) for the router Wr ([E][H] fp32; bias fp32 [E], added
+    to the logits): what moe_experts_forward takes, 128 tokens at a time."""
+    import torch
+    T, H = x.shape
+    E, dev = Wr.shape[0], x.device
+    _dense("x", x, (T, H), x.dtype, dev)
+    _dense("Wr", Wr, (E, H), torch.float32, dev)
+    if bias is not None:
+        _dense("bias", bias, (E,), torch.float32, dev)
+    if logits is not None:
+        _dense("logits", logits, (T, E), torch.float32, dev)
+    k = routing.k
+    with _on(dev, stream) as st:
+        r = routing.desc(E, dev)
+        idx = _result(stream, torch.empty, T, k, dtype=torch.int32, device=dev) if idx is None else \
+            _dense("idx", idx, (T, k), torch.int32, dev)
+        gates = _result(stream, torch.empty, T, k, dtype=torch.float32, device=dev) if gates is None else \
+            _dense("gates", gates, (T, k), torch.float32, dev)
+        ws, wsb = _workspace(moe_route_workspace_size(T, H, E), dev, workspace, stream)
+        _check(lib().md_moe_route(r, x.data_ptr(), _xtype(x.dtype), T, H, Wr.data_ptr(), _ptr(bias), E, idx.data_ptr(),
+                                  gates.data_ptr(), _ptr(logits), _ptr(ws), wsb, st))
+    return idx, gates
+
+
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs entropy top_ids top_logprobs")
+
+
+def token_logprobs_workspace_size(rows, vocab, top=0):
+    need = ctypes.c_size_t(0)
+    _check(lib().md_token_logprobs_workspace_size(rows, vocab, top, ctypes.byref(need)))
+    return need.value
+
+
+def token_logprobs(logits, tokens=None, top=0, scale=1.0, logprobs=None, entropy=None, top_ids=None,
+                   top_logprobs=None, workspace=None, stream=None):
+    """From rows of logits ([rows][vocab] fp32 or bf16, rows may be strided),
+    taken times scale (one over the temperature): the log probabilities of tokens
+    (int32 [rows][n], None: none), the entropy, and the `top` largest logits' ids
+    and log probabilities (None where top is 0)."""
+    import torch
+    if logits.dim() != 2 or (logits.shape[0] and logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits: rows of neighbouring values wanted, got {tuple(logits.shape)} strides "
+                         f"{logits.stride()}")
+    rows, vocab = logits.shape
+    dev = logits.device
+    stride = logits.stride(0) if rows > 1 else vocab
+    n = 0
+    if tokens is not None:
+        n = tokens.shape[1] if tokens.dim() == 2 else -1
+        _dense("tokens", tokens, (rows, n), torch.int32, dev)
+
+    def out(name, t, dtype, *shape):
+        if t is None:
+            return _result(stream, torch.empty, shape, dtype=dtype, device=dev)
+        return _dense(name, t, shape, dtype, dev)
+    with _on(dev, stream) as st:
+        if tokens is not None:
+            logprobs = out("logprobs", logprobs, torch.float32, rows, n)
+        entropy = out("entropy", entropy, torch.float32, rows)
+        if top:
+            top_ids = out("top_ids", top_ids, torch.int32, rows, top)
+            top_logprobs = out("top_logprobs", top_logprobs, torch.float32, rows, top)
+        ws, wsb = _workspace(token_logprobs_workspace_size(rows, vocab, top), dev, workspace, stream)
+        _check(lib().md_token_logprobs(logits.data_ptr(), _xtype(logits.dtype), stride, rows, vocab, _ptr(tokens), n,
+                                       scale, top, _ptr(logprobs), entropy.data_ptr(), _ptr(top_ids),
+                                       _ptr(top_logprobs), _ptr(ws), wsb, st))
+    return TokenLogprobs(logprobs if tokens is not None else None, entropy, top_ids if top else None,
+                         top_logprobs if top else None)

@@ -17,8 +17,8 @@ OUT_SAN = os.path.join(HERE, "libmoe_decode_san.so")
 BUILD = os.path.join(HERE, "_build")
 BUILD_SAN = os.path.join(HERE, "_build_san")
 
-SOURCES = ["gemv.hip", "decode.hip", "route.hip", "prefill.hip", "i8gemm.hip", "kv.hip", "kvattn.hip",
-           "abi.cpp", "kv_abi.cpp"]
+SOURCES = ["gemv.hip", "decode.hip", "route.hip", "prefill.hip", "i8gemm.hip", "kv.hip", "kvattn.hip", "rope.hip",
+           "routing.hip", "logprob.hip", "abi.cpp", "kv_abi.cpp", "step_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

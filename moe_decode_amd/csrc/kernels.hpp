@@ -221,6 +221,9 @@ struct KvAttn {
   int64_t q_stride, out_stride;
   int xt, yt, G, causal, window, pshift;
   float scale;
+  int masked;                 // a tree, or sinks beside a window: what follows is read
+  int sinks, words;
+  const uint64_t* tree;       // [rows][words], or nullptr
   int tile;                   // columns (query, head) of a workgroup
   int snake;                  // all workgroups run at once, two on a compute unit
   int splits, chunk;          // many columns: a split covers chunk tiles of 64 positions
@@ -239,7 +242,57 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const void* k, i
                             int64_t v_stride, int xt, hipStream_t st);
 hipError_t launch_kv_read(const KvCache& c, const int* pages, int n, void* k, void* v, int yt, hipStream_t st);
 hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int n, hipStream_t st);
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal, int yt);
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt);
 hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st);
+hipError_t launch_kv_tree(const KvBatch& b, const int* parents, uint64_t* masks, int words, int* positions,
+                          hipStream_t st);
+
+// ---- norms and rotation of queries and keys (rope.hip) ----------------------
+struct RopeArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const float *q_weight, *k_weight, *inv_freq;
+  const int* positions;
+  int rows, Hq, Hkv, D, rot;
+  float eps, factor;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& g, bool pairs, int xt, int yt, hipStream_t st);
+
+// ---- routing (routing.hip) ---------------------------------------------------
+constexpr int kRouteFew = 8;  // tokens of the form that has a workgroup for each expert
+struct RouteArgs {
+  double* part;               // [S][T][E]
+  int S, T, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
+  float scale;
+  const float *bias, *balance;
+  float* logits;
+  int* idx;
+  float* gates;
+};
+struct RoutePlan {
+  int S, Ks;  // slices of the width and the width of one
+};
+RoutePlan route_plan(int64_t T, int H, int E);
+hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, int xt, int H, const float* Wr, hipStream_t st);
+
+// ---- log probabilities (logprob.hip) ----------------------------------------
+constexpr int kMaxTop = 32;
+constexpr int kMaxChunks = 128;                                   // of a row, or one more
+constexpr int kMaxJoin = ((kMaxChunks + 1) * kMaxTop + 63) / 64;  // keys of a row's chunks, for each of 64 lanes
+struct LogpArgs {
+  const void* logits;
+  int64_t stride, rows;
+  int vocab, n_tokens, top, chunks;
+  const int* tokens;
+  float scale;
+  float *logprobs, *entropy;
+  int* top_ids;
+  float* top_logprobs;
+  void *part, *keys;  // [rows][chunks] of 16 bytes, [rows][chunks][top] of 8
+};
+int logprob_values(int64_t rows, int vocab);
+int logprob_chunks(int64_t rows, int vocab);
+hipError_t launch_logprob(const LogpArgs& g, int xt, int values, hipStream_t st);
 
 }  // namespace md

@@ -305,4 +305,40 @@ hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int 
   return hipSuccess;
 }
 
+// Trees of drafts: a thread walks from a token up to the root.  Parents lie
+// before their children, so the bits of a row fill its words from the last one
+// down, each word written once.
+__global__ __launch_bounds__(64) void k_kv_tree(KvBatch b, const int* parents, uint64_t* masks, int words, int* positions) {
+  const int s = blockIdx.y, i = blockIdx.x * 64 + threadIdx.x;
+  const int r0 = b.q_start[s], r1 = b.q_start[s + 1];
+  if (r0 < 0 || r1 < r0 || r1 > b.rows) return;
+  const int n = min(r1 - r0, b.max_q);
+  if (i >= n) return;
+  const int* up = parents + r0;
+  bool good = true;
+  int depth = 0;
+  for (int j = i; good && j >= 0; ++depth) {
+    const int p = up[j];
+    good = p >= -1 && p < j;
+    j = p;
+  }
+  uint64_t* out = masks + ((int64_t)r0 + i) * words;
+  int j = good ? i : -1;
+  for (int w = words - 1; w >= 0; --w) {
+    uint64_t bits = 0;
+    while (j >= 0 && j >> 6 == w) {
+      bits |= 1ull << (j & 63);
+      j = up[j];
+    }
+    out[w] = bits;
+  }
+  if (positions) positions[r0 + i] = good ? b.kv_len[s] - (r1 - r0) + depth - 1 : -1;
+}
+
+hipError_t launch_kv_tree(const KvBatch& b, const int* parents, uint64_t* masks, int words, int* positions,
+                          hipStream_t st) {
+  hipLaunchKernelGGL(k_kv_tree, dim3((b.max_q + 63) / 64, b.S), dim3(64), 0, st, b, parents, masks, words, positions);
+  return hipGetLastError();
+}
+
 }  // namespace md

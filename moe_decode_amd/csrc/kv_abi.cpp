@@ -26,6 +26,8 @@ constexpr int kMaxSeqs = 65535;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxPositions = 1 << 30;  // tiles' borders and windows before position 0 stay in 32 bits
+constexpr int kMaxWords = kMaxTokens / 64;
+constexpr int kMaxTree = 1024;          // tokens of a run whose masks md_kv_tree makes
 constexpr int kMaxGrid = (1 << 24) - 1;  // workgroups of 256 along x: below 2^32 threads
 
 bool valid_xtype(int32_t t) { return t == MD_X_F32 || t == MD_X_BF16; }
@@ -132,7 +134,7 @@ int seen(const md_kv_batch* b, int32_t window) { return window >= b->max_kv ? 0 
 
 // The attention's checks up to its pointers, and its launch geometry.
 md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal, int32_t window,
-                    int32_t ytype, md::KvPlan* plan, size_t* bytes) {
+                    int32_t sinks, int32_t ytype, md::KvPlan* plan, size_t* bytes) {
   md_status s;
   if ((s = check_cache(c)) != MD_OK || (s = check_batch(c, b)) != MD_OK) return s;
   if (q_heads <= 0 || q_heads % c->kv_heads)
@@ -143,7 +145,7 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
     return fail(MD_ERR_INVALID_ARG, "attention: window %d%s", window, causal ? "" : " without causal");
   if (!valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown ytype %d", ytype);
   const int G = q_heads / c->kv_heads;
-  *plan = md::kv_attn_plan(dev(c), dev(b), G, seen(b, window), causal, ytype);
+  *plan = md::kv_attn_plan(dev(c), dev(b), G, seen(b, window), sinks, causal, ytype);
   const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
   if (groups > kMaxGrid) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
   const size_t slots = attn_slots(*plan, b, q_heads);
@@ -151,6 +153,26 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
                        align256(slots * c->head_dim * sizeof(float))
                  : 0;
   return MD_OK;
+}
+
+// What a mask's call reads: sinks count beside a window only.
+int kept(const md_kv_batch* b, const md_kv_mask* m) {
+  return seen(b, m->window) ? std::min(m->sinks, b->max_kv) : 0;
+}
+md_status masked_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, const md_kv_mask* m, int32_t ytype,
+                      md::KvPlan* plan, size_t* bytes) {
+  md_status s;
+  if ((s = check_cache(c)) != MD_OK || (s = check_batch(c, b)) != MD_OK) return s;
+  if (!m) return fail(MD_ERR_INVALID_ARG, "attention: null mask");
+  if (m->sinks < 0) return fail(MD_ERR_INVALID_ARG, "attention: sinks %d", m->sinks);
+  if (m->tree) {
+    if (m->words > kMaxWords) return fail(MD_ERR_UNSUPPORTED, "attention: a tree of %d words > %d", m->words, kMaxWords);
+    if (m->words < 1 || (int64_t)64 * m->words < b->max_q)
+      return fail(MD_ERR_SHAPE, "attention: a tree of %d words for runs of %d", m->words, b->max_q);
+    if (reinterpret_cast<uintptr_t>(m->tree) & 7u) return fail(MD_ERR_ALIGNMENT, "attention: the tree is not 8-byte aligned");
+  }
+  if (m->window < 0) return fail(MD_ERR_INVALID_ARG, "attention: window %d", m->window);
+  return attn_plan(c, b, q_heads, 1, m->window, kept(b, m), ytype, plan, bytes);
 }
 
 // ---- pages -----------------------------------------------------------------
@@ -322,20 +344,32 @@ md_status md_kv_attention_workspace_size(const md_kv_cache* c, const md_kv_batch
                                          int32_t window, int32_t ytype, size_t* bytes) {
   md::KvPlan plan;
   size_t need = 0;
-  const md_status s = attn_plan(c, b, q_heads, causal, window, ytype, &plan, &need);
+  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, ytype, &plan, &need);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
   *bytes = need;
   return ok();
 }
 
-md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void* q, int32_t xtype, int32_t q_heads,
-                          int64_t q_stride, float scale, int32_t causal, int32_t window, void* out, int32_t ytype,
-                          int64_t out_stride, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+md_status md_kv_attention_masked_workspace_size(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
+                                                const md_kv_mask* mask, int32_t ytype, size_t* bytes) {
   md::KvPlan plan;
   size_t need = 0;
-  md_status s = attn_plan(c, b, q_heads, causal, window, ytype, &plan, &need);
+  const md_status s = masked_plan(c, b, q_heads, mask, ytype, &plan, &need);
   if (s != MD_OK) return s;
+  if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
+  *bytes = need;
+  return ok();
+}
+
+}  // extern "C"
+
+// The launch of a planned call, its remaining checks in front.
+static md_status attend(const md_kv_cache* c, const md_kv_batch* b, const md::KvPlan& plan, size_t need, const void* q,
+                        int32_t xtype, int32_t q_heads, int64_t q_stride, float scale, int32_t causal, int32_t window,
+                        const md_kv_mask* mask, void* out, int32_t ytype, int64_t out_stride, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  md_status s;
   if (!valid_xtype(xtype)) return fail(MD_ERR_INVALID_ARG, "unknown xtype %d", xtype);
   if (!std::isfinite(scale)) return fail(MD_ERR_INVALID_ARG, "attention: scale %g", scale);
   if (b->rows == 0) return ok();
@@ -363,6 +397,12 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
   a.window = seen(b, window);
   a.pshift = c->page == 64 ? 6 : c->page == 128 ? 7 : 8;
   a.scale = scale;
+  if (mask) {
+    a.sinks = kept(b, mask);
+    a.tree = mask->tree;
+    a.words = mask->words;
+    a.masked = a.tree || a.sinks;  // a window alone is the plain form's
+  }
   a.tile = plan.tile;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
@@ -377,6 +417,50 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
   }
   const hipError_t e = md::launch_kv_attn(a, c->head_dim, ytype, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
+}
+
+extern "C" {
+
+md_status md_kv_attention_masked(const md_kv_cache* c, const md_kv_batch* b, const void* q, int32_t xtype,
+                                 int32_t q_heads, int64_t q_stride, float scale, const md_kv_mask* mask, void* out,
+                                 int32_t ytype, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  md::KvPlan plan;
+  size_t need = 0;
+  const md_status s = masked_plan(c, b, q_heads, mask, ytype, &plan, &need);
+  if (s != MD_OK) return s;
+  return attend(c, b, plan, need, q, xtype, q_heads, q_stride, scale, 1, mask->window, mask, out, ytype, out_stride,
+                workspace, workspace_bytes, stream);
+}
+
+md_status md_kv_tree(const md_kv_batch* b, const int32_t* parents, uint64_t* masks, int32_t words, int32_t* positions,
+                     hipStream_t stream) {
+  if (!b) return fail(MD_ERR_INVALID_ARG, "null batch descriptor");
+  if (b->n_seqs <= 0 || b->rows < 0 || b->max_q <= 0)
+    return fail(MD_ERR_SHAPE, "batch: n_seqs %d rows %d max_q %d", b->n_seqs, b->rows, b->max_q);
+  if (b->n_seqs > kMaxSeqs || b->rows > kMaxTokens || b->max_q > kMaxTree)
+    return fail(MD_ERR_UNSUPPORTED, "tree: n_seqs %d (at most %d), rows %d (%d), max_q %d (%d)", b->n_seqs, kMaxSeqs,
+                b->rows, kMaxTokens, b->max_q, kMaxTree);
+  if (words > kMaxWords) return fail(MD_ERR_UNSUPPORTED, "tree: %d words > %d", words, kMaxWords);
+  if (words < 1 || 64 * words < b->max_q) return fail(MD_ERR_SHAPE, "tree: %d words for runs of %d", words, b->max_q);
+  if (b->rows == 0) return ok();
+  if (!b->q_start || !b->kv_len || !parents || !masks) return fail(MD_ERR_INVALID_ARG, "tree: null pointer");
+  if (!aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(parents) || (positions && !aligned4(positions)) ||
+      (reinterpret_cast<uintptr_t>(masks) & 7u))
+    return fail(MD_ERR_ALIGNMENT, "tree: masks not 8-byte aligned, or another array not 4-byte");
+  const hipError_t e = md::launch_kv_tree(dev(b), parents, masks, words, positions, stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "tree launch");
+}
+
+md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void* q, int32_t xtype, int32_t q_heads,
+                          int64_t q_stride, float scale, int32_t causal, int32_t window, void* out, int32_t ytype,
+                          int64_t out_stride, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  md::KvPlan plan;
+  size_t need = 0;
+  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, ytype, &plan, &need);
+  if (s != MD_OK) return s;
+  return attend(c, b, plan, need, q, xtype, q_heads, q_stride, scale, causal, window, nullptr, out, ytype, out_stride,
+                workspace, workspace_bytes, stream);
 }
 
 md_status md_kv_pages_reset(md_kv_pages* p) {

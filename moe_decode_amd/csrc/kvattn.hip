@@ -98,18 +98,23 @@ MD_DEV float nan_f() { return __uint_as_float(0x7FC00000u); }
 // The sign of the score scale goes into the digits, so that a tile's factor is
 // never negative and the raw integer scores can be compared before they are
 // scaled.
-template <int D, int ND>
+template <int D, int ND, bool M>
 struct Column {
   i32x4 qd[ND][D / 64];
   float qscale, m, l;
   int hi, lo;  // the positions it sees
+  Seen seen;   // M: instead of them
 };
-template <int D, int ND>
-MD_DEV void column_init(Column<D, ND>& o, const KvAttn& a, const Seq& q, int h, int c, int cols, int g) {
+template <int D, int ND, bool M>
+MD_DEV void column_init(Column<D, ND, M>& o, const KvAttn& a, const Seq& q, int h, int c, int cols, int g) {
   const int cc = min(c, cols - 1), qt = cc / a.G, hq = h * a.G + (cc - qt * a.G);  // past the last one: that one again
   const int pos = q.len - q.nq + qt;
-  o.hi = a.causal ? pos : q.len - 1;
-  o.lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  if constexpr (M) {
+    o.seen = seen_of(a, q, qt);
+  } else {
+    o.hi = a.causal ? pos : q.len - 1;
+    o.lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  }
   float v[D / 64][16], poison = q.bad ? nan_f() : 0.0f;
   uint32_t top = 0;
 #pragma unroll
@@ -165,14 +170,21 @@ MD_DEV Scales scales_of(float ks, float vs) {
 // One tile's raw scores masked (where it is cut), the running maximum moved:
 // returns alpha for what has been summed so far, beta for what the tile's weights
 // give, and ref, the tile's own maximum, which they are relative to.
-template <int D, int ND>
-MD_DEV float advance(Column<D, ND>& o, float (&x)[16], float f, float off, bool cut, int first, float& ref,
-                     float& beta) {
+template <int D, int ND, bool M>
+MD_DEV float advance(Column<D, ND, M>& o, const KvAttn& a, const Seq& q, float (&x)[16], float f, float off, bool cut,
+                     int first, float& ref, float& beta) {
   if (cut) {
     keep_branch();
+    if constexpr (M) {
+      const uint32_t vis = seen16(a, q, o.seen, first);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (first + i > o.hi || first + i < o.lo) x[i] = -INFINITY;
+      for (int i = 0; i < 16; ++i)
+        if (!(vis >> i & 1u)) x[i] = -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (first + i > o.hi || first + i < o.lo) x[i] = -INFINITY;
+    }
   }
   float raw = x[0];
 #pragma unroll
@@ -239,10 +251,10 @@ constexpr int kMaxDealt = 1024;
 
 // The tiles that any column of a sequence sees, one at least where it has rows:
 // somebody has to write their zeros.
-MD_DEV int tiles_of(const KvAttn& a, const Seq& q, int cols, int& t0) {
-  const Span s = span_of(a, q, 0, cols);
-  t0 = s.t0;
-  return max(s.t1 - s.t0, 1);
+template <bool M>
+MD_DEV int tiles_of(const KvAttn& a, const Seq& q, int cols, Span& s) {
+  s = span_of<M>(a, q, 0, cols);
+  return max(s.head + s.t1 - s.t0, 1);
 }
 
 template <int D, int ND>
@@ -251,11 +263,13 @@ struct FewLds {
   float m[kWaves][16], l[kWaves][16];
 };
 
-// Tiles [t_begin, t_end) of head h's column tile ct.  slot < 0: they are all
-// that it sees, and the outputs are written; else the sums go to that slot.
-template <int D, int ND>
+// Tiles [t_begin, t_end) of head h's column tile ct; M: numbered with the
+// `head` first ones in front and `skip` left out behind them.  slot < 0: they
+// are all that it sees, and the outputs are written; else the sums go to that
+// slot.
+template <int D, int ND, bool M>
 MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, const Span& sp, int t_begin, int t_end,
-                        int slot, FewLds<D, ND>& lds) {
+                        int head, int skip, int slot, FewLds<D, ND>& lds) {
   constexpr int DT = D / 16;
   auto& s_acc = lds.acc;
   auto& s_m = lds.m;
@@ -276,12 +290,13 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
                          : (16 * (col >> 2) + (col & 3)) * D + 16 * g;
   const int voff = (col << pshift) + 16 * g;
   i32x4 kf[KI][KK], vf[DT];
+  auto tile_of = [&](int t) { return M && t >= head ? t + skip : t; };
   // a page that is none reads page 0 and counts as one with scale NaN
-  auto page_at = [&](int t) { return t < t_end ? q.table[t * kTile >> pshift] : 0; };
+  auto page_at = [&](int t) { return t < t_end ? q.table[tile_of(t) * kTile >> pshift] : 0; };
   // buffer loads: past the last tile the resources are empty, and the same
   // loads read zeros without memory traffic
   auto load_k = [&](int t, int page) {
-    const int sub = (t * kTile) & ((1 << pshift) - 1);
+    const int sub = (tile_of(t) * kTile) & ((1 << pshift) - 1);
     const rsrc_t r = make_res(c.k + ((((int64_t)page * c.Hkv + h) << pshift) + sub) * D, t < t_end ? kTile * D : 0);
 #pragma unroll
     for (int i = 0; i < KI; ++i)
@@ -289,7 +304,7 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
       for (int k = 0; k < KK; ++k) kf[i][k] = load16<kAuxStream>(r, koff + (kWide ? 2 : 4) * i * D + 128 * k, 0);
   };
   auto load_v = [&](int t, int page) {
-    const int sub = (t * kTile) & ((1 << pshift) - 1);
+    const int sub = (tile_of(t) * kTile) & ((1 << pshift) - 1);
     const rsrc_t r = make_res(c.v + (((int64_t)page * c.Hkv + h) << pshift) * D + sub, t < t_end ? (D << pshift) - sub : 0);
 #pragma unroll
     for (int i = 0; i < DT; ++i) vf[i] = load16<0>(r, voff, (16 * i) << pshift);
@@ -302,8 +317,8 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
   load_k(t, page);
   load_v(t, page);
   float ks = c.k_scale[(int64_t)page * c.Hkv + h], vs = c.v_scale[(int64_t)page * c.Hkv + h];
-  Column<D, ND> o;
-  column_init<D, ND>(o, a, q, h, ct * 16 + col, cols, g);
+  Column<D, ND, M> o;
+  column_init<D, ND, M>(o, a, q, h, ct * 16 + col, cols, g);
   float acc[DT][4];
 #pragma unroll
   for (int i = 0; i < DT; ++i)
@@ -347,9 +362,9 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
       vs = c.v_scale[(int64_t)page * c.Hkv + h];
       const float f = fmaxf(o.qscale * sc.ks, 1e-37f);
       float ref, beta;
-      const int base = t * kTile;
-      const float alpha = advance<D, ND>(o, x, f, sc.off, base + kTile - 1 > sp.full_hi || base < sp.full_lo,
-                                         base + 16 * g, ref, beta);
+      const int base = tile_of(t) * kTile;
+      const float alpha = advance<D, ND, M>(o, a, q, x, f, sc.off, base + kTile - 1 > sp.full_hi || base < sp.full_lo,
+                                            base + 16 * g, ref, beta);
       i32x4 pd[kWeightDigits];
       o.l = fmaf(beta, weights(x, f, ref, pd), o.l * alpha);
       const float fv = sc.vs * (1.0f / Digits<kWeightDigits>::top) * beta;
@@ -407,7 +422,7 @@ MD_DEV void few_columns(const KvAttn& a, const Seq& q, int h, int ct, int cols, 
   if (slot >= 0 && part == 0) reinterpret_cast<float2*>(a.part_m)[at] = make_float2(mm, ll);
 }
 
-template <int D, int ND>
+template <int D, int ND, bool M>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAttn a) {
   __shared__ __attribute__((aligned(16))) FewLds<D, ND> lds;
   __shared__ int64_t first[kMaxDealt + 1], waves[kWaves];
@@ -425,8 +440,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
       int64_t n = 0;
       if (e < a.b.S) {
         const Seq q = seq_of(a.b, e, a.c.page);
-        int t0;
-        if (q.nq) n = (int64_t)((q.nq * a.G + 15) / 16) * Hkv * tiles_of(a, q, q.nq * a.G, t0);
+        Span all;
+        if (q.nq) n = (int64_t)((q.nq * a.G + 15) / 16) * Hkv * tiles_of<M>(a, q, q.nq * a.G, all);
         first[e] = sum;
       }
       sum += n;
@@ -466,8 +481,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     s = __builtin_amdgcn_readfirstlane(s);
     const Seq q = seq_of(a.b, s, a.c.page);
     const int cols = q.nq * a.G, cts = (cols + 15) / 16;
-    int t0, seg = plain_seg, from = 0;
-    const int n = cols ? tiles_of(a, q, cols, t0) : 0;
+    int seg = plain_seg, from = 0;
+    Span all{};
+    const int n = cols ? tiles_of<M>(a, q, cols, all) : 0;
     int to = n;
     if (a.pieces) {
       const int64_t in = u - first[s];
@@ -478,13 +494,21 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
       return;
     }
     const int h = __builtin_amdgcn_readfirstlane(seg / cts), ct = seg - h * cts;
-    const Span sp = span_of(a, q, ct * 16, min(ct * 16 + 16, cols));
+    const Span sp = span_of<M>(a, q, ct * 16, min(ct * 16 + 16, cols));
     // the first one's share of a workgroup goes to its slot 0, the last one's to 1
     const int slot = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (again ? 1 : 0);
     if (again) __syncthreads();  // the LDS of the one before
     // (said to be the same in all lanes, or every load would ask each of them)
-    few_columns<D, ND>(a, q, h, ct, cols, sp, __builtin_amdgcn_readfirstlane(max(t0 + from, sp.t0)),
-                       __builtin_amdgcn_readfirstlane(min(t0 + to, sp.t1)), slot, lds);
+    int lo = max(all.t0 + from, sp.t0), hi = min(all.t0 + to, sp.t1), skip = 0;
+    if constexpr (M) {
+      // of the sequence's tiles in order those that this column tile sees
+      skip = all.t0 - all.head;
+      lo = from < all.head || sp.head > all.t0 ? from : max(from, sp.t0 - skip);
+      hi = min(to, sp.t1 - skip);
+    }
+    few_columns<D, ND, M>(a, q, h, ct, cols, sp, __builtin_amdgcn_readfirstlane(lo),
+                          __builtin_amdgcn_readfirstlane(hi), __builtin_amdgcn_readfirstlane(all.head),
+                          __builtin_amdgcn_readfirstlane(skip), slot, lds);
     if (!a.pieces) return;
     if (from == 0 && to < n && tid == 0) {
       const int64_t last = ((first[s] + (int64_t)(seg + 1) * n) * runs - 1) / total;  // the run with its last tile
@@ -559,7 +583,7 @@ MD_DEV void paced() {
   __builtin_amdgcn_sched_group_barrier(0x008, kAhead * NS, GROUP);
 }
 
-template <int D, int NS>
+template <int D, int NS, bool M>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a) {
   constexpr int KS = D / 16, DT = D / 32;
   constexpr float kLag = NS == 1 ? 7.0f : 0.0f, kUnit = NS == 1 ? 128.0f : 16384.0f;
@@ -574,24 +598,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   const int cols = q.nq * a.G;
   const int ct = column_tile(a, rest / c.Hkv, (int)(gridDim.x / (a.splits * c.Hkv)));
   if (ct * kRowCols >= cols) return;
-  const Span sp = span_of(a, q, ct * kRowCols, min(ct * kRowCols + kRowCols, cols));
-  const int per = a.chunk, active = max(1, (sp.t1 - sp.t0 + per - 1) / per);
+  const Span sp = span_of<M>(a, q, ct * kRowCols, min(ct * kRowCols + kRowCols, cols));
+  const int per = a.chunk, active = max(1, (sp.head + sp.t1 - sp.t0 + per - 1) / per);
   if (split >= active) return;
-  const int t_begin = sp.t0 + split * per, t_end = min(t_begin + per, sp.t1);
+  // M: tiles numbered with the `head` first ones in front
+  const int skip = sp.t0 - sp.head;
+  const int t_begin = M ? split * per : sp.t0 + split * per, t_end = min(t_begin + per, M ? sp.t1 - skip : sp.t1);
+  auto tile_of = [&](int t) { return M && t >= sp.head ? t + skip : t; };
   const int c0 = ct * kRowCols + wave * 32;
   const bool any = c0 < cols;  // a wave past the last column only helps with the loads
-  const Span mine = span_of(a, q, any ? c0 : 0, any ? min(c0 + 32, cols) : 1);
+  const Span mine = span_of<M>(a, q, any ? c0 : 0, any ? min(c0 + 32, cols) : 1);
 
   const int pshift = a.pshift;
   u32x4 kr[L], vr[L];
   float ks_n, vs_n;
-  auto page_at = [&](int t) { return t < t_end ? q.table[t * kTile >> pshift] : 0; };
+  auto page_at = [&](int t) { return t < t_end ? q.table[tile_of(t) * kTile >> pshift] : 0; };
   int next = page_at(t_begin);  // the page of the tile that is loaded next, read a tile ahead
   auto load = [&](int t) {      // tile t's codes and scales; a page that is none is page 0 with a scale that is none
     const int id = __builtin_amdgcn_readfirstlane(next);
     next = page_at(t + 1);
     const bool good = (unsigned)id < (unsigned)c.n_pages;
-    const int page = good ? id : 0, sub = (t * kTile) & ((1 << pshift) - 1);
+    const int page = good ? id : 0, sub = (tile_of(t) * kTile) & ((1 << pshift) - 1);
     const int64_t ph = (int64_t)page * c.Hkv + h;
     ks_n = good ? c.k_scale[ph] : -1.0f;
     vs_n = c.v_scale[ph];
@@ -640,6 +667,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   const int cc = min(c0 + col, cols - 1), qt = cc / a.G, hq = h * a.G + (cc - qt * a.G);
   const int pos = q.len - q.nq + qt;
   const int hi = a.causal ? pos : q.len - 1, lo = a.window ? max(pos - a.window + 1, 0) : 0;
+  Seen seen{};
+  if constexpr (M) seen = seen_of(a, q, qt);
   f16x8 qf[NS][KS];
   float m = -INFINITY, l = q.bad ? nan_f() : 0.0f, qscale;
   {
@@ -687,7 +716,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   __syncthreads();
   int buf = 0;
   for (int t = t_begin; t < t_end; ++t, buf ^= 1) {
-    if (any && t < mine.t1 && t >= mine.t0) {
+    const int here = tile_of(t);
+    if (any && here < mine.t1 && (here >= mine.t0 || (M && here < mine.head))) {
       f32x16 x[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -703,14 +733,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
           for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
         }
       paced<2 * KS, NS, 0>();
-      const int base = t * kTile, first = base + 16 * hh;
+      const int base = here * kTile, first = base + 16 * hh;
       if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
         keep_branch();
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b) {
+          if constexpr (M) {
+            const uint32_t vis = seen16(a, q, seen, first + 32 * b);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (first + 32 * b + i > hi || first + 32 * b + i < lo) x[b][i] = -INFINITY;
+            for (int i = 0; i < 16; ++i)
+              if (!(vis >> i & 1u)) x[b][i] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (first + 32 * b + i > hi || first + 32 * b + i < lo) x[b][i] = -INFINITY;
+          }
+        }
       }
       const float f = fmaxf(qscale * sc.ks, 1e-37f);
       float raw = x[0][0];
@@ -812,8 +850,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttn a) {
   if ((int)blockIdx.x >= q.nq) return;
   const int64_t row = (int64_t)q.row0 + blockIdx.x, slot0 = (row * (a.G * a.c.Hkv) + head) * a.splits;
   const int cols = q.nq * a.G, ct = ((int)blockIdx.x * a.G + head % a.G) / a.tile;
-  const Span sp = span_of(a, q, ct * a.tile, min(ct * a.tile + a.tile, cols));
-  const int active = (sp.t1 - sp.t0 + a.chunk - 1) / a.chunk;
+  const int c1 = min(ct * a.tile + a.tile, cols);
+  const Span sp = a.masked ? span_of<true>(a, q, ct * a.tile, c1) : span_of<false>(a, q, ct * a.tile, c1);
+  const int active = (sp.head + sp.t1 - sp.t0 + a.chunk - 1) / a.chunk;
   if (active <= 1) return;
   const float2* ml = reinterpret_cast<const float2*>(a.part_m) + slot0;
   float m = -INFINITY;
@@ -890,10 +929,15 @@ __global__ __launch_bounds__(256) void k_kv_join_pieces(KvAttn a) {
   store_out4(a, (int64_t)q.row0 + qt, h * a.G + (c - qt * a.G), D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int causal, int yt) {
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt) {
   int64_t most = b.max_kv;
   if (causal && window && (int64_t)window + b.max_q < most) most = (int64_t)window + b.max_q;
-  const int64_t tiles = (most + kTile - 1) / kTile + 1;
+  int64_t tiles = (most + kTile - 1) / kTile + 1;
+  if (sinks) {  // and those of the first positions, before the window's
+    const int64_t all = ((int64_t)b.max_kv + kTile - 1) / kTile + 1;
+    tiles += (sinks + kTile - 1) / kTile;
+    if (tiles > all) tiles = all;
+  }
   KvPlan p{};
   // More than four column tiles: the form that shares its loads among 128
   // columns (80 columns, 16 sequences of 4000: 41 us, 51 in the other one; 64:
@@ -937,10 +981,15 @@ hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
   const dim3 grid = a.pieces ? dim3(a.pieces) : dim3((unsigned)(a.splits * cts * a.c.Hkv), a.b.S), block(64 * kWaves);
   const int64_t groups = (int64_t)grid.x * grid.y;
   a.snake = groups > device_cus() && groups <= 2 * device_cus();
-#define MD_ATT(D_, N_)                                                                     \
+#define MD_ATT_M(D_, N_, M_)                                                               \
   do {                                                                                     \
-    if (a.tile == 16) hipLaunchKernelGGL((k_kv_attn<D_, N_>), grid, block, 0, st, a);      \
-    else hipLaunchKernelGGL((k_kv_attn_rows<D_, N_ - 1>), grid, block, 0, st, a);          \
+    if (a.tile == 16) hipLaunchKernelGGL((k_kv_attn<D_, N_, M_>), grid, block, 0, st, a);  \
+    else hipLaunchKernelGGL((k_kv_attn_rows<D_, N_ - 1, M_>), grid, block, 0, st, a);      \
+  } while (0)
+#define MD_ATT(D_, N_)                   \
+  do {                                   \
+    if (a.masked) MD_ATT_M(D_, N_, true); \
+    else MD_ATT_M(D_, N_, false);        \
   } while (0)
   if (yt == XF32) {
     if (D == 64) MD_ATT(64, 3);
@@ -952,6 +1001,7 @@ hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
     else MD_ATT(256, 2);
   }
 #undef MD_ATT
+#undef MD_ATT_M
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.splits == 1 && !a.pieces)) return e;
 #define MD_JOIN(D_)                                                                                                   \

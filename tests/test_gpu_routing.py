@@ -1,0 +1,173 @@
+"""Routing on the GPU: the experts are the definition's, from logits in 64 bits
+rounded once; gates within the rounding of their last step."""
+import numpy as np
+import pytest
+
+from . import step_model as M
+from .gpu_common import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _inputs(rng, T, H, E, xt):
+    import torch
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32))
+    x = x.to({"f32": torch.float32, "bf16": torch.bfloat16}[xt])
+    W = (1.5 / np.sqrt(H) * rng.standard_normal((E, H))).astype(np.float32)
+    return x.cuda(), torch.from_numpy(W).cuda(), x.float().numpy().astype(np.float64) @ W.astype(np.float64).T
+
+
+def _check(x, W, exact, k, score="softmax", balance=None, groups=1, kept=1, best_two=False, renorm=True, scale=1.0,
+           bias=None):
+    import moe_decode_amd as md
+    import torch
+    dev = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    r = md.Routing(k, score, dev(balance), groups, kept, best_two, renorm, scale)
+    T, E = exact.shape
+    logits = torch.empty(T, E, device="cuda")
+    idx, gates = md.moe_route(x, W, r, bias=dev(bias), logits=logits)
+    l = (exact if bias is None else exact + bias.astype(np.float64)).astype(np.float32)
+    got = logits.cpu().numpy()
+    # the sum's last bits may fall on the other side of a tie of fp32: one step
+    assert (np.abs(got - l) <= np.spacing(np.abs(l))).all() and (got != l).mean() < 1e-4
+    idx, gates = idx.cpu().numpy(), gates.cpu().numpy()
+    for t in range(T):
+        won, g = M.route(got[t], k, score, balance, groups, kept, best_two, renorm, scale)
+        assert idx[t].tolist() == won, (t, idx[t].tolist(), won)
+        assert (np.abs(gates[t] - g) <= M.U * np.abs(g) * 1.001 + 1e-45).all(), (t, gates[t], g)
+
+
+OPTIONS = [dict(), dict(score="sigmoid"), dict(score="sigmoid", balance=0.1, groups=4, kept=2, best_two=True, scale=2.5),
+           dict(balance=0.02, renorm=False), dict(groups=2, kept=1), dict(score="sigmoid", groups=4, kept=3, renorm=False),
+           dict(groups=4, kept=4, best_two=True), dict(score="sigmoid", bias=1.0, balance=0.05)]
+
+
+@pytest.mark.parametrize("T,H,E", [(1, 256, 8), (1, 2048, 128), (3, 6144, 256), (8, 512, 60), (9, 512, 60), (17, 2048, 128),
+                                   (128, 6144, 256), (65, 768, 4), (300, 256, 160), (1000, 512, 64)])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_sizes_and_options(T, H, E, xt):
+    rng = np.random.default_rng(T + E)
+    x, W, exact = _inputs(rng, T, H, E, xt)
+    for o in OPTIONS:
+        o = dict(o)
+        for name in ("balance", "bias"):
+            if name in o:
+                o[name] = (o[name] * rng.standard_normal(E)).astype(np.float32)
+        n = E // o.get("groups", 1)
+        if o.get("best_two") and n < 2:
+            continue
+        _check(x, W, exact, min(8, n * o.get("kept", 1)), **o)
+    _check(x, W, exact, 1)
+
+
+@pytest.mark.parametrize("E,groups,kept", [(64, 64, 8), (256, 64, 7), (96, 3, 2), (160, 5, 4), (120, 40, 3), (6, 2, 1),
+                                           (2, 1, 1)])
+def test_group_shapes(E, groups, kept):
+    rng = np.random.default_rng(E)
+    for T in (2, 40):
+        x, W, exact = _inputs(rng, T, 512, E, "f32")
+        k = min(8, kept * (E // groups))
+        _check(x, W, exact, k, "sigmoid", (0.1 * rng.standard_normal(E)).astype(np.float32), groups, kept)
+        if E // groups > 1:
+            _check(x, W, exact, k, "softmax", None, groups, kept, True)
+
+
+@pytest.mark.parametrize("T", [2, 50])
+def test_equal_scores_go_to_the_lower_run_and_expert(T):
+    """Experts with the same row of weights, and a row of zeros."""
+    import torch
+    rng = np.random.default_rng(T)
+    x, W, exact = _inputs(rng, T, 256, 64, "f32")
+    W[32:] = W[:32]
+    exact[:, 32:] = exact[:, :32]
+    x[1] = 0.0
+    exact[1] = 0.0
+    for score in ("softmax", "sigmoid"):
+        _check(x, W, exact, 8, score)
+        _check(x, W, exact, 8, score, None, 8, 3)
+        _check(x, W, exact, 8, score, None, 8, 3, True)
+        _check(x, W, exact, 6, score, np.tile(np.float32([0.25, 0.5]), 32), 4, 2)
+
+
+@pytest.mark.parametrize("T", [2, 50])
+def test_far_logits_and_closed_experts(T):
+    """Logits past exp's range, experts closed by a balance of -inf."""
+    rng = np.random.default_rng(T)
+    x, W, exact = _inputs(rng, T, 256, 32, "f32")
+    bias = np.zeros(32, np.float32)
+    bias[3], bias[9] = 900.0, -900.0
+    _check(x, W, exact, 3, "softmax", bias=bias)
+    _check(x, W, exact, 8, "sigmoid", bias=bias)
+    shut = np.zeros(32, np.float32)
+    shut[5:] = -np.inf
+    _check(x, W, exact, 8, "sigmoid", shut)
+    _check(x, W, exact, 4, "softmax", shut, 4, 2)
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_nan_keeps_to_its_token(T):
+    import moe_decode_amd as md
+    import torch
+    rng = np.random.default_rng(T)
+    x, W, _ = _inputs(rng, T, 512, 60, "f32")
+    r = md.Routing(6, "sigmoid", groups=4, groups_kept=2)
+    idx, gates = md.moe_route(x, W, r)
+    x[1, 7] = float("nan")
+    idx2, gates2 = md.moe_route(x, W, r)
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(idx[keep], idx2[keep]) and torch.equal(gates[keep], gates2[keep])
+    got = idx2[1].tolist()
+    assert len(set(got)) == 6 and all(0 <= e < 60 for e in got)
+
+
+def test_rows_behind_and_captured_calls():
+    import moe_decode_amd as md
+    import torch
+    rng = np.random.default_rng(4)
+    for T in (5, 200):
+        x, W, _ = _inputs(rng, T, 512, 128, "bf16")
+        r = md.Routing(8, "sigmoid", torch.rand(128, device="cuda"), 8, 4, True, scale=2.0)
+        idx = torch.full((T + 1, 8), -3, dtype=torch.int32, device="cuda")
+        gates = torch.full((T + 1, 8), -3.0, device="cuda")
+        md.moe_route(x, W, r, idx=idx[:T], gates=gates[:T])
+        assert (idx[T] == -3).all() and (gates[T] == -3.0).all()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gi, gg = md.moe_route(x, W, r)
+        for i in range(3):
+            x.copy_(torch.randn(T, 512, device="cuda"))
+            graph.replay()
+            torch.cuda.synchronize()
+            ei, eg = md.moe_route(x, W, r)
+            assert torch.equal(gi, ei) and torch.equal(gg, eg)
+    i0, g0 = md.moe_route(x[:0], W, r)
+    assert i0.shape == (0, 8) and g0.shape == (0, 8)
+
+
+@pytest.mark.parametrize("T", [1, 5, 33])
+def test_the_layer_with_a_routing(T):
+    """moe_layer_forward(routing=...) is moe_route and moe_experts_forward; a softmax
+    over the chosen ones is the layer's own routing."""
+    import moe_decode_amd as md
+    import torch
+
+    from .gpu_common import moe_layer
+    layer = moe_layer("c3")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, layer.H, generator=g, device="cuda")
+    r = md.Routing(layer.k, "sigmoid", 0.05 * torch.randn(layer.E, generator=g, device="cuda"), 8, 4, True, scale=2.5)
+    idx, gates = md.moe_route(x, layer.Wr, r, bias=layer.bias)
+    want = md.moe_experts_forward(layer, x, idx, gates)
+    i2, g2 = torch.empty_like(idx), torch.empty_like(gates)
+    y = md.moe_layer_forward(layer, x, idx=i2, gates=g2, routing=r)
+    assert torch.equal(y, want) and torch.equal(i2, idx) and torch.equal(g2, gates)
+    assert torch.equal(md.moe_layer_forward(layer, x, routing=r), want)
+    i3, g3 = torch.empty_like(idx), torch.empty_like(gates)
+    md.moe_layer_forward(layer, x, idx=i3, gates=g3)
+    i4, g4 = md.moe_route(x, layer.Wr, md.Routing(layer.k), bias=layer.bias)
+    assert torch.equal(i3, i4) and (g3 - g4).abs().max() <= 2.0 ** -23
