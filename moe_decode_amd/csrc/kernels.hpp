@@ -261,20 +261,26 @@ hipError_t launch_qk_norm_rope(const RopeArgs& g, bool pairs, int xt, int yt, hi
 
 // ---- routing (routing.hip) ---------------------------------------------------
 constexpr int kRouteFew = 8;  // tokens of the form that has a workgroup for each expert
+constexpr int64_t kRouteFast = 4000000000;  // operations from which the logits are bounded on the bf16 matrix cores first
 struct RouteArgs {
   double* part;               // [S][T][E]
-  int S, T, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
+  int S, T, H, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
   float scale;
   const float *bias, *balance;
   float* logits;
   int* idx;
   float* gates;
+  float *wnorm, *xnorm, *most;  // squared norms [H / 256][E], [S][T]; [2]: the largest row's, of a finite balance
+  int *count, *list;          // [1], [T]: tokens that are done in fp64
 };
 struct RoutePlan {
   int S, Ks;  // slices of the width and the width of one
+  bool fast;
+  size_t planes, wnorm, most, xnorm, count, list, part, bytes;  // the workspace's parts and size
 };
-RoutePlan route_plan(int64_t T, int H, int E);
-hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, int xt, int H, const float* Wr, hipStream_t st);
+RoutePlan route_plan(int64_t T, int H, int E, bool fast);
+hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, int xt, const float* Wr, void* ws,
+                        hipStream_t st);
 
 // ---- log probabilities (logprob.hip) ----------------------------------------
 constexpr int kMaxTop = 32;

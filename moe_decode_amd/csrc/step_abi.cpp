@@ -139,7 +139,9 @@ md_status md_moe_route_workspace_size(int32_t T, int32_t H, int32_t E, size_t* b
   const md_status s = check_route(T, H, E);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
-  *bytes = T ? align256(sizeof(double) * (size_t)T * E * md::route_plan(T, H, E).S) : 0;
+  // with and without the logits' rounded values, which one form gives
+  const size_t a = T ? md::route_plan(T, H, E, true).bytes : 0, b = T ? md::route_plan(T, H, E, false).bytes : 0;
+  *bytes = a > b ? a : b;
   return ok();
 }
 
@@ -158,11 +160,10 @@ md_status md_moe_route(const md_routing* r, const void* x, int32_t xtype, int32_
   if (!workspace || workspace_bytes < need)
     return fail(MD_ERR_WORKSPACE, "workspace: %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
   if (!aligned16(workspace)) return fail(MD_ERR_ALIGNMENT, "workspace not 16-byte aligned");
-  const md::RoutePlan p = md::route_plan(T, H, E);
+  const md::RoutePlan p = md::route_plan(T, H, E, !logits);
   md::RouteArgs g{};
-  g.part = static_cast<double*>(workspace);
-  g.S = p.S;
   g.T = T;
+  g.H = H;
   g.E = E;
   g.k = r->k;
   g.sigmoid = r->score == MD_SCORE_SIGMOID;
@@ -178,7 +179,7 @@ md_status md_moe_route(const md_routing* r, const void* x, int32_t xtype, int32_
   g.logits = logits;
   g.idx = idx;
   g.gates = gates;
-  const hipError_t e = md::launch_route(g, p, x, xtype, H, W_r, stream);
+  const hipError_t e = md::launch_route(g, p, x, xtype, W_r, workspace, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "routing launch");
 }
 

@@ -171,3 +171,92 @@ def test_the_layer_with_a_routing(T):
     md.moe_layer_forward(layer, x, idx=i3, gates=g3)
     i4, g4 = md.moe_route(x, layer.Wr, md.Routing(layer.k), bias=layer.bias)
     assert torch.equal(i3, i4) and (g3 - g4).abs().max() <= 2.0 ** -23
+
+
+# ---- many tokens: logits bounded first ---------------------------------------
+
+def _off(x, W):
+    """How far the bounded form's logits may be off: 2^-19 |x| |w|, and one step of
+    fp32 that the definition's rounding has."""
+    l = x.double() @ W.double().t()
+    n = x.double().norm(dim=1, keepdim=True) * W.double().norm(dim=1).max()
+    return (2.0 ** -19 * n + 2.0 ** -23 * l.abs().amax(1, keepdim=True)).cpu().numpy()
+
+
+MANY = [(2100, 4096, 256, "f32"), (8191, 1024, 256, "bf16"), (9001, 2304, 100, "f32"), (1100, 8192, 256, "bf16"),
+        (4000, 6144, 129, "bf16")]
+
+
+@pytest.mark.parametrize("T,H,E,xt", MANY)
+@pytest.mark.parametrize("kind", ["random", "close", "same", "positive"])
+def test_many_tokens_choose_as_few(T, H, E, xt, kind):
+    """The experts are those of the form that keeps every logit in fp64 (a call that
+    asks for the logits); a gate is off by what its logit's bound allows.  `close`:
+    experts that differ in the last bits of their weights, `same`: pairs of equal
+    ones, `positive`: sums without any cancellation."""
+    import moe_decode_amd as md
+    import torch
+    assert 2 * T * H * E >= 4e9
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(E, H, generator=g, device="cuda") * (1.5 / H ** 0.5)
+    if kind == "positive":
+        x, W = x.abs(), W.abs() / H ** 0.5
+    if kind in ("close", "same"):
+        W[E // 2:] = W[:E - E // 2] * (1 + 2.0 ** -22 if kind == "close" else 1)
+    x = x.to({"f32": torch.float32, "bf16": torch.bfloat16}[xt])
+    logits = torch.empty(T, E, device="cuda")
+    off = _off(x, W)
+    for r in (md.Routing(8, "sigmoid", 0.05 * torch.randn(E, generator=g, device="cuda"), scale=2.5),
+              md.Routing(6, renorm=False), md.Routing(3, "softmax", 0.5 / E * torch.randn(E, generator=g, device="cuda")),
+              md.Routing(4, "sigmoid", groups=2 if E % 2 == 0 else 1, best_two=True)):
+        idx, gates = md.moe_route(x, W, r)
+        want, wg = md.moe_route(x, W, r, logits=logits)
+        assert torch.equal(idx, want), (idx != want).any(1).nonzero()[:4].tolist()
+        # a score moves by the factor exp(2 off) at most, a sum of them too
+        err, wg = (gates - wg).abs().cpu().numpy(), wg.abs().cpu().numpy()
+        assert (err <= wg * (4.1 * off + 4 * M.U)).all(), float((err / wg).max())
+
+
+def test_many_tokens_special_values():
+    """Zeros (all experts equal), NaN and infinities in some tokens, closed experts,
+    weights near the smallest normal numbers."""
+    import moe_decode_amd as md
+    import torch
+    T, H, E = 2100, 4096, 256
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(E, H, generator=g, device="cuda") * (1.5 / H ** 0.5)
+    logits = torch.empty(T, E, device="cuda")
+    shut = torch.zeros(E, device="cuda")
+    shut[10:] = float("-inf")
+    x[3], x[7, 9], x[8, 1], x[2099, 0] = 0.0, float("nan"), float("inf"), 3e38
+    x[64:128] *= 1e-30
+    for w in (W, torch.zeros_like(W), W * 1e-37):
+        for r in (md.Routing(8, "sigmoid"), md.Routing(8, "sigmoid", shut), md.Routing(2, "softmax", None, 8, 3)):
+            idx, gates = md.moe_route(x, w, r)
+            want, wg = md.moe_route(x, w, r, logits=logits)
+            keep = torch.isfinite(x).all(1)
+            assert torch.equal(idx[keep], want[keep])
+            ok = torch.isclose(gates, wg, rtol=1e-3, atol=0, equal_nan=True)
+            assert ok[keep].all()
+            assert ((idx >= 0) & (idx < E)).all() and (idx.sort(1).values.diff(dim=1) > 0).all()
+
+
+def test_many_tokens_captured():
+    import moe_decode_amd as md
+    import torch
+    T, H, E = 2100, 4096, 256
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    W = torch.randn(E, H, device="cuda") * (1.5 / H ** 0.5)
+    r = md.Routing(8, "sigmoid", None, 8, 4, True)
+    graph = torch.cuda.CUDAGraph()
+    md.moe_route(x, W, r)
+    with torch.cuda.graph(graph):
+        gi, gg = md.moe_route(x, W, r)
+    for i in range(3):
+        x.copy_(torch.randn(T, H, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ei, eg = md.moe_route(x, W, r)
+        assert torch.equal(gi, ei) and torch.equal(gg, eg)
