@@ -284,21 +284,24 @@ hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, i
 
 // ---- log probabilities (logprob.hip) ----------------------------------------
 constexpr int kMaxTop = 32;
-constexpr int kMaxChunks = 128;                                   // of a row, or one more
-constexpr int kMaxJoin = ((kMaxChunks + 1) * kMaxTop + 63) / 64;  // keys of a row's chunks, for each of 64 lanes
+constexpr int kMaxSegs = 128;                               // of a row
+constexpr int kMaxJoin = (kMaxSegs * kMaxTop + 63) / 64;    // keys of a row's segments, for each of 64 lanes
+constexpr int kSegGroups = 6;                               // workgroups a compute unit that a row is split for
 struct LogpArgs {
   const void* logits;
   int64_t stride, rows;
-  int vocab, n_tokens, top, chunks;
+  int vocab, n_tokens, top, segs, steps;
   const int* tokens;
   float scale;
   float *logprobs, *entropy;
   int* top_ids;
   float* top_logprobs;
-  void *part, *keys;  // [rows][chunks] of 16 bytes, [rows][chunks][top] of 8
+  void *part, *keys;  // [rows][segs] of 16 bytes, [rows][segs][top] of 8
 };
-int logprob_values(int64_t rows, int vocab);
-int logprob_chunks(int64_t rows, int vocab);
+struct LogpPlan {
+  int values, segs, steps;  // values a thread and step, segments of a row, steps of a segment
+};
+LogpPlan logprob_plan(int64_t rows, int vocab);
 hipError_t launch_logprob(const LogpArgs& g, int xt, int values, hipStream_t st);
 
 }  // namespace md

@@ -3,19 +3,27 @@
 //
 //   z = scale x,  log p = z - log sum exp z,  entropy = log sum exp z - sum z exp z / sum exp z
 //
-// Bound by the one read of the logits.  A workgroup takes a chunk of a row into
-// registers, 32 values a thread (8 where there are few chunks), and leaves for
-// it the maximum, the sums of exp and z exp relative to it, and the chunk's
-// `top` largest values as 64-bit keys: the order of fp32 in the high word, the
-// complement of the id in the low one, so that keys are all different, an
-// integer comparison is the order, and equal logits go to the lower id.  A row
-// of one chunk is finished there, else by a second kernel, a wave for each row.
+// Bound by the one read of the logits.  A workgroup takes a segment of a row, some
+// steps of N values a thread in registers, the next step's on their way; a thread
+// keeps its maximum and its sums of exp and z exp relative to it.  It leaves the
+// segment's, and its `top` largest values as 64-bit keys: the order of fp32 in the
+// high word, the complement of the id in the low one, so that keys are all
+// different, an integer comparison is the order, and equal logits go to the lower
+// id.  A row of one segment is finished there, else by a second kernel, a wave for
+// each row.
 //
-// The largest of a wave's values: its 64 lanes' own maxima are sorted, and the
-// `top`-th of them is a bound that at least `top` values reach.  Only values of
-// those `top` lanes can (the keys differ), so at most top values a lane, and
-// usually little more than top, pass into LDS, where each counts the larger
-// ones: its rank.
+// The largest: of each wave's 64 lanes the maxima of the first step are sorted; at
+// least `top` values reach the `top`-th of them, and the highest of the four waves'
+// bounds lets little more than `top` values pass into LDS.  Later steps use the
+// same bound until many have passed; then the list is ranked (each key counts the
+// larger ones), cut to `top`, and the bound is its last.  A step that would
+// overfill it (equal or ascending logits) has its winners taken one at a time.
+//
+// Measured: 4096 rows of 32000 fp32 logits without alternatives 88 us (524 MB, 6.0
+// TB/s); 288 rows of 131071 bf16 with the 8 largest 32 us and 4.6 for the join (75
+// MB: the vector ALU's work a value, not memory; a step a workgroup, bounds and
+// sums joined for each, 44 and 10).  Three or twelve workgroups a compute unit
+// instead of six: 39 and 38 us against 37 with the join.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -31,21 +39,40 @@ typedef unsigned long long Key;
 MD_DEV uint32_t order_of(float x) { return x == x ? order_key32(x) : 1u; }
 MD_DEV Key key_of(float x, int id) { return (Key)order_of(x) << 32 | (uint32_t)~id; }
 
-// The n-th largest (n in 1..64) of the wave's keys, one a lane.
-MD_DEV Key wave_nth(Key k, int n) {
+// The n-th largest (n in 1..64) of the wave's values, one a lane.
+template <int OFF>
+MD_DEV Key other(Key k) {
+  const float lo = xor_lanes<OFF>(__uint_as_float((uint32_t)k)), hi = xor_lanes<OFF>(__uint_as_float((uint32_t)(k >> 32)));
+  return (Key)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+template <int OFF>
+MD_DEV float other(float v) { return xor_lanes<OFF>(v); }
+template <int SIZE, int OFF, typename V>
+MD_DEV V sort_step(V v) {
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int size = 2; size <= 64; size <<= 1)
-#pragma unroll
-    for (int off = size >> 1; off; off >>= 1) {
-      const Key o = __shfl_xor(k, off, 64);
-      const bool up = ((lane & size) == 0) == ((lane & off) == 0);  // this lane keeps the larger one
-      k = (k > o) == up ? k : o;
-    }
-  return __shfl(k, n - 1, 64);
+  const V o = other<OFF>(v);
+  const bool up = ((lane & SIZE) == 0) == ((lane & OFF) == 0);  // this lane keeps the larger one
+  v = (v > o) == up ? v : o;
+  if constexpr (OFF > 1) return sort_step<SIZE, OFF / 2>(v);
+  else return v;
+}
+template <int SIZE = 2, typename V>
+MD_DEV V wave_nth(V v, int n) {
+  v = sort_step<SIZE, SIZE / 2>(v);
+  if constexpr (SIZE < 64) return wave_nth<2 * SIZE>(v, n);
+  else return __shfl(v, n - 1, 64);
 }
 
-// What the second kernel reads of a chunk.
+// The larger of the wave's keys, in every lane.
+template <int OFF = 32>
+MD_DEV Key wave_max_key(Key k) {
+  const Key o = other<OFF>(k);
+  k = o > k ? o : k;
+  if constexpr (OFF > 1) return wave_max_key<OFF / 2>(k);
+  else return k;
+}
+
+// What the second kernel reads of a segment.
 struct Part {
   float m, s, sx, pad;
 };
@@ -57,6 +84,34 @@ struct Sums {
 
 MD_DEV float nan_f32() { return __uint_as_float(0x7FC00000u); }
 
+template <int XT>
+MD_DEV float logit(const LogpArgs& g, int64_t row, int id) {
+  const int64_t at = row * g.stride + id;
+  if constexpr (XT == XF32) return static_cast<const float*>(g.logits)[at];
+  else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(g.logits)[at] << 16);
+}
+
+// One wave: where fewer than top logits are above -inf, the row's -inf ones follow
+// in order, then its NaNs.
+template <int XT>
+MD_DEV void fill(const LogpArgs& g, int64_t row, int have, Key* top) {
+  const int lane = threadIdx.x & 63;
+  for (int pass = 0; pass < 2 && have < g.top; ++pass)
+    for (int i = 0; i < g.vocab && have < g.top; i += 512) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = i + 64 * j + lane < g.vocab ? logit<XT>(g, row, i + 64 * j + lane) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool it = pass ? x[j] != x[j] : x[j] == -INFINITY;
+        const uint64_t all = __builtin_amdgcn_ballot_w64(it);
+        const int at = have + __popcll(all & ((1ull << lane) - 1ull));
+        if (it && at < g.top) top[at] = key_of(x[j], i + 64 * j + lane);
+        have += __popcll(all);
+      }
+    }
+}
+
 // A row's outputs from its sums: thread t of n does every n-th.
 template <int XT>
 MD_DEV void finish(const LogpArgs& g, int64_t row, const Sums& r, const Key* keys, int t, int n) {
@@ -67,13 +122,7 @@ MD_DEV void finish(const LogpArgs& g, int64_t row, const Sums& r, const Key* key
   for (int i = t; i < g.n_tokens; i += n) {
     const int id = g.tokens[row * g.n_tokens + i];
     float lp = nan_f32();
-    if (ok && (unsigned)id < (unsigned)g.vocab) {
-      const int64_t at = row * g.stride + id;
-      float x;
-      if constexpr (XT == XF32) x = static_cast<const float*>(g.logits)[at];
-      else x = __uint_as_float((uint32_t)static_cast<const uint16_t*>(g.logits)[at] << 16);
-      lp = (float)(((double)x - (double)r.m) * scale - log_s);
-    }
+    if (ok && (unsigned)id < (unsigned)g.vocab) lp = (float)(((double)logit<XT>(g, row, id) - (double)r.m) * scale - log_s);
     g.logprobs[row * g.n_tokens + i] = lp;
   }
   for (int i = t; i < g.top; i += n) {
@@ -88,19 +137,31 @@ MD_DEV void finish(const LogpArgs& g, int64_t row, const Sums& r, const Key* key
 MD_DEV void rank_keys(const Key* list, int cnt, int top, Key* out, int t, int n) {
   for (int i = t; i < cnt; i += n) {
     const Key k = list[i];
-    int r = 0;
-    for (int j = 0; j < cnt; ++j) r += list[j] > k;
+    int r = 0, j = 0;
+    for (; j + 8 <= cnt; j += 8) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) r += list[j + u] > k;
+    }
+    for (; j < cnt; ++j) r += list[j] > k;
     if (r < top) out[r] = k;
   }
 }
 
-template <int XT, int N>  // N values a thread
+// The next fp32 value (of +inf: none, a NaN, which nothing reaches).
+MD_DEV float above(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return __uint_as_float(x == 0.0f ? 1u : u >> 31 ? u - 1u : u + 1u);
+}
+
+constexpr int kPass = 512;                       // keys that a list holds
+constexpr float kLowest = -3.4028234663852886e38f;
+
+template <int XT, int N, bool TOP>  // N values a thread and step
 __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   constexpr int V = XT == XF32 ? 4 : 8, J = N / V;
-  __shared__ float s_m[4], s_s[4], s_sx[4];
+  __shared__ float s_m[4], s_s[4], s_sx[4], s_tau[4];
   __shared__ int s_bad[4], s_cnt;
-  __shared__ Key s_tau[4], s_top[kMaxTop];
-  __shared__ Key s_list[4 * kMaxTop * N];
+  __shared__ Key s_best[4], s_top[kMaxTop], s_list[kPass];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   if (row >= g.rows) return;
@@ -111,121 +172,189 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15) / es;
   const char* from = base - shift * es;
   const int last = g.vocab + shift;  // values [shift, last) of `from` are the row's
-  const int c0 = blockIdx.x * 256 * N;
-  float v[N];
+  const int c_end = min((blockIdx.x + 1) * g.steps * (256 * N), (last + 256 * N - 1) / (256 * N) * (256 * N));
+  // buffer loads: past the row's last 16 bytes they read zeros and touch no memory
+  const rsrc_t res = make_res(from, (last * es + 15) & ~15);
+  u32x4 w[J];
+  int c0 = blockIdx.x * g.steps * (256 * N);
+  auto load = [&](int at) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int i = c0 + (j * 256 + tid) * V;
-    u32x4 w{0, 0, 0, 0};
-    if (i < last) w = *reinterpret_cast<const u32x4*>(from + (int64_t)i * es);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float x;
-      if constexpr (XT == XF32) x = __uint_as_float(w[e]);
-      else x = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-      v[j * V + e] = i + e >= shift && i + e < last ? x : -INFINITY;
-    }
-  }
-  float m = -INFINITY;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    m = fmaxf(m, v[i]);
-    bad |= v[i] != v[i];
-  }
-  m = group_max<64>(m);
-  if (lane == 0) s_m[wave] = m;
-  const bool wave_bad = __builtin_amdgcn_ballot_w64(bad) != 0;
-  if (lane == 0) s_bad[wave] = wave_bad;
+    for (int j = 0; j < J; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b128(res, (j * 256 + tid) * 16, at * es, 0);
+  };
+  if (c0 < c_end) load(c0);
   if (tid == 0) s_cnt = 0;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
-  const float ref = m > -INFINITY ? m : 0.0f;
-  float s = 0.0f, sx = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float z = fmaxf((v[i] - ref) * g.scale, -200.0f);  // exp(-200) is 0 here: -inf adds nothing
-    const float e = __builtin_amdgcn_exp2f(z * 1.4426950408889634f);
-    s += e;
-    sx = fmaf(z, e, sx);
-  }
-  s = group_sum<64>(s);
-  sx = group_sum<64>(sx);
-  if (lane == 0) s_s[wave] = s, s_sx[wave] = sx;
-  if (g.top) {
-    Key best = 0;
+  // y = z log2 e, relative to the thread's maximum m, the lowest finite value at
+  // first; exp2(-300) is 0 in fp32, so that -inf adds nothing
+  const float c = g.scale * 1.4426950408889634f;
+  float m = kLowest, s = 0.0f, sx = 0.0f, tau = -INFINITY;
+  int cnt = 0;
+  bool bad = false;
+  for (; c0 < c_end; c0 += 256 * N) {
+    float v[N];
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const int i = c0 + (j * 256 + tid) * V + e;
-        const Key k = i >= shift && i < last ? key_of(v[j * V + e], i - shift) : 0;
-        best = k > best ? k : best;
+        if constexpr (XT == XF32) v[j * V + e] = __uint_as_float(w[j][e]);
+        else v[j * V + e] = __uint_as_float(e & 1 ? w[j][e >> 1] & 0xFFFF0000u : w[j][e >> 1] << 16);
       }
-    const Key nth = wave_nth(best, g.top);
-    if (lane == 0) s_tau[wave] = nth;
-    __syncthreads();
-    // the best of the four bounds; a wave with fewer values than top has bound 0
-    Key tau = 1;
+    if (c0 + 256 * N < c_end) load(c0 + 256 * N);
+    auto id_of = [&](int n) { return c0 + (n / V * 256 + tid) * V + n % V - shift; };  // value n's, if it is the row's
+    if (c0 < shift || c0 + 256 * N > last) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) tau = s_tau[w] > tau ? s_tau[w] : tau;
-    if (__builtin_amdgcn_ballot_w64(best >= tau)) {
+      for (int n = 0; n < N; ++n)
+        if ((unsigned)id_of(n) >= (unsigned)g.vocab) v[n] = -INFINITY;
+    }
+    float mine = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+    for (int n = 0; n < N; ++n) {
+      mine = fmaxf(mine, v[n]);
+      bad |= v[n] != v[n];
+    }
+    const float m1 = fmaxf(m, mine), d = fmaxf((m - m1) * c, -300.0f), f = __builtin_amdgcn_exp2f(d);
+    m = m1;
+    float ps = 0.0f, px = 0.0f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int i = c0 + (j * 256 + tid) * V + e;
-          const Key k = i >= shift && i < last ? key_of(v[j * V + e], i - shift) : 0;
-          if (k >= tau) s_list[atomicAdd(&s_cnt, 1)] = k;
+    for (int n = 0; n < N; ++n) {
+      const float y = fmaxf((v[n] - m) * c, -300.0f);
+      const float e = __builtin_amdgcn_exp2f(y);
+      ps += e;
+      px = fmaf(y, e, px);
+    }
+    sx = fmaf(f, fmaf(d, s, sx), px);
+    s = fmaf(f, s, ps);
+    if constexpr (TOP) {
+      const bool first = !(tau > -INFINITY);
+      if (first) {  // the same in all threads
+        const float nth = wave_nth(mine, g.top);
+        __syncthreads();  // s_tau of a step before
+        if (lane == 0) s_tau[wave] = nth;
+        __syncthreads();
+        tau = fmaxf(fmaxf(s_tau[0], s_tau[1]), fmaxf(s_tau[2], s_tau[3]));
+      }
+      // without a bound: all but -inf; behind a bound's step only larger ones (the lower ids are there)
+      const float pass = first ? fmaxf(tau, kLowest) : above(tau);
+      if (__builtin_amdgcn_ballot_w64(mine >= pass)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (v[n] >= pass) {
+            const int at = atomicAdd(&s_cnt, 1);
+            if (at < kPass) s_list[at] = key_of(v[n], id_of(n));
+          }
+      }
+      __syncthreads();
+      const int had = cnt;
+      cnt = s_cnt;
+      __syncthreads();  // all have read it
+      if (cnt > kPass) {
+        // too many: this step's winners one at a time, in place of what it added
+        Key below = ~(Key)0;
+        cnt = had;
+        for (int j = 0; j < g.top; ++j) {
+          Key best = 0;
+#pragma unroll 1
+          for (int n = 0; n < N; ++n) {  // (values read anew: they need not stay in registers for this)
+            const int id = id_of(n);
+            const float x = (unsigned)id < (unsigned)g.vocab ? logit<XT>(g, row, id) : -INFINITY;
+            const Key k = x >= pass ? key_of(x, id) : 0;
+            if (k < below && k > best) best = k;
+          }
+          best = wave_max_key(best);
+          __syncthreads();
+          if (lane == 0) s_best[wave] = best;
+          __syncthreads();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) best = s_best[i] > best ? s_best[i] : best;
+          if (tid == 0) s_list[cnt] = best;
+          ++cnt;
+          below = best;
         }
+        if (tid == 0) s_cnt = cnt;
+        __syncthreads();
+      }
+      if (cnt > kPass / 2) {  // cut to the largest: a step adds up to kMaxTop where it overfills the list
+        rank_keys(s_list, cnt, g.top, s_top, tid, 256);
+        __syncthreads();
+        if (tid < g.top) s_list[tid] = s_top[tid];
+        if (tid == 0) s_cnt = g.top;
+        cnt = g.top;
+        tau = key_logit((uint32_t)(s_top[g.top - 1] >> 32));
+        __syncthreads();
+      }
     }
   }
+  float all = group_max<64>(m);
+  const bool wave_bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+  if (lane == 0) s_m[wave] = all, s_bad[wave] = wave_bad;
   __syncthreads();
-  Sums r{m, 0.0, 0.0};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) r.s += s_s[w], r.sx += s_sx[w];
-  if (bad) r.s = __longlong_as_double(0x7FF8000000000000ll);
-  const int cnt = g.top ? s_cnt : 0;
-  if (g.chunks == 1) {
-    if (g.top) rank_keys(s_list, cnt, g.top, s_top, tid, 256);
-    __syncthreads();
-    finish<XT>(g, row, r, s_top, tid, 256);
-    return;
-  }
-  const int64_t at = row * g.chunks + blockIdx.x;
-  if (tid == 0) reinterpret_cast<Part*>(g.part)[at] = Part{m, (float)r.s, (float)r.sx, 0.0f};
-  if (g.top) {
-    Key* out = reinterpret_cast<Key*>(g.keys) + at * g.top;
-    for (int i = cnt + tid; i < g.top; i += 256) out[i] = 0;  // a last chunk of fewer values
+  all = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+  const float d = fmaxf((m - all) * c, -300.0f), f = __builtin_amdgcn_exp2f(d);
+  sx = group_sum<64>(f * fmaf(d, s, sx));
+  s = group_sum<64>(f * s);
+  if (lane == 0) s_s[wave] = s, s_sx[wave] = sx;
+  Key* out = g.segs == 1 ? s_top : reinterpret_cast<Key*>(g.keys) + (row * g.segs + blockIdx.x) * g.top;
+  if constexpr (TOP) {
+    __syncthreads();  // s_top of a cut before
+    for (int i = cnt + tid; i < g.top; i += 256) out[i] = 0;
     rank_keys(s_list, cnt, g.top, out, tid, 256);
   }
+  __syncthreads();
+  Sums r{all, 0.0, 0.0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.s += s_s[i], r.sx += s_sx[i];
+  r.sx *= 0.6931471805599453;
+  if (bad) r.s = __longlong_as_double(0x7FF8000000000000ll);
+  if (g.segs > 1) {
+    if (tid == 0) reinterpret_cast<Part*>(g.part)[row * g.segs + blockIdx.x] = Part{all, (float)r.s, (float)r.sx, 0.0f};
+    return;
+  }
+  if (TOP && cnt < g.top) {
+    if (wave == 0) fill<XT>(g, row, cnt, s_top);
+    __syncthreads();
+  }
+  finish<XT>(g, row, r, s_top, tid, 256);
 }
 
-// A row's chunks: one wave.  Its keys as in the chunk, a lane's in steps of 64.
+// A row's segments: one wave.  Up to kPass keys are ranked among all; of more the
+// largest are bounded first, as in the segment: a lane's keys in steps of 64, at
+// most kMaxJoin of them.  Keys of 0 are none.
 template <int XT>
 __global__ __launch_bounds__(64) void k_logprob_join(LogpArgs g) {
   __shared__ Key s_list[kMaxTop * kMaxJoin], s_top[kMaxTop];
   __shared__ int s_cnt;
   const int lane = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const Part* p = reinterpret_cast<const Part*>(g.part) + row * g.chunks;
-  float m = -INFINITY;
-  for (int i = lane; i < g.chunks; i += 64) m = fmaxf(m, p[i].m);
-  m = group_max<64>(m);
-  const double ref = m > -INFINITY ? (double)m : 0.0;
-  double s = 0.0, sx = 0.0;
-  for (int i = lane; i < g.chunks; i += 64) {
-    const Part q = p[i];
-    if (q.m == -INFINITY && q.s == 0.0f) continue;  // nothing there (a NaN among its values: s is NaN)
-    const double d = ((double)q.m - ref) * (double)g.scale, w = exp(d);
-    s += w * q.s;
-    sx += w * ((double)q.sx + d * q.s);
+  const Part* p = reinterpret_cast<const Part*>(g.part) + row * g.segs;
+  const Key* k = reinterpret_cast<const Key*>(g.keys) + row * g.segs * g.top;
+  const int n = g.segs * g.top;
+  Part q[2];  // up to 128 segments
+#pragma unroll
+  for (int i = 0; i < 2; ++i) q[i] = lane + 64 * i < g.segs ? p[lane + 64 * i] : Part{kLowest, 0.0f, 0.0f, 0.0f};
+  int have = 0;
+  if (n <= kPass) {
+#pragma unroll
+    for (int i = 0; i < kPass / 64; ++i) {
+      const Key x = lane + 64 * i < n ? k[lane + 64 * i] : 0;
+      if (lane + 64 * i < n) s_list[lane + 64 * i] = x;
+      have += __popcll(__builtin_amdgcn_ballot_w64(x != 0));
+    }
   }
-  const Sums r{m, wave_sum_f64(s), wave_sum_f64(sx)};
-  if (g.top) {
-    const Key* k = reinterpret_cast<const Key*>(g.keys) + row * g.chunks * g.top;
-    const int n = g.chunks * g.top;
+  const float m = group_max<64>(fmaxf(q[0].m, q[1].m));
+  double s = 0.0, sx = 0.0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (64 * i >= g.segs) break;
+    // (a segment of nothing but -inf: its sums are 0, and its maximum the lowest finite value)
+    const double d = ((double)q[i].m - (double)m) * (double)g.scale, w = exp(d);
+    s += w * q[i].s;
+    sx += w * ((double)q[i].sx + d * q[i].s);
+  }
+  const Sums r{m, wave_total(s), wave_total(sx)};
+  __syncthreads();
+  if (n <= kPass) {
+    rank_keys(s_list, n, g.top, s_top, lane, 64);
+  } else {
     Key best = 0;
     for (int i = lane; i < n; i += 64) best = k[i] > best ? k[i] : best;
     if (lane == 0) s_cnt = 0;
@@ -234,33 +363,51 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogpArgs g) {
     for (int i = lane; i < n; i += 64)
       if (k[i] >= tau) s_list[atomicAdd(&s_cnt, 1)] = k[i];
     __syncthreads();
-    rank_keys(s_list, s_cnt, g.top, s_top, lane, 64);
+    have = s_cnt;
+    rank_keys(s_list, have, g.top, s_top, lane, 64);
+  }
+  __syncthreads();
+  if (have < g.top) {
+    fill<XT>(g, row, have, s_top);
     __syncthreads();
   }
   finish<XT>(g, row, r, s_top, lane, 64);
 }
 
-// Values a thread: 32, or 8 where that leaves compute units without work.
-int logprob_values(int64_t rows, int vocab) {
-  return rows * ((vocab + 8191) / 8192) >= 2 * (int64_t)device_cus() || vocab > kMaxChunks * 2048 - 8 ? 32 : 8;
-}
-int logprob_chunks(int64_t rows, int vocab) {
-  const int per = 256 * logprob_values(rows, vocab);
-  return (vocab + 7 + per - 1) / per;  // a row may begin up to 7 values past 16 bytes
+// Values a thread and step: 32, or 8 where that leaves compute units without work;
+// segments of a row: enough for some workgroups on every compute unit.
+LogpPlan logprob_plan(int64_t rows, int vocab) {
+  LogpPlan p{};
+  const int64_t cus = device_cus();
+  auto steps_of = [&](int n) { return (vocab + 7 + 256 * n - 1) / (256 * n); };  // a row may begin up to 7 values past 16 bytes
+  p.values = rows * steps_of(32) >= 2 * cus ? 32 : 8;
+  const int total = steps_of(p.values);
+  int64_t segs = (kSegGroups * cus + rows - 1) / rows;
+  if (segs > total) segs = total;
+  if (segs > kMaxSegs) segs = kMaxSegs;
+  p.steps = (int)((total + segs - 1) / segs);
+  p.segs = (total + p.steps - 1) / p.steps;
+  return p;
 }
 
 hipError_t launch_logprob(const LogpArgs& g, int xt, int values, hipStream_t st) {
   const unsigned y = g.rows < 32768 ? (unsigned)g.rows : 32768u, z = (unsigned)((g.rows + y - 1) / y);
-  const dim3 grid(g.chunks, y, z), block(256);
+  const dim3 grid(g.segs, y, z), block(256);
+#define MD_LOGP(X_, N_)                                                                        \
+  do {                                                                                         \
+    if (g.top) hipLaunchKernelGGL((k_logprob<X_, N_, true>), grid, block, 0, st, g);           \
+    else hipLaunchKernelGGL((k_logprob<X_, N_, false>), grid, block, 0, st, g);                \
+  } while (0)
   if (xt == XF32) {
-    if (values == 32) hipLaunchKernelGGL((k_logprob<XF32, 32>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((k_logprob<XF32, 8>), grid, block, 0, st, g);
+    if (values == 32) MD_LOGP(XF32, 32);
+    else MD_LOGP(XF32, 8);
   } else {
-    if (values == 32) hipLaunchKernelGGL((k_logprob<XBF16, 32>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((k_logprob<XBF16, 8>), grid, block, 0, st, g);
+    if (values == 32) MD_LOGP(XBF16, 32);
+    else MD_LOGP(XBF16, 8);
   }
+#undef MD_LOGP
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || g.chunks == 1) return e;
+  if (e != hipSuccess || g.segs == 1) return e;
   if (xt == XF32) hipLaunchKernelGGL((k_logprob_join<XF32>), dim3((unsigned)g.rows), dim3(64), 0, st, g);
   else hipLaunchKernelGGL((k_logprob_join<XBF16>), dim3((unsigned)g.rows), dim3(64), 0, st, g);
   return hipGetLastError();

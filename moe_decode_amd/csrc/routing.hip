@@ -13,8 +13,6 @@
 // error, and only the tokens whose choice that bound leaves open are done in fp64.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
 #include "common.hpp"
 #include "i8.hpp"
 #include "kernels.hpp"
@@ -457,33 +455,6 @@ __global__ __launch_bounds__(512, 2) void k_route_fast(const void* __restrict__ 
 MD_DEV uint64_t order64(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
-}
-
-// The value of one lane (the same for all).
-MD_DEV float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
-MD_DEV double lane_of(double v, int lane) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-
-// The wave's sum, by row moves; the total ends in the last lane.
-MD_DEV double wave_total(double v) {
-  auto step = [&](auto ctrl, auto rows) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-    v += __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-  };
-  using std::integral_constant;
-  step(integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});   // quads
-  step(integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});
-  step(integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});  // mirrored half rows, rows
-  step(integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});
-  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // into the rows behind
-  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
-  return lane_of(v, 63);
 }
 
 // How a token's logits come.

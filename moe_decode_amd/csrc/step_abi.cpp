@@ -81,7 +81,7 @@ md_status check_logp(int32_t rows, int32_t vocab, int32_t top) {
                 vocab, kMaxVocab, top, md::kMaxTop);
   return MD_OK;
 }
-size_t part_bytes(int32_t rows, int chunks) { return align256((size_t)rows * chunks * 16); }
+size_t part_bytes(int32_t rows, int segs) { return align256((size_t)rows * segs * 16); }
 
 }  // namespace
 
@@ -224,8 +224,8 @@ md_status md_token_logprobs_workspace_size(int32_t rows, int32_t vocab, int32_t 
   const md_status s = check_logp(rows, vocab, top);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
-  const int chunks = rows ? md::logprob_chunks(rows, vocab) : 1;
-  *bytes = chunks > 1 ? part_bytes(rows, chunks) + align256((size_t)rows * chunks * top * 8) : 0;
+  const int segs = rows ? md::logprob_plan(rows, vocab).segs : 1;
+  *bytes = segs > 1 ? part_bytes(rows, segs) + align256((size_t)rows * segs * top * 8) : 0;
   return ok();
 }
 
@@ -261,7 +261,9 @@ md_status md_token_logprobs(const void* logits, int32_t xtype, int64_t stride, i
   g.vocab = vocab;
   g.n_tokens = n_tokens;
   g.top = top;
-  g.chunks = md::logprob_chunks(rows, vocab);
+  const md::LogpPlan plan = md::logprob_plan(rows, vocab);
+  g.segs = plan.segs;
+  g.steps = plan.steps;
   g.tokens = tokens;
   g.scale = scale;
   g.logprobs = logprobs;
@@ -270,9 +272,9 @@ md_status md_token_logprobs(const void* logits, int32_t xtype, int64_t stride, i
   g.top_logprobs = top_logprobs;
   if (need) {
     g.part = workspace;
-    g.keys = static_cast<char*>(workspace) + part_bytes(rows, g.chunks);
+    g.keys = static_cast<char*>(workspace) + part_bytes(rows, g.segs);
   }
-  const hipError_t e = md::launch_logprob(g, xtype, md::logprob_values(rows, vocab), stream);
+  const hipError_t e = md::launch_logprob(g, xtype, plan.values, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "log probabilities launch");
 }
 

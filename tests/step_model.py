@@ -135,9 +135,11 @@ def logprobs(x, scale):
     """Rows of fp32 values -> log probabilities, entropy, and the bounds on both.
 
     A term's z = (x - max) scale is off by 2 u |z|, its exp by that, one rounding of
-    the exponent's product (u |z|) and the instruction's 2 u; a chunk's sum (32
-    terms a thread, 6 levels, 4 waves) by 42 u.  With E = sum p |z|, E2 = sum p z^2:
-    log Z by 3 u E + 44 u, sum p z by 3 u E2 + 46 u E and by E times what Z is off."""
+    the exponent's product (u |z|) and the instruction's 2 u; a sum by k = 42 u and
+    two roundings for each step of it (32 terms a thread and step, steps of 2048
+    values at least, 6 levels, 4 waves).  With E = sum p |z|, E2 = sum p z^2: log Z
+    by 3 u E + (k + 2) u, sum p z by 3 u E2 + (k + 4) u E and by E times what Z is off."""
+    k = 42 + 2 * -(-(x.shape[1] + 7) // 2048)
     x = x.astype(np.float64)
     with np.errstate(invalid="ignore"):
         z = (x - x.max(1, keepdims=True)) * scale
@@ -147,9 +149,9 @@ def logprobs(x, scale):
         lp = z - np.log(Z)
         H = np.log(Z)[:, 0] - (p * zz).sum(1)
         E, E2 = (p * np.abs(zz)).sum(1), (p * zz * zz).sum(1)
-    dz = 3 * U * E + 44 * U
+    dz = 3 * U * E + (k + 2) * U
     return (lp, 1.1 * dz[:, None] + np.where(np.isfinite(lp), U * np.abs(lp), 0.0),
-            H, 1.1 * (dz * (1 + E) + 3 * U * E2 + 46 * U * E) + U * np.abs(H))
+            H, 1.1 * (dz * (1 + E) + 3 * U * E2 + (k + 4) * U * E) + U * np.abs(H))
 
 
 def top_ids(x, n):
