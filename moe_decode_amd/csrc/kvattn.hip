@@ -586,6 +586,10 @@ MD_DEV void paced() {
 template <int D, int NS, bool M>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a) {
   constexpr int KS = D / 16, DT = D / 32;
+  // blocks of 32 tokens of a softmax step: a masked call with two parts of each
+  // weight takes them one by one, which spares the registers that 128 channels lack
+  // (reloads of spilled ones wait for the next tile's loads too)
+  constexpr int NB = M && NS == 2 ? 1 : 2;
   constexpr float kLag = NS == 1 ? 7.0f : 0.0f, kUnit = NS == 1 ? 128.0f : 16384.0f;
   constexpr int L = kTile * D / 16 / 256;  // 16-byte chunks of codes per thread, keys or values
   __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kTile * D], s_v[2][kTile * D];
@@ -718,91 +722,94 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   for (int t = t_begin; t < t_end; ++t, buf ^= 1) {
     const int here = tile_of(t);
     if (any && here < mine.t1 && (here >= mine.t0 || (M && here < mine.head))) {
-      f32x16 x[2];
+#pragma unroll 1
+      for (int b0 = 0; b0 < 2; b0 += NB) {
+        f32x16 x[NB];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
+          for (int i = 0; i < 16; ++i) x[b][i] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int tok = 32 * b + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
-          const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][kslot(tok, 2 * k + hh)]);
+          for (int b = 0; b < NB; ++b) {
+            const int tok = 32 * (b0 + b) + 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+            const f16x8 kf = *reinterpret_cast<const f16x8*>(&s_k[buf][kslot(tok, 2 * k + hh)]);
 #pragma unroll
-          for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
-        }
-      paced<2 * KS, NS, 0>();
-      const int base = here * kTile, first = base + 16 * hh;
-      if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
-        keep_branch();
+            for (int e = 0; e < NS; ++e) x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[e][k], x[b], 0, 0, 0);
+          }
+        paced<NB * KS, NS, 0>();
+        const int base = here * kTile, first = base + 32 * b0 + 16 * hh;
+        if (base + kTile - 1 > mine.full_hi || base < mine.full_lo) {
+          keep_branch();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if constexpr (M) {
-            const uint32_t vis = seen16(a, q, seen, first + 32 * b);
+          for (int b = 0; b < NB; ++b) {
+            if constexpr (M) {
+              const uint32_t vis = seen16(a, q, seen, first + 32 * b);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!(vis >> i & 1u)) x[b][i] = -INFINITY;
-          } else {
+              for (int i = 0; i < 16; ++i)
+                if (!(vis >> i & 1u)) x[b][i] = -INFINITY;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (first + 32 * b + i > hi || first + 32 * b + i < lo) x[b][i] = -INFINITY;
+              for (int i = 0; i < 16; ++i)
+                if (first + 32 * b + i > hi || first + 32 * b + i < lo) x[b][i] = -INFINITY;
+            }
           }
         }
-      }
-      const float f = fmaxf(qscale * sc.ks, 1e-37f);
-      float raw = x[0][0];
+        const float f = fmaxf(qscale * sc.ks, 1e-37f);
+        float raw = x[0][0];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) raw = fmaxf(raw, x[b][i]);
-      if (raw > -INFINITY) l += sc.off;
-      raw = fmaxf(raw, xor_lanes<32>(raw)) * f;
-      if (raw == INFINITY) l = nan_f();
-      const float m1 = raw > m + kLag ? raw : m, ref = m1 > -INFINITY ? m1 : 0.0f;
-      const float alpha = __builtin_amdgcn_exp2f(m - ref);
-      m = m1;
-      // R is a power of two, so both factors are exact
-      const int e1 = max(ex_r, (int)(__float_as_uint(sc.vs) >> 23));
-      const float down = __uint_as_float((uint32_t)max(127 + ex_r - e1, 0) << 23);
-      const float w = sc.vs * __uint_as_float((uint32_t)(254 - e1) << 23) * kUnit;
-      ex_r = e1;
-      f16x8 pf[NS][4];
-      float sum = 0.0f;
+          for (int i = 0; i < 16; ++i) raw = fmaxf(raw, x[b][i]);
+        if (raw > -INFINITY) l += sc.off;
+        raw = fmaxf(raw, xor_lanes<32>(raw)) * f;
+        if (raw == INFINITY) l = nan_f();
+        const float m1 = raw > m + kLag ? raw : m, ref = m1 > -INFINITY ? m1 : 0.0f;
+        const float alpha = __builtin_amdgcn_exp2f(m - ref);
+        m = m1;
+        // R is a power of two, so both factors are exact
+        const int e1 = max(ex_r, (int)(__float_as_uint(sc.vs) >> 23));
+        const float down = __uint_as_float((uint32_t)max(127 + ex_r - e1, 0) << 23);
+        const float w = sc.vs * __uint_as_float((uint32_t)(254 - e1) << 23) * kUnit;
+        ex_r = e1;
+        f16x8 pf[NS][2 * NB];
+        float sum = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(x[b][i], f, -ref));
-          sum += p;
-          float pw = p * w;
-          // both parts from one rounded product: fused into the first conversion and not into the second, a
-          // tie could round two ways and leave a weight 2^-11 off
-          if constexpr (NS == 2) asm volatile("" : "+v"(pw));
-          pf[0][2 * b + (i >> 3)][i & 7] = (_Float16)pw;
-          if constexpr (NS == 2) pf[1][2 * b + (i >> 3)][i & 7] = (_Float16)(pw - (float)pf[0][2 * b + (i >> 3)][i & 7]);
+          for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(x[b][i], f, -ref));
+            sum += p;
+            float pw = p * w;
+            // both parts from one rounded product: fused into the first conversion and not into the second, a
+            // tie could round two ways and leave a weight 2^-11 off
+            if constexpr (NS == 2) asm volatile("" : "+v"(pw));
+            pf[0][2 * b + (i >> 3)][i & 7] = (_Float16)pw;
+            if constexpr (NS == 2) pf[1][2 * b + (i >> 3)][i & 7] = (_Float16)(pw - (float)pf[0][2 * b + (i >> 3)][i & 7]);
+          }
+        l = fmaf(l, alpha, sum);
+        const float scale = alpha * down;
+        if (__builtin_amdgcn_ballot_w64(scale != 1.0f)) {
+          keep_branch();
+#pragma unroll
+          for (int n = 0; n < DT; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[n][i] *= scale;
         }
-      l = fmaf(l, alpha, sum);
-      const float scale = alpha * down;
-      if (__builtin_amdgcn_ballot_w64(scale != 1.0f)) {
-        keep_branch();
 #pragma unroll
-        for (int n = 0; n < DT; ++n)
+        for (int n = 0; n < DT; ++n) {
+          const int d = 32 * n + col;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[n][i] *= scale;
-      }
+          for (int k = 0; k < 2 * NB; ++k) {
+            // block k / 2, step k % 2: tokens 32 (k / 2) + 16 hh + 8 (k % 2) ..
+            const f16x8 vf = *reinterpret_cast<const f16x8*>(&s_v[buf][vslot(d, 4 * (b0 + (k >> 1)) + 2 * hh + (k & 1))]);
 #pragma unroll
-      for (int n = 0; n < DT; ++n) {
-        const int d = 32 * n + col;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // block k / 2, step k % 2: tokens 32 (k / 2) + 16 hh + 8 (k % 2) ..
-          const f16x8 vf = *reinterpret_cast<const f16x8*>(&s_v[buf][vslot(d, 4 * (k >> 1) + 2 * hh + (k & 1))]);
-#pragma unroll
-          for (int e = 0; e < NS; ++e) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[e][k], acc[n], 0, 0, 0);
+            for (int e = 0; e < NS; ++e) acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[e][k], acc[n], 0, 0, 0);
+          }
         }
+        paced<2 * NB * DT, NS, 1>();
       }
-      paced<4 * DT, NS, 1>();
     }
     if (t + 1 < t_end) {
       stage(buf ^ 1);
