@@ -11,6 +11,7 @@ read its outputs.
 """
 import collections
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -542,13 +543,18 @@ class ExpertTier:
 
 # ---- the attention block in 8-bit integers -----------------------------------
 
+_XTYPES = {}
+
+
 def _xtype(dtype):
-    import torch
-    if dtype == torch.float32:
-        return X_F32
-    if dtype == torch.bfloat16:
-        return X_BF16
-    raise TypeError(f"float32 or bfloat16 wanted, got {dtype}")
+    t = _XTYPES.get(dtype)
+    if t is None:
+        import torch
+        _XTYPES.update({torch.float32: X_F32, torch.bfloat16: X_BF16})
+        if dtype not in _XTYPES:
+            raise TypeError(f"float32 or bfloat16 wanted, got {dtype}")
+        t = _XTYPES[dtype]
+    return t
 
 
 def _dense(name, t, shape, dtype, device):
@@ -992,38 +998,50 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     2 p with 2 p + 1; cosines and sines times factor.  q_out, k_out may be q and k
     themselves; out_dtype: the inputs' type by default.  Returns both."""
     import torch
-    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.dtype != q.dtype)):
-        raise ValueError("q and k [rows][heads][head_dim] of one length and type wanted")
-    rows, heads, dim = q.shape
-    dev = q.device
-    kh = 0 if k is None else k.shape[1]
-    qs, ks = _rows("q", q, heads, dim, dev), 0 if k is None else _rows("k", k, kh, dim, dev)
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    if len(shape) != 3:
+        raise ValueError(f"q: [rows][heads][head_dim] wanted, got {tuple(shape)}")
+    rows, heads, dim = shape
+    qs, ks, kh = _rows("q", q, heads, dim, dev), 0, 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != 3 or kshape[0] != rows or k.dtype is not dtype:
+            raise ValueError(f"k: {rows} rows of {dtype} wanted, got {tuple(kshape)} of {k.dtype}")
+        kh = kshape[1]
+        ks = _rows("k", k, kh, dim, dev)
     _dense("positions", positions, (rows,), torch.int32, dev)
-    _dense("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32, dev)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _dense(name, w, (dim,), torch.float32, dev)
-    given = q_out if q_out is not None else k_out
-    dt = out_dtype or (q.dtype if given is None else given.dtype)
+    half = inv_freq.numel()
+    _dense("inv_freq", inv_freq, (half,), torch.float32, dev)
+    qw = kw = None
+    if q_weight is not None:
+        qw = _dense("q_weight", q_weight, (dim,), torch.float32, dev).data_ptr()
+    if k_weight is not None:
+        kw = _dense("k_weight", k_weight, (dim,), torch.float32, dev).data_ptr()
+    dt = out_dtype
+    if dt is None:
+        dt = q_out.dtype if q_out is not None else dtype if k_out is None else k_out.dtype
 
-    def out(name, t, n):
-        if t is None:
-            return _result(stream, torch.empty, rows, n, dim, dtype=dt, device=dev)
-        if t.dtype != dt or t.shape[0] != rows:
+    def given(name, t, n):
+        if t.dtype is not dt or t.shape[0] != rows:
             raise ValueError(f"{name}: {rows} rows of {dt} wanted, got {tuple(t.shape)} of {t.dtype}")
-        return t
+        return _rows(name, t, n, dim, dev)
+    new = torch.empty if stream is None else functools.partial(_result, stream, torch.empty)
     with _on(dev, stream) as st:
-        q_out = out("q_out", q_out, heads)
-        qo = _rows("q_out", q_out, heads, dim, dev)
-        ko = 0
+        qo, ko, kp, kop = heads * dim, kh * dim, None, None
+        if q_out is None:
+            q_out = new(rows, heads, dim, dtype=dt, device=dev)
+        else:
+            qo = given("q_out", q_out, heads)
         if k is not None:
-            k_out = out("k_out", k_out, kh)
-            ko = _rows("k_out", k_out, kh, dim, dev)
-        d = RopeDesc(dim, 2 * inv_freq.numel(), int(interleaved), inv_freq.data_ptr(), factor, eps, _ptr(q_weight),
-                     _ptr(k_weight))
-        _check(lib().md_qk_norm_rope(ctypes.byref(d), positions.data_ptr(), rows, q.data_ptr(), heads, qs, _ptr(k), kh,
-                                     ks, _xtype(q.dtype), q_out.data_ptr(), qo, _ptr(k_out), ko, _xtype(dt), st))
-    return q_out, k_out
+            if k_out is None:
+                k_out = new(rows, kh, dim, dtype=dt, device=dev)
+            else:
+                ko = given("k_out", k_out, kh)
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        d = RopeDesc(dim, 2 * half, interleaved, inv_freq.data_ptr(), factor, eps, qw, kw)
+        _check(lib().md_qk_norm_rope(ctypes.byref(d), positions.data_ptr(), rows, q.data_ptr(), heads, qs, kp, kh, ks,
+                                     _xtype(dtype), q_out.data_ptr(), qo, kop, ko, _xtype(dt), st))
+    return q_out, k_out if k is not None else None
 
 
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -1047,14 +1065,24 @@ class Routing:
         self.groups, self.groups_kept, self.best_two = groups, groups_kept, bool(best_two)
         self.renorm, self.scale = bool(renorm), scale
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_made":         # what desc has checked and packed
+            object.__setattr__(self, "_made", None)
+
     def desc(self, E, device):
-        """The C descriptor for a call on E experts."""
-        import torch
-        b = self.balance
-        if b is not None:
-            _dense("balance", b, (E,), torch.float32, device)
-        return ctypes.byref(RoutingDesc(self.k, self.score, self.groups, self.groups_kept, int(self.best_two),
-                                        int(self.renorm), self.scale, _ptr(b)))
+        """The C descriptor for a call on E experts, packed once while the
+        attributes stay."""
+        b, made = self.balance, self._made
+        at = None if b is None else b.data_ptr()
+        if made is None or made[0] != at or made[1] != E or made[2] != device:
+            import torch
+            if b is not None:
+                _dense("balance", b, (E,), torch.float32, device)
+            d = RoutingDesc(self.k, self.score, self.groups, self.groups_kept, int(self.best_two), int(self.renorm),
+                            self.scale, at)
+            made = self._made = (at, E, device, ctypes.byref(d))
+        return made[3]
 
 
 def moe_route_workspace_size(T, H, E):
@@ -1063,28 +1091,35 @@ def moe_route_workspace_size(T, H, E):
     return need.value
 
 
+@functools.lru_cache(maxsize=64)
+def _route_need(device, T, H, E):
+    """moe_route_workspace_size with `device` current: it follows from these alone."""
+    return moe_route_workspace_size(T, H, E)
+
+
 def moe_route(x, Wr, routing, bias=None, idx=None, gates=None, logits=None, workspace=None, stream=None):
     """The experts of each row of x ([T][H] fp32 or bf16, any T) and their gates
     ([T][k], int32 and fp32) for the router Wr ([E][H] fp32; bias fp32 [E], added
     to the logits): what moe_experts_forward takes, 128 tokens at a time."""
     import torch
     T, H = x.shape
-    E, dev = Wr.shape[0], x.device
-    _dense("x", x, (T, H), x.dtype, dev)
+    E, dev, dtype = Wr.shape[0], x.device, x.dtype
+    _dense("x", x, (T, H), dtype, dev)
     _dense("Wr", Wr, (E, H), torch.float32, dev)
     if bias is not None:
         _dense("bias", bias, (E,), torch.float32, dev)
     if logits is not None:
         _dense("logits", logits, (T, E), torch.float32, dev)
     k = routing.k
+    new = torch.empty if stream is None else functools.partial(_result, stream, torch.empty)
     with _on(dev, stream) as st:
         r = routing.desc(E, dev)
-        idx = _result(stream, torch.empty, T, k, dtype=torch.int32, device=dev) if idx is None else \
+        idx = new(T, k, dtype=torch.int32, device=dev) if idx is None else \
             _dense("idx", idx, (T, k), torch.int32, dev)
-        gates = _result(stream, torch.empty, T, k, dtype=torch.float32, device=dev) if gates is None else \
+        gates = new(T, k, dtype=torch.float32, device=dev) if gates is None else \
             _dense("gates", gates, (T, k), torch.float32, dev)
-        ws, wsb = _workspace(moe_route_workspace_size(T, H, E), dev, workspace, stream)
-        _check(lib().md_moe_route(r, x.data_ptr(), _xtype(x.dtype), T, H, Wr.data_ptr(), _ptr(bias), E, idx.data_ptr(),
+        ws, wsb = _workspace(_route_need(dev, T, H, E), dev, workspace, stream)
+        _check(lib().md_moe_route(r, x.data_ptr(), _xtype(dtype), T, H, Wr.data_ptr(), _ptr(bias), E, idx.data_ptr(),
                                   gates.data_ptr(), _ptr(logits), _ptr(ws), wsb, st))
     return idx, gates
 
@@ -1098,6 +1133,12 @@ def token_logprobs_workspace_size(rows, vocab, top=0):
     return need.value
 
 
+@functools.lru_cache(maxsize=64)
+def _logprobs_need(device, rows, vocab, top):
+    """token_logprobs_workspace_size with `device` current: it follows from these alone."""
+    return token_logprobs_workspace_size(rows, vocab, top)
+
+
 def token_logprobs(logits, tokens=None, top=0, scale=1.0, logprobs=None, entropy=None, top_ids=None,
                    top_logprobs=None, workspace=None, stream=None):
     """From rows of logits ([rows][vocab] fp32 or bf16, rows may be strided),
@@ -1105,31 +1146,34 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, logprobs=None, entropy
     (int32 [rows][n], None: none), the entropy, and the `top` largest logits' ids
     and log probabilities (None where top is 0)."""
     import torch
-    if logits.dim() != 2 or (logits.shape[0] and logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError(f"logits: rows of neighbouring values wanted, got {tuple(logits.shape)} strides "
-                         f"{logits.stride()}")
-    rows, vocab = logits.shape
-    dev = logits.device
-    stride = logits.stride(0) if rows > 1 else vocab
-    n = 0
+    shape, dev, dtype = logits.shape, logits.device, logits.dtype
+    if len(shape) != 2:
+        raise ValueError(f"logits: [rows][vocab] wanted, got {tuple(shape)}")
+    rows, vocab = shape
+    stride, one = logits.stride()
+    if rows and vocab > 1 and one != 1:
+        raise ValueError(f"logits: rows of neighbouring values wanted, got strides {(stride, one)}")
+    f32, n, tok, lp = torch.float32, 0, None, None
     if tokens is not None:
         n = tokens.shape[1] if tokens.dim() == 2 else -1
-        _dense("tokens", tokens, (rows, n), torch.int32, dev)
-
-    def out(name, t, dtype, *shape):
-        if t is None:
-            return _result(stream, torch.empty, shape, dtype=dtype, device=dev)
-        return _dense(name, t, shape, dtype, dev)
+        tok = _dense("tokens", tokens, (rows, n), torch.int32, dev).data_ptr()
+    new = torch.empty if stream is None else functools.partial(_result, stream, torch.empty)
     with _on(dev, stream) as st:
         if tokens is not None:
-            logprobs = out("logprobs", logprobs, torch.float32, rows, n)
-        entropy = out("entropy", entropy, torch.float32, rows)
+            logprobs = new(rows, n, dtype=f32, device=dev) if logprobs is None else \
+                _dense("logprobs", logprobs, (rows, n), f32, dev)
+            lp = logprobs.data_ptr()
+        entropy = new(rows, dtype=f32, device=dev) if entropy is None else \
+            _dense("entropy", entropy, (rows,), f32, dev)
+        ids = tlp = None
         if top:
-            top_ids = out("top_ids", top_ids, torch.int32, rows, top)
-            top_logprobs = out("top_logprobs", top_logprobs, torch.float32, rows, top)
-        ws, wsb = _workspace(token_logprobs_workspace_size(rows, vocab, top), dev, workspace, stream)
-        _check(lib().md_token_logprobs(logits.data_ptr(), _xtype(logits.dtype), stride, rows, vocab, _ptr(tokens), n,
-                                       scale, top, _ptr(logprobs), entropy.data_ptr(), _ptr(top_ids),
-                                       _ptr(top_logprobs), _ptr(ws), wsb, st))
+            top_ids = new(rows, top, dtype=torch.int32, device=dev) if top_ids is None else \
+                _dense("top_ids", top_ids, (rows, top), torch.int32, dev)
+            top_logprobs = new(rows, top, dtype=f32, device=dev) if top_logprobs is None else \
+                _dense("top_logprobs", top_logprobs, (rows, top), f32, dev)
+            ids, tlp = top_ids.data_ptr(), top_logprobs.data_ptr()
+        ws, wsb = _workspace(_logprobs_need(dev, rows, vocab, top), dev, workspace, stream)
+        _check(lib().md_token_logprobs(logits.data_ptr(), _xtype(dtype), stride if rows > 1 else vocab, rows, vocab, tok, n,
+                                       scale, top, lp, entropy.data_ptr(), ids, tlp, _ptr(ws), wsb, st))
     return TokenLogprobs(logprobs if tokens is not None else None, entropy, top_ids if top else None,
                          top_logprobs if top else None)

@@ -587,9 +587,11 @@ template <int D, int NS, bool M>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a) {
   constexpr int KS = D / 16, DT = D / 32;
   // blocks of 32 tokens of a softmax step: a masked call with two parts of each
-  // weight takes them one by one, which spares the registers that 128 channels lack
-  // (reloads of spilled ones wait for the next tile's loads too)
-  constexpr int NB = M && NS == 2 ? 1 : 2;
+  // weight and 128 channels or more takes them one by one, which spares registers:
+  // reloads of spilled ones wait for the next tile's loads too (2 x 61 drafts on up
+  // to 65535 tokens, 32 heads on 8 of 128: 317 us with 27 spilled, 263 with none;
+  // 256 channels: 92 spilled, 47)
+  constexpr int NB = M && NS == 2 && D > 64 ? 1 : 2;
   constexpr float kLag = NS == 1 ? 7.0f : 0.0f, kUnit = NS == 1 ? 128.0f : 16384.0f;
   constexpr int L = kTile * D / 16 / 256;  // 16-byte chunks of codes per thread, keys or values
   __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kTile * D], s_v[2][kTile * D];
