@@ -191,7 +191,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr double kFastError = 5.5 * 0x1p-23;
 constexpr int kRest = 1024;
-constexpr int kFT = 128;  // tokens, and experts, of a workgroup
+constexpr int kTT = 64, kFT = 128;  // tokens and experts of a workgroup
 template <int XT> constexpr int kFastStep = XT == XF32 ? 32 : 64;
 
 MD_DEV void split3(float v, uint16_t& a, uint16_t& b, uint16_t& c) {
@@ -244,33 +244,36 @@ __global__ __launch_bounds__(256) void k_route_split(const float* __restrict__ W
     norms[(int64_t)blockIdx.y * E + e] = (s_n[0][lane] + s_n[1][lane]) + (s_n[2][lane] + s_n[3][lane]);
 }
 
-// 128 tokens x 128 experts and a K-slice a workgroup, eight waves of 64 x 32.  The
-// parts of W_r, in operand order, come straight from L2, a step ahead; x goes
-// through LDS: two buffers, and the two steps behind them on their way in
-// registers.  A[i][k], B[k][j] of the 32x32x16 product: eight k at lane 32 (k / 8)
-// + i (j); D[8 a + 4 (lane / 32) + b][lane % 32] in element 4 a + b.
-// Measured: 8191 tokens x 6144 columns x 256 experts, bf16, 101 us (77 Gflop of
-// parts, 0.77 Pflop/s; the matrix cores are busy for 38 us).  What the waves wait
-// for is spread: with every load from the caches 80 us, without the products 79,
-// without both 40.  Measured and dropped: both operands through LDS 104 us, four
-// waves of 128 x 32 (a wave a SIMD) 122.
+// 64 tokens x 128 experts and a K-slice a workgroup, four waves of 64 x 32, two
+// workgroups on a compute unit.  The parts of W_r, in operand order, come straight
+// from L2, a step ahead; x goes through LDS: two buffers, and the two steps behind
+// them on their way in registers.  A[i][k], B[k][j] of the 32x32x16 product: eight
+// k at lane 32 (k / 8) + i (j); D[8 a + 4 (lane / 32) + b][lane % 32] in element
+// 4 a + b.
+// Measured: 8191 tokens x 6144 columns x 256 experts, bf16, 96 us (77 Gflop of
+// parts, 0.8 Pflop/s; the matrix cores are busy for 38 us of them).  With a third
+// of W_r's loads 76 us, with every load from the caches 78, without the products 75,
+// without the sums in fp64 88: mostly the 16 bytes a lane and product that the parts
+// of W_r take through L1, beside the products, not hidden behind them.  Measured and
+// dropped: both operands through LDS 104 us, workgroups of 128 x 128 the same as
+// this, waves of 128 x 32 (half the loads of W_r, one wave a SIMD) 122.
 template <int XT>
-__global__ __launch_bounds__(512, 2) void k_route_fast(const void* __restrict__ x, int T, int H,
+__global__ __launch_bounds__(256, 2) void k_route_fast(const void* __restrict__ x, int T, int H,
                                                        const uint16_t* __restrict__ planes, int E, int Ks, int S,
                                                        double* __restrict__ part, float* __restrict__ xnorm,
                                                        const float* __restrict__ wnorm, const float* __restrict__ balance,
                                                        float* __restrict__ most) {
   constexpr int KS = kFastStep<XT>, C = KS / 8, XP = XT == XF32 ? 3 : 1;  // columns, chunks of 16 bytes, parts of x
-  constexpr int kTile = kFT * KS;                                         // values of a part of x's tile
+  constexpr int kTile = kTT * KS;                                         // values of a part of x's tile
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * XP * kTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ets = (E + kFT - 1) / kFT;
   // workgroups that follow each other go to different dies: those of one die
   // take the same experts and slice, so that its L2 holds these parts of W_r
   const int combo = blockIdx.x % (ets * S), ex = combo % ets, sl = combo / ets;
-  const int t0 = blockIdx.x / (ets * S) * kFT, e0 = ex * kFT;
+  const int t0 = blockIdx.x / (ets * S) * kTT, e0 = ex * kFT;
   const int kbeg = sl * Ks, kend = min(kbeg + Ks, H);
-  const int wm = wave & 1, wn = wave >> 1, l31 = lane & 31, hh = lane >> 5;
+  const int l31 = lane & 31, hh = lane >> 5;
   // sixteen lanes of a fragment read hit sixteen chunks of 256 bytes: two rows of 128, or four of 64
   auto slot = [](int row, int chunk) { return row * KS + 8 * (chunk ^ (C == 8 ? (row >> 1) & 7 : (row >> 2) & 3)); };
   // staging: four threads a row, C / 4 chunks of 16 bytes
@@ -330,7 +333,7 @@ __global__ __launch_bounds__(512, 2) void k_route_fast(const void* __restrict__ 
   };
   // the wave's operands of W_r, a step's
   bf16x8 w[KS / 16][3];
-  const uint16_t* wp = planes + ((int64_t)(4 * ex + wn) * (H / 16) + kbeg / 16) * 1536 + 8 * lane;
+  const uint16_t* wp = planes + ((int64_t)(4 * ex + wave) * (H / 16) + kbeg / 16) * 1536 + 8 * lane;
   auto load_w = [&](int k) {
 #pragma unroll
     for (int p = 0; p < 3; ++p) w[k][p] = *reinterpret_cast<const bf16x8*>(wp + k * 1536 + p * 512);
@@ -368,7 +371,7 @@ __global__ __launch_bounds__(512, 2) void k_route_fast(const void* __restrict__ 
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int p = 0; p < XP; ++p)
-          v[k & 1][t][p] = *reinterpret_cast<const bf16x8*>(b + p * kTile + slot(64 * wm + 32 * t + l31, 2 * k + hh));
+          v[k & 1][t][p] = *reinterpret_cast<const bf16x8*>(b + p * kTile + slot(32 * t + l31, 2 * k + hh));
     };
     if (first) {
 #pragma unroll
@@ -432,13 +435,13 @@ __global__ __launch_bounds__(512, 2) void k_route_fast(const void* __restrict__ 
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[t][i] += (double)r[t][i];
-  const int e = e0 + 32 * wn + l31;
+  const int e = e0 + 32 * wave + l31;
   if (e < E) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int tok = t0 + 64 * wm + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3);
+        const int tok = t0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3);
         if (tok < T) part[((int64_t)sl * T + tok) * E + e] = acc[t][i];
       }
   }
@@ -718,7 +721,7 @@ static hipError_t launch_fast(const RouteArgs& g, const RoutePlan& p, const void
                               hipStream_t st) {
   const int ets = (g.E + kFT - 1) / kFT;
   hipLaunchKernelGGL(k_route_split, dim3(ets * kFT / 32, H / 256), dim3(256), 0, st, Wr, g.E, H, planes, g.wnorm, g.count);
-  hipLaunchKernelGGL((k_route_fast<XT>), dim3(ets * p.S * ((g.T + kFT - 1) / kFT)), dim3(512), 0, st, x, g.T, H, planes,
+  hipLaunchKernelGGL((k_route_fast<XT>), dim3(ets * p.S * ((g.T + kTT - 1) / kTT)), dim3(256), 0, st, x, g.T, H, planes,
                      g.E, p.Ks, p.S, g.part, g.xnorm, g.wnorm, g.balance, g.most);
   hipLaunchKernelGGL((k_route_select<kBounded>), dim3(g.T), dim3(64), 0, st, g);
   hipLaunchKernelGGL((k_route_gemm<XT, true>), dim3(kListGroups), dim3(256), 0, st, x, g.T, H, Wr, g.E, 0, g.part, g.count,
