@@ -261,7 +261,6 @@ hipError_t launch_qk_norm_rope(const RopeArgs& g, bool pairs, int xt, int yt, hi
 
 // ---- routing (routing.hip) ---------------------------------------------------
 constexpr int kRouteFew = 8;  // tokens of the form that has a workgroup for each expert
-constexpr int64_t kRouteFast = 4000000000;  // operations from which the logits are bounded on the bf16 matrix cores first
 struct RouteArgs {
   double* part;               // [S][T][E]
   int S, T, H, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
@@ -278,7 +277,8 @@ struct RoutePlan {
   bool fast;
   size_t planes, wnorm, most, xnorm, count, list, part, bytes;  // the workspace's parts and size
 };
-RoutePlan route_plan(int64_t T, int H, int E, bool fast);
+// fast: the bf16 form may be taken (no logits are asked for)
+RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast);
 hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, int xt, const float* Wr, void* ws,
                         hipStream_t st);
 

@@ -486,6 +486,13 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
     S = list_plan((int)n, E, g.H).S;
     t = g.list[t];
   }
+  // (loaded first: they are on their way with the partials)
+  float bias[4], bal[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bias[i] = g.bias && lane + 64 * i < E ? g.bias[lane + 64 * i] : 0.0f;
+    bal[i] = g.balance && lane + 64 * i < E ? g.balance[lane + 64 * i] : 0.0f;
+  }
   double l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) l[i] = 0.0;
@@ -509,7 +516,7 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
     const int e = lane + 64 * i;
     f[i] = -INFINITY;
     if (e < E) {
-      if (g.bias) l[i] += (double)g.bias[e];
+      if (g.bias) l[i] += (double)bias[i];
       f[i] = (float)l[i];
       if (!B && g.logits) g.logits[t * E + e] = f[i];
       far = fmaxf(far, fabsf(f[i]));
@@ -563,7 +570,7 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
     const int e = lane + 64 * i;
     hi[i] = lo[i] = 0;
     if (e < E) {
-      c[i] = g.balance ? s[i] + (F)g.balance[e] : s[i];
+      c[i] = g.balance ? s[i] + (F)bal[i] : s[i];
       if (c[i] != c[i]) c[i] = -INFINITY;
       if constexpr (B) {
         hi[i] = order_key32(c[i]);
@@ -620,19 +627,26 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
   for (int j = 0; j < g.k + (B ? 1 : 0); ++j) {
     const uint32_t h = wave_max_u32(max(max(hi[0], hi[1]), max(hi[2], hi[3])));
     if (B && h == 0) break;  // k experts are all that may be chosen
-    uint32_t w = 0;
-    if constexpr (!B) {
+    uint64_t has[4];
+    int n_has = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      has[i] = __builtin_amdgcn_ballot_w64(hi[i] == h);
+      n_has += __popcll(has[i]);
+    }
+    if (!B && n_has > 1) {  // the same high word twice: the low one decides
+      uint32_t w = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (hi[i] == h) w = max(w, lo[i]);
       w = wave_max_u32(w);
-    }
-    int who = -1, slot = 0;
 #pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      const uint64_t has = __builtin_amdgcn_ballot_w64(hi[i] == h && lo[i] == w);
-      if (has) who = __builtin_ctzll(has), slot = i;
+      for (int i = 0; i < 4; ++i) has[i] = __builtin_amdgcn_ballot_w64(hi[i] == h && lo[i] == w);
     }
+    int who = 0, slot = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+      if (has[i]) who = __builtin_ctzll(has[i]), slot = i;
     F v = s[0], cc = c[0];
     double lv = l[0];
 #pragma unroll
@@ -674,16 +688,23 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
   }
 }
 
-// The bf16 form pays from some 4 Gflop on.
-static bool route_fast(int64_t T, int H, int E) { return 2 * T * H * E >= kRouteFast; }
+// Whether the bf16 form pays: both forms' times in us, linear in Gflop (whole tiles
+// of experts in the bf16 form), as measured over 128 to 16384 tokens.  us, bf16
+// form and fp64: 6144 x 256, bf16, 512 tokens 57 and 41, 1024 59 and 72, 8192 158
+// and 439; fp32 1024 86 and 72, 2048 101 and 120, 8192 257 and 435; 2048 x 128, fp32,
+// 4096 76 and 53, 8192 84 and 93; 4096 x 64, bf16, 4096 52 and 54, 8192 66 and 93.
+static bool route_fast(int64_t T, int H, int E, int xt) {
+  const double g = 2e-9 * T * H * E, whole = 2e-9 * T * H * ((E + kFT - 1) / kFT * kFT);
+  return 18.0 + 16.2 * g > (xt == XF32 ? 55.0 + 7.5 * whole : 40.0 + 4.3 * whole);
+}
 
 // K-slices of the product: enough that every compute unit has a workgroup, a
 // slice of 256 at least (the bf16 form: of 1024).
-RoutePlan route_plan(int64_t T, int H, int E, bool fast) {
+RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast) {
   RoutePlan p{};
   p.Ks = H;
   p.S = 1;
-  p.fast = fast && route_fast(T, H, E);
+  p.fast = fast && T > kRouteFew && route_fast(T, H, E, xt);
   if (T > kRouteFew) {
     const int tile = p.fast ? kFT : kGT, step = p.fast ? 1024 : 256;
     const int64_t tiles = (int64_t)((E + tile - 1) / tile) * ((T + tile - 1) / tile);

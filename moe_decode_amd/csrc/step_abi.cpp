@@ -139,9 +139,13 @@ md_status md_moe_route_workspace_size(int32_t T, int32_t H, int32_t E, size_t* b
   const md_status s = check_route(T, H, E);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
-  // with and without the logits' rounded values, which one form gives
-  const size_t a = T ? md::route_plan(T, H, E, true).bytes : 0, b = T ? md::route_plan(T, H, E, false).bytes : 0;
-  *bytes = a > b ? a : b;
+  // enough for either type of x, with the logits or without
+  size_t most = 0;
+  for (int form = 0; T && form < 3; ++form) {
+    const size_t b = md::route_plan(T, H, E, form == 1 ? MD_X_BF16 : MD_X_F32, form < 2).bytes;
+    if (b > most) most = b;
+  }
+  *bytes = most;
   return ok();
 }
 
@@ -160,7 +164,7 @@ md_status md_moe_route(const md_routing* r, const void* x, int32_t xtype, int32_
   if (!workspace || workspace_bytes < need)
     return fail(MD_ERR_WORKSPACE, "workspace: %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
   if (!aligned16(workspace)) return fail(MD_ERR_ALIGNMENT, "workspace not 16-byte aligned");
-  const md::RoutePlan p = md::route_plan(T, H, E, !logits);
+  const md::RoutePlan p = md::route_plan(T, H, E, xtype, !logits);
   md::RouteArgs g{};
   g.T = T;
   g.H = H;
