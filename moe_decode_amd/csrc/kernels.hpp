@@ -226,13 +226,15 @@ struct KvAttn {
   const uint64_t* tree;       // [rows][words], or nullptr
   int tile;                   // columns (query, head) of a workgroup
   int snake;                  // all workgroups run at once, two on a compute unit
-  int splits, chunk;          // many columns: a split covers chunk tiles of 64 positions
+  int splits, chunk;          // many columns: a split covers chunk tiles of 64 positions (masked: at least)
+  int deal;                   // workgroups that run at once
   int pieces;                 // few columns: workgroups that all tiles are dealt out to, or 0
   float *part, *part_m;       // [rows][Hq][splits][D], [rows][Hq][splits][2]; [2 pieces][16][D], [2 pieces][16][2]
-  int4* shares;               // [pieces]: of the segment that begins there, how many shares, which one, first slot
+  int4* shares;               // [pieces]: of the segment that begins there, how many shares, which one, first slot;
+                              // masked, many columns: int [S][column tiles], splits of each
 };
 struct KvPlan {
-  int tile, splits, chunk, pieces;
+  int tile, splits, chunk, pieces, notes;
 };
 constexpr int kPairsPerLaunch = 448;  // page pairs that fit a launch's 4 KB of arguments
 struct PagePairs {
@@ -242,7 +244,7 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const void* k, i
                             int64_t v_stride, int xt, hipStream_t st);
 hipError_t launch_kv_read(const KvCache& c, const int* pages, int n, void* k, void* v, int yt, hipStream_t st);
 hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int n, hipStream_t st);
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt);
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt, bool masked);
 hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st);
 hipError_t launch_kv_tree(const KvBatch& b, const int* parents, uint64_t* masks, int words, int* positions,
                           hipStream_t st);

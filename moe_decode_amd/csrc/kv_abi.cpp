@@ -129,12 +129,14 @@ size_t attn_slots(const md::KvPlan& p, const md_kv_batch* b, int32_t q_heads) {
   return p.splits > 1 ? (size_t)b->rows * q_heads * p.splits : 0;
 }
 
+size_t notes_bytes(const md::KvPlan& p) { return p.pieces * sizeof(int4) + p.notes * sizeof(int); }
+
 // A window that reaches past every position is none.
 int seen(const md_kv_batch* b, int32_t window) { return window >= b->max_kv ? 0 : window; }
 
 // The attention's checks up to its pointers, and its launch geometry.
 md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads, int32_t causal, int32_t window,
-                    int32_t sinks, int32_t ytype, md::KvPlan* plan, size_t* bytes) {
+                    int32_t sinks, bool masked, int32_t ytype, md::KvPlan* plan, size_t* bytes) {
   md_status s;
   if ((s = check_cache(c)) != MD_OK || (s = check_batch(c, b)) != MD_OK) return s;
   if (q_heads <= 0 || q_heads % c->kv_heads)
@@ -145,11 +147,11 @@ md_status attn_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_heads,
     return fail(MD_ERR_INVALID_ARG, "attention: window %d%s", window, causal ? "" : " without causal");
   if (!valid_xtype(ytype)) return fail(MD_ERR_INVALID_ARG, "unknown ytype %d", ytype);
   const int G = q_heads / c->kv_heads;
-  *plan = md::kv_attn_plan(dev(c), dev(b), G, seen(b, window), sinks, causal, ytype);
+  *plan = md::kv_attn_plan(dev(c), dev(b), G, seen(b, window), sinks, causal, ytype, masked);
   const int64_t groups = ((int64_t)b->max_q * G + plan->tile - 1) / plan->tile * c->kv_heads * plan->splits;
   if (groups > kMaxGrid) return fail(MD_ERR_UNSUPPORTED, "attention: max_q %d on %d heads", b->max_q, q_heads);
   const size_t slots = attn_slots(*plan, b, q_heads);
-  *bytes = slots ? align256(plan->pieces * sizeof(int4)) + align256(slots * 2 * sizeof(float)) +
+  *bytes = slots ? align256(notes_bytes(*plan)) + align256(slots * 2 * sizeof(float)) +
                        align256(slots * c->head_dim * sizeof(float))
                  : 0;
   return MD_OK;
@@ -172,7 +174,8 @@ md_status masked_plan(const md_kv_cache* c, const md_kv_batch* b, int32_t q_head
     if (reinterpret_cast<uintptr_t>(m->tree) & 7u) return fail(MD_ERR_ALIGNMENT, "attention: the tree is not 8-byte aligned");
   }
   if (m->window < 0) return fail(MD_ERR_INVALID_ARG, "attention: window %d", m->window);
-  return attn_plan(c, b, q_heads, 1, m->window, kept(b, m), ytype, plan, bytes);
+  const int sinks = kept(b, m);
+  return attn_plan(c, b, q_heads, 1, m->window, sinks, m->tree || sinks, ytype, plan, bytes);
 }
 
 // ---- pages -----------------------------------------------------------------
@@ -344,7 +347,7 @@ md_status md_kv_attention_workspace_size(const md_kv_cache* c, const md_kv_batch
                                          int32_t window, int32_t ytype, size_t* bytes) {
   md::KvPlan plan;
   size_t need = 0;
-  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, ytype, &plan, &need);
+  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, false, ytype, &plan, &need);
   if (s != MD_OK) return s;
   if (!bytes) return fail(MD_ERR_INVALID_ARG, "null size pointer");
   *bytes = need;
@@ -410,7 +413,7 @@ static md_status attend(const md_kv_cache* c, const md_kv_batch* b, const md::Kv
   if (need) {
     char* at = static_cast<char*>(workspace);
     a.shares = reinterpret_cast<int4*>(at);
-    at += align256(plan.pieces * sizeof(int4));
+    at += align256(notes_bytes(plan));
     a.part_m = reinterpret_cast<float*>(at);
     at += align256(attn_slots(plan, b, q_heads) * 2 * sizeof(float));
     a.part = reinterpret_cast<float*>(at);
@@ -457,7 +460,7 @@ md_status md_kv_attention(const md_kv_cache* c, const md_kv_batch* b, const void
                           int64_t out_stride, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   md::KvPlan plan;
   size_t need = 0;
-  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, ytype, &plan, &need);
+  const md_status s = attn_plan(c, b, q_heads, causal, window, 0, false, ytype, &plan, &need);
   if (s != MD_OK) return s;
   return attend(c, b, plan, need, q, xtype, q_heads, q_stride, scale, causal, window, nullptr, out, ytype, out_stride,
                 workspace, workspace_bytes, stream);

@@ -567,6 +567,35 @@ MD_DEV uint2 codes_f16(uint32_t w) {
 
 constexpr int kRowCols = 128;  // columns of a workgroup
 
+// Tiles of a split of the sequence q.  Plain calls: what the host's bounds gave.
+// Masked ones: all column tiles' tiles, by the lengths on the device, over the
+// workgroups that run at once (a.deal; one more would wait for all of them), four at
+// least and as many as leave a.splits of them enough (2 x 61 drafts on 65535 and 37843 tokens, 32 heads on 8 of 128:
+// 263 us with splits of the longest one's, 228).  Every thread of the workgroup calls it; there are at most 256
+// sequences where a.splits > 1.
+template <bool M>
+MD_DEV int split_tiles(const KvAttn& a, const Seq& q) {
+  if (!M || a.splits == 1) return a.chunk;
+  __shared__ int64_t s_sum[kWaves];
+  // tiles, and in the upper bits segments: one more split each, where tiles do not come out even
+  int64_t sum = 0;
+  Span all;
+  if ((int)threadIdx.x < a.b.S) {
+    const Seq r = seq_of(a.b, threadIdx.x, a.c.page);
+    const int cts = (r.nq * a.G + a.tile - 1) / a.tile;
+    if (r.nq) sum = (int64_t)tiles_of<true>(a, r, r.nq * a.G, all) * cts + ((int64_t)cts << 40);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  const int n = q.nq ? tiles_of<true>(a, q, q.nq * a.G, all) : 1;
+  const int64_t total = (sum & ((1ll << 40) - 1)) * a.c.Hkv, groups = max(a.deal - (sum >> 40) * a.c.Hkv, (int64_t)a.deal / 4);
+  const int64_t per = max((total + groups - 1) / groups, (int64_t)a.chunk);
+  return __builtin_amdgcn_readfirstlane((int)max(per, (int64_t)((n + a.splits - 1) / a.splits)));
+}
+
 // Schedules a block of N LDS reads that feed NS matrix instructions each with
 // four reads in flight; left to itself the compiler waits for every read right
 // after it (4096 new of 5003 tokens, 128 channels: 152 -> 149 us, 2048 of 2048 of
@@ -598,15 +627,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
+  // M: many of the splits may have nothing to do (split_tiles); those that have follow
+  // each other, since workgroups are spread over the dies by their number
+  const int heads = (int)(gridDim.x / a.splits);
+  const int split = M ? blockIdx.x / heads : blockIdx.x % a.splits, rest = M ? blockIdx.x % heads : blockIdx.x / a.splits;
   const int h = rest % c.Hkv, s = blockIdx.y;
   const Seq q = seq_of(a.b, s, c.page);
   const int cols = q.nq * a.G;
   const int ct = column_tile(a, rest / c.Hkv, (int)(gridDim.x / (a.splits * c.Hkv)));
+  const int per = split_tiles<M>(a, q);
   if (ct * kRowCols >= cols) return;
   const Span sp = span_of<M>(a, q, ct * kRowCols, min(ct * kRowCols + kRowCols, cols));
-  const int per = a.chunk, active = max(1, (sp.head + sp.t1 - sp.t0 + per - 1) / per);
+  const int active = max(1, (sp.head + sp.t1 - sp.t0 + per - 1) / per);
   if (split >= active) return;
+  if (M && a.splits > 1 && split == 0 && h == 0 && tid == 0)  // for the join
+    reinterpret_cast<int*>(a.shares)[s * (heads / c.Hkv) + ct] = active;
   // M: tiles numbered with the `head` first ones in front
   const int skip = sp.t0 - sp.head;
   const int t_begin = M ? split * per : sp.t0 + split * per, t_end = min(t_begin + per, M ? sp.t1 - skip : sp.t1);
@@ -859,9 +894,13 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttn a) {
   if ((int)blockIdx.x >= q.nq) return;
   const int64_t row = (int64_t)q.row0 + blockIdx.x, slot0 = (row * (a.G * a.c.Hkv) + head) * a.splits;
   const int cols = q.nq * a.G, ct = ((int)blockIdx.x * a.G + head % a.G) / a.tile;
-  const int c1 = min(ct * a.tile + a.tile, cols);
-  const Span sp = a.masked ? span_of<true>(a, q, ct * a.tile, c1) : span_of<false>(a, q, ct * a.tile, c1);
-  const int active = (sp.head + sp.t1 - sp.t0 + a.chunk - 1) / a.chunk;
+  int active;
+  if (a.masked) {
+    active = reinterpret_cast<const int*>(a.shares)[s * ((gridDim.x * a.G + a.tile - 1) / a.tile) + ct];
+  } else {
+    const Span sp = span_of<false>(a, q, ct * a.tile, min(ct * a.tile + a.tile, cols));
+    active = (sp.t1 - sp.t0 + a.chunk - 1) / a.chunk;
+  }
   if (active <= 1) return;
   const float2* ml = reinterpret_cast<const float2*>(a.part_m) + slot0;
   float m = -INFINITY;
@@ -938,7 +977,7 @@ __global__ __launch_bounds__(256) void k_kv_join_pieces(KvAttn a) {
   store_out4(a, (int64_t)q.row0 + qt, h * a.G + (c - qt * a.G), D, d, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
 }
 
-KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt) {
+KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt, bool masked) {
   int64_t most = b.max_kv;
   if (causal && window && (int64_t)window + b.max_q < most) most = (int64_t)window + b.max_q;
   int64_t tiles = (most + kTile - 1) / kTile + 1;
@@ -981,6 +1020,12 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int s
   if (chunk < 4) chunk = 4;
   p.chunk = (int)(chunk < tiles ? chunk : tiles);
   p.splits = (int)((tiles + p.chunk - 1) / p.chunk);
+  if (masked && p.splits > 1) {  // split_tiles deals by the lengths: room for twice as many of the longest sequence
+    const int64_t most = (tiles + 3) / 4;
+    p.splits = (int)(2 * p.splits < most ? 2 * p.splits : most);
+    p.chunk = 4;
+    p.notes = b.S * (int)((cols + p.tile - 1) / p.tile);
+  }
   return p;
 }
 
@@ -989,6 +1034,7 @@ hipError_t launch_kv_attn(const KvAttn& a0, int D, int yt, hipStream_t st) {
   const int64_t cts = ((int64_t)a.b.max_q * a.G + a.tile - 1) / a.tile;
   const dim3 grid = a.pieces ? dim3(a.pieces) : dim3((unsigned)(a.splits * cts * a.c.Hkv), a.b.S), block(64 * kWaves);
   const int64_t groups = (int64_t)grid.x * grid.y;
+  a.deal = 2 * device_cus();
   a.snake = groups > device_cus() && groups <= 2 * device_cus();
 #define MD_ATT_M(D_, N_, M_)                                                               \
   do {                                                                                     \
