@@ -20,6 +20,11 @@
 // key of 0.97 of the weight, bf16 out: 0.2% off the definition (the output's
 // rounding); 5% against the running maximum with two digits, one of 8191 24%.
 //
+// Masked calls (M: a tree of drafts, or a window with first positions that stay
+// visible) take the same two forms; they differ in which tiles a column sees (kv.hpp:
+// the first ones, then those of the window) and in how a cut tile's scores are
+// masked: sixteen bits a lane, made of the row's borders and its words of the tree.
+//
 // Operand layout.  Keys enter as the A operand (rows = tokens), queries as B
 // (columns = (query, head) pairs that share the key head), so the scores come
 // out with a column's tokens in one lane: lane l holds column l % 16 and the

@@ -8,6 +8,10 @@
 // lane, four pairs of them, so that a pair never leaves its lane and the sines
 // and cosines, which all heads of a row share, are formed once for the lane's
 // pairs and kept in registers over the row's heads.
+//
+// Measured: 8191 rows of 64 + 8 heads of 128, bf16, 62 us (302 MB, 4.9 TB/s, what a
+// large copy reaches); one row of 32 + 4 heads of 64 3 us, its heads shared out over
+// five workgroups.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
