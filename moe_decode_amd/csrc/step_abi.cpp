@@ -241,7 +241,7 @@ md_status md_token_logprobs(const void* logits, int32_t xtype, int64_t stride, i
   const md_status s = md_token_logprobs_workspace_size(rows, vocab, top, &need);
   if (s != MD_OK) return s;
   if (!valid_xtype(xtype)) return fail(MD_ERR_INVALID_ARG, "unknown xtype %d", xtype);
-  if (!std::isfinite(scale) || scale <= 0.0f) return fail(MD_ERR_INVALID_ARG, "log probabilities: scale %g", scale);
+  if (!(scale > 0.0f && scale <= 0x1p64f)) return fail(MD_ERR_INVALID_ARG, "log probabilities: scale %g", scale);
   if (n_tokens < 0) return fail(MD_ERR_SHAPE, "log probabilities: %d tokens", n_tokens);
   if (n_tokens > kMaxGiven) return fail(MD_ERR_UNSUPPORTED, "log probabilities: %d tokens > %d", n_tokens, kMaxGiven);
   if (stride < vocab) return fail(MD_ERR_SHAPE, "log probabilities: row stride %lld < %d", (long long)stride, vocab);

@@ -115,7 +115,7 @@ def test_logprob_refusals():
              tlp=OUT, ws=FAKE, wsb=sz.value):
         return _st(L.md_token_logprobs(x, xt, stride, rows, V, tok, n, scale, top, lp, ent, ids, tlp, ws, wsb, None))
     for kw, want in [(dict(xt=2), "INVALID_ARG"), (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("nan")), "INVALID_ARG"),
-                     (dict(scale=-1.0), "INVALID_ARG"), (dict(n=-1), "SHAPE"), (dict(n=65), "UNSUPPORTED"),
+                     (dict(scale=-1.0), "INVALID_ARG"), (dict(scale=3e38), "INVALID_ARG"), (dict(n=-1), "SHAPE"), (dict(n=65), "UNSUPPORTED"),
                      (dict(stride=99999), "SHAPE"), (dict(x=None), "INVALID_ARG"), (dict(tok=None), "INVALID_ARG"),
                      (dict(lp=None), "INVALID_ARG"), (dict(ids=None), "INVALID_ARG"), (dict(tlp=None), "INVALID_ARG"),
                      (dict(x=FAKE + 2), "ALIGNMENT"), (dict(xt=1, x=FAKE + 1), "ALIGNMENT"), (dict(tok=FAKE + 2), "ALIGNMENT"),
