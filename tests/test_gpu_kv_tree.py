@@ -189,6 +189,68 @@ def test_bad_sequences_and_rows_behind():
     assert (got[:2] == 0).all() and not (got[2] == 0).all()
 
 
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 70)])
+def test_captured_calls_follow_lengths_and_trees(yt, window, sinks):
+    """Many columns whose splits are dealt out by the lengths on the device: a graph
+    replayed over other lengths (from nothing cached to the bound) and other trees."""
+    import moe_decode_amd as md
+    import torch
+    rng = np.random.default_rng(21)
+    nq, most = [40, 0, 33], 9000
+    table, n = _tables([most] * 3, 64, rng)
+    m = Cache(n, 1, 64, 64, rng)
+    c, b = _to_gpu(m), _batch(nq, [most] * 3, table)
+    q, qn = _rn(rng, (73, 4, 64), "bf16")
+    masks, pos = md.kv_tree(b, _i32([p for a in nq for p in _tree(rng, a, "tree")]))
+    kw = dict(window=window, sinks=sinks, tree=masks, out_dtype=_dt(yt))
+    md.kv_attention(c, b, q, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = md.kv_attention(c, b, q, **kw)
+    for lens in ([40, 0, 9000], [8999, 17, 33], [3000, 5, 2500], [9000, 9000, 9000]):
+        bits = [x for a in nq for x in M.tree_bits(_tree(rng, a, "tree"))]
+        masks.copy_(torch.from_numpy(M.pack(bits, 1)))
+        b.kv_len.copy_(_i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, md.kv_attention(c, b, q, **kw))
+        at = 0
+        for s, (a, length) in enumerate(zip(nq, lens)):
+            if not a:
+                continue
+            rows = sorted({0, a // 2, a - 1})
+            seen = [M.visible(length, a, i, window, sinks, bits[at + i]) for i in rows]
+            o, tol = M.attend(qn[[at + i for i in rows]], m.values("k", table[s], length), m.values("v", table[s], length),
+                              64 ** -0.5, seen, yt, True)
+            err = np.abs(got[[at + i for i in rows]].float().cpu().numpy() - o)
+            assert (err <= tol).all(), (lens, s, float((err / tol).max()))
+            at += a
+
+
+def test_calls_on_two_streams():
+    """Two calls at once, each on its own stream and workspace."""
+    import moe_decode_amd as md
+    import torch
+    rng = np.random.default_rng(22)
+    table, n = _tables([5000, 3000], 64, rng)
+    c = _to_gpu(Cache(n, 2, 64, 64, rng))
+    b = _batch([64, 40], [5000, 3000], table)
+    q = [_rn(rng, (104, 8, 64), "f32")[0] for _ in range(2)]
+    masks, _ = md.kv_tree(b, _i32([p for a in (64, 40) for p in _tree(rng, a, "tree")]))
+    x = torch.randn(2100, 4096, device="cuda")
+    W = torch.randn(256, 4096, device="cuda") * 0.02
+    r = md.Routing(8, "sigmoid")
+    want = [md.kv_attention(c, b, t, tree=masks) for t in q] + list(md.moe_route(x, W, r))
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        got = [md.kv_attention(c, b, t, tree=masks, stream=st) for t, st in zip(q, s)] + \
+            list(md.moe_route(x, W, r, stream=s[2]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, w) for a, w in zip(got, want))
+
+
 @pytest.mark.parametrize("nq", [[1], [5, 0, 64], [65, 1, 130], [1024]])
 def test_masks_and_positions(nq):
     import moe_decode_amd as md
