@@ -699,13 +699,13 @@ md_status md_qk_norm_rope(const md_rope *r /*host*/, const int32_t *positions, i
  * descending order, gates: their s (not c), with renorm divided by the chosen
  * ones' sum (a sum of 0 gives gates of 0), times scale.  Equal values go to the
  * lower run and expert.  Scores, values and gates are fp64 until a gate is rounded
- * to fp32, so that the choice is the definition's.  Where that pays (some 2.5
- * Gflop of products from bf16, 5 from fp32) a call that asks for no logits forms
- * them on the bf16 matrix cores first, off by at most 5.5 2^-23 |x| |w| (the norms
- * of the token and of the longest row of W_r; an instruction there is taken to be
- * off by 2^-23 of its sum), and does in fp64 only the tokens whose choice that
- * leaves open: the choice is the definition's there too, and a gate is off by what
- * its logits' bound allows, relatively by at most 4.1 times it (measured: 1e-7).
+ * to fp32, so that the choice is the definition's.  Where that pays (from some 2
+ * Gflop of products on) a call that asks for no logits forms them on the fp16 matrix
+ * cores first, off by at most 6.25 2^-23 |x| |w| (fp32 x: 9.25; the norms of the token
+ * and of the longest row of W_r; an instruction there is taken to be off by 2^-23 of
+ * its sum), and does in fp64 only the tokens whose choice that leaves open: the
+ * choice is the definition's there too, and a gate is off by what its logits' bound
+ * allows, relatively by at most 4.1 times it (measured: 1e-7).
  * x: T x H fp32 or bf16; logits (T x E fp32, may be NULL).  T: 0..2^20 (0: nothing
  * to do); H, E, k as md_moe_route_topk; groups: up to 64.  A NaN is the smallest of
  * all (as -inf is, which closes an expert in balance); idx then still names k

@@ -266,6 +266,7 @@ constexpr int kRouteFew = 8;  // tokens of the form that has a workgroup for eac
 struct RouteArgs {
   double* part;               // [S][T][E]
   int S, T, H, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
+  bool f32;                   // x
   float scale;
   const float *bias, *balance;
   float* logits;
@@ -277,9 +278,9 @@ struct RouteArgs {
 struct RoutePlan {
   int S, Ks;  // slices of the width and the width of one
   bool fast;
-  size_t planes, wnorm, most, xnorm, count, list, part, bytes;  // the workspace's parts and size
+  size_t planes, scales, wnorm, most, xnorm, count, list, part, bytes;  // the workspace's parts and size
 };
-// fast: the bf16 form may be taken (no logits are asked for)
+// fast: the fp16 form may be taken (no logits are asked for)
 RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast);
 hipError_t launch_route(const RouteArgs& g, const RoutePlan& p, const void* x, int xt, const float* Wr, void* ws,
                         hipStream_t st);

@@ -9,7 +9,7 @@
 // fp64 (the logits are rounded to fp32 once, as the layer's own router's are):
 // products of two fp32 values are exact there, and the choice is the
 // definition's.  Where the fp64 matrix cores would be what a call waits for (78
-// Tflop/s), the logits are formed on the bf16 ones first, with a bound on their
+// Tflop/s), the logits are formed on the fp16 ones first, with a bound on their
 // error, and only the tokens whose choice that bound leaves open are done in fp64.
 #include <hip/hip_runtime.h>
 
@@ -178,43 +178,55 @@ __global__ __launch_bounds__(256) void k_route_gemm(const void* __restrict__ x, 
   }
 }
 
-// The bf16 form.  An fp32 value is the sum of three bf16 (8 + 8 + 8 bits, each
-// part at most 2^-9 of the one before), so a product with a bf16 x is three
-// products, with an fp32 x the six that are not below 2^-26 of it.  The first
-// parts' product is summed in fp32 over 64 columns, the others, which are small,
-// over kRest, and these sums are added in fp64.  With |x|, |w| the norms of the
+// The fp16 form.  64 columns of a row, scaled by a power of two to a largest value
+// in [2^14, 2^15), are two fp16 (11 + 11 bits, the second at most 2^-11 of the first),
+// off by at most 2^-23; a bf16 x is one.  A product with a bf16 x is two products,
+// with an fp32 x the three that are not below 2^-22 of it.  64 columns are summed in
+// fp32, the small parts first, and added in fp64.  With |x|, |w| the norms of the
 // rows, a partial sum over some columns is at most |x| |w| of these, and the parts'
 // products add up to at most the whole's.  An instruction is taken to be off by at
-// most 2^-23 of its sum: there are four of full size in 64 columns, and at most 320
-// below 2^-8 (1 + 2^-4) of it in kRest.  In all 2^-23 (4 + 1.33) |x| |w|, and 2^-26
-// for the products left out: kFastError.  What lies below bf16's smallest normal
-// adds 2^-119 (|x| + |w|).  Measured, random rows, rows without any cancellation,
-// growing, falling: at most 0.13 2^-23 |x| |w|.  Of 8191 tokens some 100 are left
-// open (sigmoid, 8 of 256).
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// most 2^-23 of its sum: there are four of full size in 64 columns, those of the
+// small parts add 2^-8; values below fp16's smallest normal one are lost if the
+// instruction flushes them, 2^-14 of 2^14 for each of 64 columns on either side, at
+// most 2^-24; a slice's sum is rounded to fp32.  In all, in 2^-23 |x| |w|: 4.01, 1 for
+// W_r's parts, 0.5 and 0.5; with an fp32 x 1 more for its parts and 2 for the products left out: fast_error.  What
+// fp32's own range loses adds 2^-119 (|x| + |w|).  Measured, in the same unit: random
+// rows 0.05, without any cancellation 0.16, with sizes over orders of magnitude (few
+// products make the sum) 1.45.  Of 8191 random tokens some 100 are left open (sigmoid,
+// 8 of 256).
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr double kFastError = 5.5 * 0x1p-23;
-constexpr int kRest = 1024;
+constexpr float fast_error(bool f32) { return (f32 ? 9.25f : 6.25f) * 0x1p-23f; }
 constexpr int kTT = 64, kFT = 128;  // tokens and experts of a workgroup
-template <int XT> constexpr int kFastStep = XT == XF32 ? 32 : 64;
+constexpr int kFastStep = 64;  // columns
 
-MD_DEV void split3(float v, uint16_t& a, uint16_t& b, uint16_t& c) {
-  a = to_bf16(v);
-  v -= __uint_as_float((uint32_t)a << 16);
-  b = to_bf16(v);
-  c = to_bf16(v - __uint_as_float((uint32_t)b << 16));
+// The power of two that brings values of at most m into [2^14, 2^15), and back.
+MD_DEV float scale_to_half(float m, float& back) {
+  const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
+  back = __uint_as_float((e - 14) << 23);
+  return __uint_as_float((268 - e) << 23);
+}
+MD_DEV uint32_t half_bits(_Float16 v) { return __builtin_bit_cast(uint16_t, v); }
+// v in two fp16, rounded to nearest
+MD_DEV void split2(float v, uint32_t& a, uint32_t& b) {
+  const _Float16 h = (_Float16)v;
+  a = half_bits(h);
+  b = half_bits((_Float16)(v - (float)h));
 }
 
-// The three parts of W_r as the product's operands (rows up to a whole tile are
-// zeros): [32 experts][16 columns][part][lane][8], its rows' squared norms over
-// 256 columns each, and an empty list.  A wave makes the operands of 64 columns.
+// The two parts of W_r as the product's operands (rows up to a whole tile are
+// zeros): [32 experts][16 columns][part][lane][8], what 64 columns were scaled by
+// ([64 columns][expert of whole tiles]), its rows' squared norms over 256 columns
+// each, and an empty list.  A wave makes the operands of 64 columns.
 __global__ __launch_bounds__(256) void k_route_split(const float* __restrict__ Wr, int E, int H, uint16_t* __restrict__ planes,
-                                                     float* __restrict__ norms, int* __restrict__ count) {
+                                                     float* __restrict__ scales, float* __restrict__ norms,
+                                                     int* __restrict__ count) {
   __shared__ float s_n[4][32];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 32 + (lane & 31), c0 = blockIdx.y * 256 + 64 * wave + 8 * (lane >> 5);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *count = 0;
-  float v[4][8], nn = 0.0f;
+  float v[4][8], nn = 0.0f, most = 0.0f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -222,23 +234,30 @@ __global__ __launch_bounds__(256) void k_route_split(const float* __restrict__ W
     if (e < E) load8<XF32>(Wr, (int64_t)e * H + c0 + 16 * k, v[k]);
   }
 #pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      most = fmaxf(most, fabsf(v[k][i]));
+      nn = fmaf(v[k][i], v[k][i], nn);
+    }
+  most = fmaxf(most, xor_lanes<32>(most));
+  float back;
+  const float up = scale_to_half(most, back);
+  if (lane < 32) scales[((int64_t)blockIdx.y * 4 + wave) * (gridDim.x * 32) + e] = back;
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    u32x4 o[3];
+    u32x4 o[2];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      uint16_t a[2], b[2], d[2];
+      uint32_t a[2], b[2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        split3(v[k][i + m], a[m], b[m], d[m]);
-        nn = fmaf(v[k][i + m], v[k][i + m], nn);
-      }
-      o[0][i / 2] = a[0] | (uint32_t)a[1] << 16;
-      o[1][i / 2] = b[0] | (uint32_t)b[1] << 16;
-      o[2][i / 2] = d[0] | (uint32_t)d[1] << 16;
+      for (int m = 0; m < 2; ++m) split2(v[k][i + m] * up, a[m], b[m]);
+      o[0][i / 2] = a[0] | a[1] << 16;
+      o[1][i / 2] = b[0] | b[1] << 16;
     }
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<u32x4*>(planes + (((int64_t)blockIdx.x * (H / 16) + blockIdx.y * 16 + 4 * wave + k) * 3 + p) * 512 +
+    for (int p = 0; p < 2; ++p)
+      *reinterpret_cast<u32x4*>(planes + (((int64_t)blockIdx.x * (H / 16) + blockIdx.y * 16 + 4 * wave + k) * 2 + p) * 512 +
                                 8 * lane) = o[p];
   }
   nn += xor_lanes<32>(nn);
@@ -248,211 +267,232 @@ __global__ __launch_bounds__(256) void k_route_split(const float* __restrict__ W
     norms[(int64_t)blockIdx.y * E + e] = (s_n[0][lane] + s_n[1][lane]) + (s_n[2][lane] + s_n[3][lane]);
 }
 
-// 64 tokens x 128 experts and a K-slice a workgroup, four waves of 64 x 32, two
-// workgroups on a compute unit.  The parts of W_r, in operand order, come straight
-// from L2, a step ahead; x goes through LDS: two buffers, and the two steps behind
-// them on their way in registers.  A[i][k], B[k][j] of the 32x32x16 product: eight
-// k at lane 32 (k / 8) + i (j); D[8 a + 4 (lane / 32) + b][lane % 32] in element
-// 4 a + b.
-// Measured: 8191 tokens x 6144 columns x 256 experts, bf16, 96 us (77 Gflop of
-// parts, 0.8 Pflop/s; the matrix cores are busy for 38 us of them).  With a third
-// of W_r's loads 76 us, with every load from the caches 78, without the products 75,
-// without the sums in fp64 88: mostly the 16 bytes a lane and product that the parts
-// of W_r take through L1, beside the products, not hidden behind them.  Measured and
-// dropped: both operands through LDS 104 us, workgroups of 128 x 128 the same as
-// this, waves of 128 x 32 (half the loads of W_r, one wave a SIMD) 122.
-template <int XT>
-__global__ __launch_bounds__(256, 2) void k_route_fast(const void* __restrict__ x, int T, int H,
-                                                       const uint16_t* __restrict__ planes, int E, int Ks, int S,
-                                                       double* __restrict__ part, float* __restrict__ xnorm,
+// 64 tokens x 32 NW experts and a K-slice a workgroup, NW waves of 64 x 32, two on a
+// SIMD.  The parts of W_r, in operand order, come straight from L2, a step of 64
+// columns ahead; x goes through LDS: two buffers, and the two steps behind them on
+// their way in registers.  A step's sums are added in fp64, and the next step's x is
+// scaled and written, beside the step's products.  A[i][k], B[k][j] of the 32x32x16
+// product: eight k at lane 32 (k / 8) + i (j); D[8 a + 4 (lane / 32) + b][lane % 32]
+// in element 4 a + b.  No load stands behind a branch (rows past T read the last
+// one, steps past the last one again the last): the compiler's waits count loads,
+// and one that may not have been issued makes them wait for those behind it.
+// Measured: 8191 tokens x 6144 columns x 256 experts, bf16, 71 us (52 Gflop of
+// parts; the matrix cores are busy for 21 us of them, the vector ALU for 33), fp32
+// 94.  In three bf16 parts 91 (96 without a scale for 64 columns), loads behind
+// branches +8, the sums and x behind the products +4, workgroups of 64 x 128 (x read
+// twice) +8; LDS read two parts ahead, and the order of products and the vector ALU's
+// work prescribed: the same.  Measured before with three parts and dropped: both
+// operands through LDS +8 us, waves of 128 x 32 (half the loads of W_r, one wave a
+// SIMD) +26.
+template <int XT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_route_fast(const void* __restrict__ x, int T, int H,
+                                                       const uint16_t* __restrict__ planes,
+                                                       const float* __restrict__ scales, int E, int Ks, int S,
+                                                       float* __restrict__ part, float* __restrict__ xnorm,
                                                        const float* __restrict__ wnorm, const float* __restrict__ balance,
                                                        float* __restrict__ most) {
-  constexpr int KS = kFastStep<XT>, C = KS / 8, XP = XT == XF32 ? 3 : 1;  // columns, chunks of 16 bytes, parts of x
-  constexpr int kTile = kTT * KS;                                         // values of a part of x's tile
+  constexpr int KS = kFastStep, C = KS / 8, XP = XT == XF32 ? 2 : 1;  // columns, chunks of 16 bytes, parts of x
+  constexpr int kTile = kTT * KS;                                     // values of a part of x's tile
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * XP * kTile];
+  __shared__ __attribute__((aligned(16))) float s_back[4][kTT];  // what a step's tokens were scaled by
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ets = (E + kFT - 1) / kFT;
+  constexpr int FT = 32 * NW;
+  const int ets = (E + FT - 1) / FT, whole = (E + kFT - 1) / kFT * kFT;
   // workgroups that follow each other go to different dies: those of one die
   // take the same experts and slice, so that its L2 holds these parts of W_r
   const int combo = blockIdx.x % (ets * S), ex = combo % ets, sl = combo / ets;
-  const int t0 = blockIdx.x / (ets * S) * kTT, e0 = ex * kFT;
+  const int t0 = blockIdx.x / (ets * S) * kTT, e0 = ex * FT;
   const int kbeg = sl * Ks, kend = min(kbeg + Ks, H);
   const int l31 = lane & 31, hh = lane >> 5;
-  // sixteen lanes of a fragment read hit sixteen chunks of 256 bytes: two rows of 128, or four of 64
-  auto slot = [](int row, int chunk) { return row * KS + 8 * (chunk ^ (C == 8 ? (row >> 1) & 7 : (row >> 2) & 3)); };
-  // staging: four threads a row, C / 4 chunks of 16 bytes
-  constexpr int CH = C / 4;
-  const int row = tid >> 2, ch0 = (tid & 3) * CH;
-  float xreg[2][XT == XF32 ? 8 * CH : 1];
+  // sixteen lanes of a fragment read hit sixteen chunks of 256 bytes: two rows of 128
+  auto slot = [](int row, int chunk) { return row * KS + 8 * (chunk ^ ((row >> 1) & 7)); };
+  // staging: NW threads a row, C / NW chunks of 16 bytes
+  constexpr int CH = C / NW;
+  const int row = tid / NW, ch0 = tid % NW * CH;
+  float xreg[2][XT == XF32 ? CH : 1][8];
   u32x4 xraw[2][XT == XF32 ? 1 : CH];
   float xx = 0.0f;
   const bool norms = ex == 0;
   const bool has_t = t0 + row < T;
+  const int64_t row_at = (int64_t)min(t0 + row, T - 1) * H + 8 * ch0;
   auto fetch = [&](int kc, int s) {
-    const int64_t at = (int64_t)(t0 + row) * H + kc + 8 * ch0;
+    const int64_t at = row_at + min(kc, kend - KS);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (XT == XF32) load8<XF32>(x, at + 8 * c, xreg[s][c]);
+      else xraw[s][c] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at + 8 * c);
+    }
+  };
+  // a step's columns of x into LDS: what they are scaled by, and two values a thread at a time
+  float up = 0.0f;
+  auto put_scale = [&](int s, float* to) {
+    float m = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if constexpr (XT == XF32) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (has_t) load8<XF32>(x, at + 8 * c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xreg[s][8 * c + i] = v[i];
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(xreg[s][c][i]));
       } else {
-        xraw[s][c] = u32x4{0, 0, 0, 0};
-        if (has_t) xraw[s][c] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at + 8 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = fmaxf(fmaxf(m, fabsf(__uint_as_float(xraw[s][c][i] << 16))), fabsf(__uint_as_float(xraw[s][c][i])));
       }
     }
+    m = fmaxf(m, xor_lanes<1>(m));
+    m = fmaxf(m, xor_lanes<2>(m));
+    if constexpr (NW == 8) m = fmaxf(m, xor_lanes<4>(m));
+    float back;
+    up = scale_to_half(m, back);
+    to[row] = back;  // (a row's lanes, one value: no branch, behind which the compiler would move the sums)
   };
-  auto put = [&](int buf, int s) {
-    uint16_t* b = lds + buf * XP * kTile;
+  u32x4 o[XP];
+  auto put = [&](int s, int g, uint16_t* b) {
+    const int c = g / 4, i = g % 4;
+    float u, v;
+    if constexpr (XT == XF32) {
+      u = xreg[s][c][2 * i], v = xreg[s][c][2 * i + 1];
+      uint32_t p[2], q[2];
+      split2(u * up, p[0], q[0]);
+      split2(v * up, p[1], q[1]);
+      o[0][i] = p[0] | p[1] << 16;
+      o[XP - 1][i] = q[0] | q[1] << 16;
+    } else {  // exact, down to fp16's smallest normal value
+      u = __uint_as_float(xraw[s][c][i] << 16), v = __uint_as_float(xraw[s][c][i] & 0xFFFF0000u);
+      o[0][i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(u * up, v * up));
+    }
+    if (norms) xx = fmaf(u, u, fmaf(v, v, xx));
+    if (i == 3) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if constexpr (XT == XF32) {
-        u32x4 o[3];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          uint16_t p[3][2];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const float v = xreg[s][8 * c + i + m];
-            split3(v, p[0][m], p[1][m], p[2][m]);
-            if (norms) xx = fmaf(v, v, xx);
-          }
-#pragma unroll
-          for (int q = 0; q < 3; ++q) o[q][i / 2] = p[q][0] | (uint32_t)p[q][1] << 16;
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<u32x4*>(b + q * kTile + slot(row, ch0 + c)) = o[q];
-      } else {
-        *reinterpret_cast<u32x4*>(b + slot(row, ch0 + c)) = xraw[s][c];
-        if (norms) {
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float u = __uint_as_float(xraw[s][c][m] << 16), v = __uint_as_float(xraw[s][c][m] & 0xFFFF0000u);
-            xx = fmaf(u, u, fmaf(v, v, xx));
-          }
-        }
-      }
+      for (int q = 0; q < XP; ++q) *reinterpret_cast<u32x4*>(b + q * kTile + slot(row, ch0 + c)) = o[q];
     }
   };
-  // the wave's operands of W_r, a step's
-  bf16x8 w[KS / 16][3];
-  const uint16_t* wp = planes + ((int64_t)(4 * ex + wave) * (H / 16) + kbeg / 16) * 1536 + 8 * lane;
-  auto load_w = [&](int k) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) w[k][p] = *reinterpret_cast<const bf16x8*>(wp + k * 1536 + p * 512);
-  };
+  // the wave's operands of W_r, a step's, and what its columns were scaled by
+  f16x8 w[KS / 16][2];
+  float wback;
+  const int e = e0 + 32 * wave + l31;
+  const uint16_t* wp = planes + ((int64_t)(NW * ex + wave) * (H / 16) + kbeg / 16) * 1024 + 8 * lane;
+  const float* sp = scales + (int64_t)(kbeg / 64) * whole + e;
+  auto load_w = [&](int k, int p) { w[k][p] = *reinterpret_cast<const f16x8*>(wp + k * 1024 + p * 512); };
   double acc[2][16];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.0;
-  if (blockIdx.x == 0 && wave == 0) {  // what every token's bound needs: the largest squared norm and finite balance
-    float wn_max = 0.0f, bal = 0.0f;
-    for (int e = lane; e < E; e += 64) {
-      float n = 0.0f;
-#pragma unroll 8
-      for (int c = 0; c < H / 256; ++c) n += wnorm[(int64_t)c * E + e];
-      wn_max = fmaxf(wn_max, n);
-      if (balance && balance[e] > -INFINITY) bal = fmaxf(bal, fabsf(balance[e]));
+  if (blockIdx.x == 0) {  // what every token's bound needs: the largest squared norm and finite balance
+    float n = 0.0f, bal = 0.0f;  // E is up to 256
+    if (tid < E) {
+#pragma unroll 16
+      for (int c = 0; c < H / 256; ++c) n += wnorm[(int64_t)c * E + tid];
+      if (balance && balance[tid] > -INFINITY) bal = fabsf(balance[tid]);
     }
-    wn_max = group_max<64>(wn_max);
+    n = group_max<64>(n);
     bal = group_max<64>(bal);
-    if (lane == 0) most[0] = wn_max, most[1] = bal;
+    if (lane == 0 && wave < 4) s_back[0][wave] = n, s_back[1][wave] = bal;
+    __syncthreads();
+    if (tid < 2) most[tid] = fmaxf(fmaxf(s_back[tid][0], s_back[tid][1]), fmaxf(s_back[tid][2], s_back[tid][3]));
+    __syncthreads();
   }
-  f32x16 d[2], r[2];  // the first parts' product, and the others
+  f32x16 d[2][2];  // of two steps: the sums of the one before are added beside the products of this one
+  double sw = 0.0;  // what its columns of W_r were scaled by
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[t][i] = 0.0f;
-  // first, last: of 64 columns; flush: of kRest; more: a step follows
-  auto step = [&](int buf, bool first, bool last, bool flush, bool more) {
-    constexpr int K = KS / 16;
-    const uint16_t* b = lds + buf * XP * kTile;
-    bf16x8 v[2][2][XP];
-    auto read = [&](int k) {
+    for (int i = 0; i < 16; ++i) d[1][t][i] = 0.0f;
+  if (tid < kTT) s_back[3][tid] = 0.0f;
+  auto add = [&](int h, int g, const f32x4& sx) {
+    const int t = g / 4, a = g % 4;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int p = 0; p < XP; ++p)
-          v[k & 1][t][p] = *reinterpret_cast<const bf16x8*>(b + p * kTile + slot(32 * t + l31, 2 * k + hh));
-    };
-    if (first) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[t][i] = 0.0f;
-    }
-    wp += K * 1536;
-    read(0);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k + 1 < K) read(k + 1);
-#pragma unroll
-      for (int o = 2; o >= 0; --o)
-#pragma unroll
-        for (int p = 0; p < XP; ++p) {
-          const int q = o - p;
-          if (q < 0) continue;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            f32x16& to = o ? r[t] : d[t];
-            to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[k & 1][t][p], w[k][q], to, 0, 0, 0);
-          }
-        }
-      if (more) load_w(k);
-    }
-    if (last) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[t][i] += (double)d[t][i];
-    }
-    if (flush) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc[t][i] += (double)r[t][i];
-          r[t][i] = 0.0f;
-        }
-    }
+    for (int i = 0; i < 4; ++i) acc[t][4 * a + i] = fma((double)(d[h][t][4 * a + i] * sx[i]), sw, acc[t][4 * a + i]);
   };
+  auto scaled = [&](int st, int g) {
+    return *reinterpret_cast<const f32x4*>(s_back[st & 3] + 32 * (g / 4) + 8 * (g % 4) + 4 * hh);
+  };
+  // step st, in LDS h; the next one comes from registers 1 - h
+  auto step = [&](int h, int st, bool more) {
+    const uint16_t* b = lds + h * XP * kTile;
+    uint16_t* nb = lds + (1 - h) * XP * kTile;
+    f16x8 v[2][2], v1[2][2];
+    auto read = [&](int g) {
 #pragma unroll
-  for (int k = 0; k < KS / 16; ++k) load_w(k);
+      for (int t = 0; t < 2; ++t) {
+        const uint16_t* at = b + slot(32 * t + l31, 2 * (g % 4) + hh);
+        v[g & 1][t] = *reinterpret_cast<const f16x8*>(at);
+        if (XP == 2 && g < 4) v1[g & 1][t] = *reinterpret_cast<const f16x8*>(at + kTile);
+      }
+    };
+    const double sw_next = (double)wback;
+    if (more) wp += KS * 64, sp += whole;
+    wback = *sp;
+    f32x4 sx[2];
+    read(0);
+    sx[0] = scaled(st + 3, 0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d[h][t][i] = 0.0f;
+    const float so_far = xx;
+    // eight parts, in this order: the loads of W_r behind the products that use their registers up
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const int k = g % 4, p = g < 4 ? 1 : 0;  // the small products first
+      __builtin_amdgcn_sched_barrier(0);
+      if (g < 7) {
+        read(g + 1);
+        sx[(g + 1) & 1] = scaled(st + 3, g + 1);
+      }
+      if (g == 0) put_scale(1 - h, s_back[(st + 1) & 3]);
+      if (XP == 2 && g < 4) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          d[h][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1[g & 1][t], w[k][0], d[h][t], 0, 0, 0);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        d[h][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[g & 1][t], w[k][p], d[h][t], 0, 0, 0);
+      add(1 - h, g, sx[g & 1]);
+      if (CH == 2 || g % 2) put(1 - h, CH == 2 ? g : g / 2, nb);
+      __builtin_amdgcn_sched_barrier(0);
+      load_w(k, p);
+    }
+    xx = more ? xx : so_far;
+    sw = sw_next;
+  };
   fetch(kbeg, 0);
-  if (kbeg + KS < kend) fetch(kbeg + KS, 1);
-  put(0, 0);
-  __syncthreads();
-  for (int kc = kbeg; kc < kend; kc += 2 * KS) {
+  fetch(kbeg + KS, 1);
+  wback = *sp;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // step kc / KS + h is in LDS h, the next one in registers 1 - h
-      const int at = kc + h * KS;
-      if (at >= kend) break;
-      if (at + 2 * KS < kend) fetch(at + 2 * KS, h);
-      step(h, KS == 64 || h == 0, KS == 64 || h == 1, h == 1 && (at + KS - kbeg) % kRest == 0, at + KS < kend);
-      if (at + KS < kend) put(1 - h, 1 - h);
+  for (int p = 1; p >= 0; --p)
+#pragma unroll
+    for (int k = 0; k < KS / 16; ++k) load_w(k, p);
+  put_scale(0, s_back[0]);
+#pragma unroll
+  for (int g = 0; g < 4 * CH; ++g) put(0, g, lds);
+  __syncthreads();
+  for (int kc = kbeg, st = 0; kc < kend; kc += 2 * KS, st += 2) {  // a slice is a multiple of 256 columns
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fetch(kc + (h + 2) * KS, h);
+      __builtin_amdgcn_sched_barrier(0);
+      step(h, st + h, kc + (h + 1) * KS < kend);
       __syncthreads();
     }
   }
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] += (double)r[t][i];
-  const int e = e0 + 32 * wave + l31;
+  for (int g = 0; g < 8; ++g) add(1, g, scaled((kend - kbeg) / KS + 3, g));
   if (e < E) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int tok = t0 + 32 * t + 8 * (i >> 2) + 4 * hh + (i & 3);
-        if (tok < T) part[((int64_t)sl * T + tok) * E + e] = acc[t][i];
+        if (tok < T) part[((int64_t)sl * T + tok) * E + e] = (float)acc[t][i];
       }
   }
   if (norms) {
     xx += xor_lanes<1>(xx);
     xx += xor_lanes<2>(xx);
-    if ((tid & 3) == 0 && has_t) xnorm[(int64_t)sl * T + t0 + row] = xx;
+    if constexpr (NW == 8) xx += xor_lanes<4>(xx);
+    if (tid % NW == 0 && has_t) xnorm[(int64_t)sl * T + t0 + row] = xx;
   }
 }
 
@@ -466,7 +506,7 @@ MD_DEV uint64_t order64(double x) {
 
 // How a token's logits come.
 //   kExact   partials of g.S slices, for every token; everything is fp64
-//   kBounded the bf16 form's: scores and order in fp32, and a token whose choice
+//   kBounded the fp16 form's: scores and order in fp32, and a token whose choice
 //            the bound on both leaves open is put on the list; the winners' scores
 //            are formed again in fp64 for the gates
 //   kListed  the list's tokens, as kExact
@@ -478,21 +518,11 @@ enum Logits { kExact, kBounded, kListed };
 // Measured: one token of 128 experts 5.2 us (a chain of loads, fp64 exp and k
 // rounds), 128 of 256 7.6, 8191 of 256 in fp32 21 (bound by the vector ALU's issue;
 // in fp64 28).
-template <Logits FROM>
-__global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
+template <Logits FROM, typename F = std::conditional_t<FROM == kBounded, float, double>>  // F: of scores
+MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int64_t n, int S) {
   constexpr bool B = FROM == kBounded;
-  using F = std::conditional_t<B, float, double>;  // scores
-  __shared__ F s_c[256];
   const int lane = threadIdx.x;
   const int E = g.E;
-  int64_t t = blockIdx.x, at = t, n = g.T;
-  int S = g.S;
-  if constexpr (FROM == kListed) {
-    n = min(*g.count, g.T);
-    if (t >= n) return;
-    S = list_plan((int)n, E, g.H).S;
-    t = g.list[t];
-  }
   // (loaded first: they are on their way with the partials)
   float bias[4], bal[4];
 #pragma unroll
@@ -511,7 +541,12 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
     for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i][j] = p + j < S && lane + 64 * i < E ? g.part[((int64_t)(p + j) * n + at) * E + lane + 64 * i] : 0.0;
+        if (p + j < S && lane + 64 * i < E) {
+          const int64_t o = ((int64_t)(p + j) * n + at) * E + lane + 64 * i;
+          v[i][j] = B ? (double)reinterpret_cast<const float*>(g.part)[o] : g.part[o];
+        } else {
+          v[i][j] = 0.0;
+        }
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
@@ -567,7 +602,7 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
     for (int p = 0; p < S; ++p) xn += g.xnorm[(int64_t)p * g.T + t];
     far = group_max<64>(far);
     const float nx = sqrtf(xn) * 1.001f, nw = sqrtf(g.most[0]) * 1.001f;  // their own sums' rounding
-    off = (float)kFastError * nx * nw + 0x1p-119f * (nx + nw) + 0x1p-22f * far;
+    off = fast_error(g.f32) * nx * nw + 0x1p-119f * (nx + nw) + 0x1p-22f * far;
     open = !(off < 0.01f);  // past where the slopes hold, or no number
     const float edge = g.sigmoid ? 0x1p-21f * (1.0f + g.most[1]) : 0x1p-24f * top_s + 0x1p-23f * g.most[1] + 1e-14f;
 #pragma unroll
@@ -707,25 +742,41 @@ __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
   }
 }
 
-// Whether the bf16 form pays: both forms' times in us, linear in Gflop (whole tiles
-// of experts in the bf16 form), as measured over 128 to 16384 tokens.  us, bf16
-// form and fp64: 6144 x 256, bf16, 512 tokens 57 and 41, 1024 59 and 72, 8192 158
-// and 439; fp32 1024 86 and 72, 2048 101 and 120, 8192 257 and 435; 2048 x 128, fp32,
-// 4096 76 and 53, 8192 84 and 93; 4096 x 64, bf16, 4096 52 and 54, 8192 66 and 93.
-static bool route_fast(int64_t T, int H, int E, int xt) {
-  const double g = 2e-9 * T * H * E, whole = 2e-9 * T * H * ((E + kFT - 1) / kFT * kFT);
-  return 18.0 + 16.2 * g > (xt == XF32 ? 55.0 + 7.5 * whole : 40.0 + 4.3 * whole);
+template <Logits FROM>
+__global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
+  __shared__ std::conditional_t<FROM == kBounded, float, double> s_c[256];
+  if constexpr (FROM == kListed) {
+    const int n = min(*g.count, g.T), S = list_plan(n, g.E, g.H).S;
+    for (int at = blockIdx.x; at < n; at += gridDim.x) {
+      route_choose<FROM>(g, s_c, g.list[at], at, n, S);
+      __syncthreads();  // s_c
+    }
+  } else {
+    route_choose<FROM>(g, s_c, blockIdx.x, blockIdx.x, g.T, g.S);
+  }
 }
 
-// K-slices of the product: enough that every compute unit has a workgroup, a
-// slice of 256 at least (the bf16 form: of 1024).
+// Whether the fp16 form pays: both forms' times in us, linear in Gflop (whole tiles
+// of experts in the fp16 form), as measured over 128 to 16384 tokens.  us, fp16
+// form and fp64: 6144 x 256, bf16, 512 tokens 69 and 41, 1024 60 and 72, 8192 113
+// and 439; fp32 1024 63 and 72, 8192 140 and 436; 2048 x 128, fp32, 4096 52 and 53,
+// 8192 61 and 93; 4096 x 64, bf16, 4096 49 and 54, 8192 61 and 93.
+static bool route_fast(int64_t T, int H, int E, int xt) {
+  const double g = 2e-9 * T * H * E, whole = 2e-9 * T * H * ((E + kFT - 1) / kFT * kFT);
+  return 18.0 + 16.2 * g > (xt == XF32 ? 48.0 + 3.6 * whole : 46.0 + 2.6 * whole);
+}
+
+// K-slices of the product: enough that every compute unit has a workgroup (of 128 x
+// 128 as it counts here, whether one of 64 x 256 or two of 64 x 128), a slice of 256
+// at least.
 RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast) {
   RoutePlan p{};
   p.Ks = H;
   p.S = 1;
   p.fast = fast && T > kRouteFew && route_fast(T, H, E, xt);
   if (T > kRouteFew) {
-    const int tile = p.fast ? kFT : kGT, step = p.fast ? 1024 : 256;
+    constexpr int step = 256;
+    const int tile = p.fast ? kFT : kGT;
     const int64_t tiles = (int64_t)((E + tile - 1) / tile) * ((T + tile - 1) / tile);
     const int units = (H + step - 1) / step;
     int S = (int)((device_cus() + tiles - 1) / tiles);
@@ -742,15 +793,15 @@ RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast) {
   size_t rows = (size_t)T * p.S;
   if (p.fast) {
     const size_t ets = (E + kFT - 1) / kFT, small = (E + kGT - 1) / kGT;
-    p.planes = take(6 * ets * kFT * H);
+    p.planes = take(4 * ets * kFT * H);
+    p.scales = take(4 * ets * kFT * (H / 64));
     p.wnorm = take(4 * (size_t)E * (H / 256));
     p.most = take(8);
     p.xnorm = take(4 * rows);
     p.count = take(4);
     p.list = take(4 * (size_t)T);
-    // the list's slices: kListGroups workgroups of a tile each, or one slice
-    const size_t listed = (size_t)kListGroups / small * kGT;
-    if (rows < listed) rows = listed;
+    // fp32 sums; over them the list's slices: kListGroups workgroups of a tile each, or one slice
+    rows = std::max((rows + 1) / 2, std::max((size_t)T, (size_t)kListGroups / small * kGT));
   }
   p.part = take(8 * rows * E);
   return p;
@@ -758,15 +809,22 @@ RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast) {
 
 template <int XT>
 static hipError_t launch_fast(const RouteArgs& g, const RoutePlan& p, const void* x, int H, const float* Wr, uint16_t* planes,
-                              hipStream_t st) {
+                              float* scales, hipStream_t st) {
   const int ets = (g.E + kFT - 1) / kFT;
-  hipLaunchKernelGGL(k_route_split, dim3(ets * kFT / 32, H / 256), dim3(256), 0, st, Wr, g.E, H, planes, g.wnorm, g.count);
-  hipLaunchKernelGGL((k_route_fast<XT>), dim3(ets * p.S * ((g.T + kTT - 1) / kTT)), dim3(256), 0, st, x, g.T, H, planes,
-                     g.E, p.Ks, p.S, g.part, g.xnorm, g.wnorm, g.balance, g.most);
+  hipLaunchKernelGGL(k_route_split, dim3(ets * kFT / 32, H / 256), dim3(256), 0, st, Wr, g.E, H, planes, scales, g.wnorm,
+                     g.count);
+  const int tiles = p.S * ((g.T + kTT - 1) / kTT);
+  float* part = reinterpret_cast<float*>(g.part);
+  if (ets == 2)
+    hipLaunchKernelGGL((k_route_fast<XT, 8>), dim3(tiles), dim3(512), 0, st, x, g.T, H, planes, scales, g.E, p.Ks, p.S, part,
+                       g.xnorm, g.wnorm, g.balance, g.most);
+  else
+    hipLaunchKernelGGL((k_route_fast<XT, 4>), dim3(tiles), dim3(256), 0, st, x, g.T, H, planes, scales, g.E, p.Ks, p.S, part,
+                       g.xnorm, g.wnorm, g.balance, g.most);
   hipLaunchKernelGGL((k_route_select<kBounded>), dim3(g.T), dim3(64), 0, st, g);
   hipLaunchKernelGGL((k_route_gemm<XT, true>), dim3(kListGroups), dim3(256), 0, st, x, g.T, H, Wr, g.E, 0, g.part, g.count,
                      g.list);
-  hipLaunchKernelGGL((k_route_select<kListed>), dim3(g.T), dim3(64), 0, st, g);
+  hipLaunchKernelGGL((k_route_select<kListed>), dim3(std::min(g.T, kListGroups)), dim3(64), 0, st, g);
   return hipGetLastError();
 }
 
@@ -784,7 +842,10 @@ hipError_t launch_route(const RouteArgs& g0, const RoutePlan& p, const void* x, 
     g.count = reinterpret_cast<int*>(at + p.count);
     g.list = reinterpret_cast<int*>(at + p.list);
     uint16_t* planes = reinterpret_cast<uint16_t*>(at + p.planes);
-    return xt == XF32 ? launch_fast<XF32>(g, p, x, H, Wr, planes, st) : launch_fast<XBF16>(g, p, x, H, Wr, planes, st);
+    float* scales = reinterpret_cast<float*>(at + p.scales);
+    g.f32 = xt == XF32;
+    return xt == XF32 ? launch_fast<XF32>(g, p, x, H, Wr, planes, scales, st)
+                      : launch_fast<XBF16>(g, p, x, H, Wr, planes, scales, st);
   }
   if (g.T <= kRouteFew) {
     if (xt == XF32) hipLaunchKernelGGL((k_route_few<XF32>), dim3(g.E), dim3(256), 0, st, x, g.T, H, Wr, g.E, g.part);

@@ -217,6 +217,34 @@ def test_many_tokens_choose_as_few(T, H, E, xt, kind):
         assert (err <= wg * (4.1 * off + 4 * M.U)).all(), float((err / wg).max())
 
 
+@pytest.mark.parametrize("T,H,E,xt", [(2999, 6144, 256, "bf16"), (2999, 6144, 200, "f32"), (5001, 4096, 100, "bf16")])
+def test_many_tokens_of_uneven_columns(T, H, E, xt):
+    """Values whose sizes differ by orders of magnitude: from column to column, from
+    one run of 64 columns to the next (x one way, W_r the other) and from token to
+    token; and one column alone."""
+    import moe_decode_amd as md
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    runs = torch.exp2(torch.randint(-30, 31, (H // 64,), generator=g, device="cuda").float()).repeat_interleave(64)
+    x, W = rn(T, H), rn(E, H) * (1.5 / H ** 0.5)
+    alone = torch.zeros(H, device="cuda")
+    alone[H // 2 + 5] = H ** 0.5
+    cases = [(x * torch.exp(2 * rn(T, H)) / 8, W * torch.exp(2 * rn(E, H)) / 8), (x * runs, W / runs),
+             (x * torch.exp2(torch.randint(-8, 3, (T, 1), generator=g, device="cuda").float()), W), (x * alone, W)]
+    logits = torch.empty(T, E, device="cuda")
+    for x, W in cases:
+        x = x.to({"f32": torch.float32, "bf16": torch.bfloat16}[xt])
+        off = _off(x, W)
+        for r in (md.Routing(8, "sigmoid", 0.05 * rn(E), scale=2.5), md.Routing(6, renorm=False)):
+            idx, gates = md.moe_route(x, W, r)
+            want, wg = md.moe_route(x, W, r, logits=logits)
+            assert torch.equal(idx, want), (idx != want).any(1).nonzero()[:4].tolist()
+            err, wg = (gates - wg).abs().cpu().numpy(), wg.abs().cpu().numpy()
+            # where the bound is above 0.01 every token is done in fp64
+            assert (err <= wg * (4.1 * np.minimum(off, 0.01) + 4 * M.U)).all(), float((err / wg).max())
+
+
 def test_many_tokens_special_values():
     """Zeros (all experts equal), NaN and infinities in some tokens, closed experts,
     weights near the smallest normal numbers."""
