@@ -28,6 +28,10 @@ FLAGS = [
     "-Wall", "-Wno-unused-function", "-Wno-pass-failed",
     "-I", os.path.join(ROOT, "include"),
 ]
+# attention: matrix instructions write their sums to vector registers in every kernel.  By itself the compiler
+# puts them into accumulation registers in the kernels of more than 256 registers and copies each one back (256
+# channels, fp32 out, few columns: 288 of 1000 vector instructions a tile; many columns: up to 89 registers spilled)
+FILE_FLAGS = {"kvattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 # host-side sanitizers only (the device code is built as usual)
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
@@ -37,8 +41,8 @@ SAN_LINK = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=unde
 def _compile(src, build_dir=BUILD, defines=(), extra=()):
     obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [HIPCC] + FLAGS + list(extra) + [f"-D{d}" for d in defines] + lang + ["-c", os.path.join(CSRC, src), "-o",
-                                                                               obj]
+    cmd = [HIPCC] + FLAGS + FILE_FLAGS.get(src, []) + list(extra) + [f"-D{d}" for d in defines] + lang
+    cmd += ["-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

@@ -435,6 +435,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
   const int tid = threadIdx.x;
   int s = blockIdx.y, plain_seg = blockIdx.x;  // without a deal: one segment a workgroup
   int64_t u = 0, end = 1, total = 0, runs = 0;
+  int run = 0;
   if (a.pieces) {
     // tiles before each sequence; a thread takes `per` neighbouring ones
     const int per = (a.b.S + 255) >> 8;
@@ -470,10 +471,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     __syncthreads();
     // runs of four tiles at least: one a wave
     runs = max(min((int64_t)a.pieces, total / kWaves), (int64_t)(total > 0));
-    if (tid == 0) a.shares[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (blockIdx.x >= runs) return;
-    u = blockIdx.x * total / runs;
-    end = (blockIdx.x + 1) * total / runs;
+    // Runs that follow each other go to workgroups of one die: the column tiles of a
+    // sequence and key head read the same cache, through one L2 (9 x up to 12 drafts on
+    // up to 5000 tokens, 16 heads on 2 of 256: 44.5 -> 42 us; one column tile: no change).
+    run = blockIdx.x;
+    if (run < runs) {
+      const int die = run & 7, each = (int)(runs >> 3);
+      run = die * each + min(die, (int)(runs & 7)) + (run >> 3);
+    }
+    if (tid == 0) a.shares[run] = make_int4(0, 0, 0, 0);
+    if (run >= runs) return;
+    u = run * total / runs;
+    end = (run + 1) * total / runs;
     int lo = 0, hi = a.b.S;  // the sequence of tile u: first[lo] <= u < first[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -501,7 +510,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     const int h = __builtin_amdgcn_readfirstlane(seg / cts), ct = seg - h * cts;
     const Span sp = span_of<M>(a, q, ct * 16, min(ct * 16 + 16, cols));
     // the first one's share of a workgroup goes to its slot 0, the last one's to 1
-    const int slot = from == 0 && to == n ? -1 : 2 * (int)blockIdx.x + (again ? 1 : 0);
+    const int slot = from == 0 && to == n ? -1 : 2 * run + (again ? 1 : 0);
     if (again) __syncthreads();  // the LDS of the one before
     // (said to be the same in all lanes, or every load would ask each of them)
     int lo = max(all.t0 + from, sp.t0), hi = min(all.t0 + to, sp.t1), skip = 0;
@@ -517,7 +526,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
     if (!a.pieces) return;
     if (from == 0 && to < n && tid == 0) {
       const int64_t last = ((first[s] + (int64_t)(seg + 1) * n) * runs - 1) / total;  // the run with its last tile
-      a.shares[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, s, seg, slot);
+      a.shares[run] = make_int4((int)(last - run) + 1, s, seg, slot);
     }
     u += to - from;
     while (u < end && u >= first[s + 1]) ++s;  // u < end <= total: there is one that holds it
