@@ -302,9 +302,9 @@ struct LogpArgs {
   void *part, *keys;  // [rows][segs] of 16 bytes, [rows][segs][top] of 8
 };
 struct LogpPlan {
-  int values, segs, steps;  // values a thread and step, segments of a row, steps of a segment
+  int values, waves, segs, steps;  // values a thread and step, waves of a workgroup, segments of a row, steps of a segment
 };
 LogpPlan logprob_plan(int64_t rows, int vocab);
-hipError_t launch_logprob(const LogpArgs& g, int xt, int values, hipStream_t st);
+hipError_t launch_logprob(const LogpArgs& g, int xt, const LogpPlan& p, hipStream_t st);
 
 }  // namespace md

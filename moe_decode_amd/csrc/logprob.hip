@@ -21,9 +21,12 @@
 //
 // Measured: 4096 rows of 32000 fp32 logits without alternatives 88 us (524 MB, 6.0
 // TB/s); 288 rows of 131071 bf16 with the 8 largest 32 us and 4.6 for the join (75
-// MB: the vector ALU's work a value, not memory; a step a workgroup, bounds and
-// sums joined for each, 44 and 10).  Three or twelve workgroups a compute unit
-// instead of six: 39 and 38 us against 37 with the join.
+// MB: the vector ALU is busy for 21 of them, a chain of steps with a barrier waits for
+// the rest; a step a workgroup, bounds and sums joined for each, 44 and 10).  There,
+// with the join: three or twelve workgroups a compute unit instead of six 39 and 38 us
+// against 37, steps of 16 values a thread 41, 80 registers (six workgroups a compute
+// unit at once) 45.  One row of 131071 fp32 with the 5 largest 9.3 us (the join's keys
+// ranked without a bound 37).
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -156,12 +159,12 @@ MD_DEV float above(float x) {
 constexpr int kPass = 512;                       // keys that a list holds
 constexpr float kLowest = -3.4028234663852886e38f;
 
-template <int XT, int N, bool TOP>  // N values a thread and step
-__global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
-  constexpr int V = XT == XF32 ? 4 : 8, J = N / V;
-  __shared__ float s_m[4], s_s[4], s_sx[4], s_tau[4];
-  __shared__ int s_bad[4], s_cnt;
-  __shared__ Key s_best[4], s_top[kMaxTop], s_list[kPass];
+template <int XT, int N, int NW, bool TOP>  // N values a thread and step, NW waves
+__global__ __launch_bounds__(64 * NW) void k_logprob(LogpArgs g) {
+  constexpr int V = XT == XF32 ? 4 : 8, J = N / V, B = 64 * NW;
+  __shared__ float s_m[NW], s_s[NW], s_sx[NW], s_tau[NW];
+  __shared__ int s_bad[NW], s_cnt;
+  __shared__ Key s_best[NW], s_top[kMaxTop], s_list[kPass];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   if (row >= g.rows) return;
@@ -172,14 +175,14 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15) / es;
   const char* from = base - shift * es;
   const int last = g.vocab + shift;  // values [shift, last) of `from` are the row's
-  const int c_end = min((blockIdx.x + 1) * g.steps * (256 * N), (last + 256 * N - 1) / (256 * N) * (256 * N));
+  const int c_end = min((blockIdx.x + 1) * g.steps * (B * N), (last + B * N - 1) / (B * N) * (B * N));
   // buffer loads: past the row's last 16 bytes they read zeros and touch no memory
   const rsrc_t res = make_res(from, (last * es + 15) & ~15);
   u32x4 w[J];
-  int c0 = blockIdx.x * g.steps * (256 * N);
+  int c0 = blockIdx.x * g.steps * (B * N);
   auto load = [&](int at) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b128(res, (j * 256 + tid) * 16, at * es, 0);
+    for (int j = 0; j < J; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b128(res, (j * B + tid) * 16, at * es, 0);
   };
   if (c0 < c_end) load(c0);
   if (tid == 0) s_cnt = 0;
@@ -189,7 +192,7 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   float m = kLowest, s = 0.0f, sx = 0.0f, tau = -INFINITY;
   int cnt = 0;
   bool bad = false;
-  for (; c0 < c_end; c0 += 256 * N) {
+  for (; c0 < c_end; c0 += B * N) {
     float v[N];
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -198,9 +201,9 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
         if constexpr (XT == XF32) v[j * V + e] = __uint_as_float(w[j][e]);
         else v[j * V + e] = __uint_as_float(e & 1 ? w[j][e >> 1] & 0xFFFF0000u : w[j][e >> 1] << 16);
       }
-    if (c0 + 256 * N < c_end) load(c0 + 256 * N);
-    auto id_of = [&](int n) { return c0 + (n / V * 256 + tid) * V + n % V - shift; };  // value n's, if it is the row's
-    if (c0 < shift || c0 + 256 * N > last) {
+    if (c0 + B * N < c_end) load(c0 + B * N);
+    auto id_of = [&](int n) { return c0 + (n / V * B + tid) * V + n % V - shift; };  // value n's, if it is the row's
+    if (c0 < shift || c0 + B * N > last) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
         if ((unsigned)id_of(n) >= (unsigned)g.vocab) v[n] = -INFINITY;
@@ -230,7 +233,9 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
         __syncthreads();  // s_tau of a step before
         if (lane == 0) s_tau[wave] = nth;
         __syncthreads();
-        tau = fmaxf(fmaxf(s_tau[0], s_tau[1]), fmaxf(s_tau[2], s_tau[3]));
+        tau = s_tau[0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) tau = fmaxf(tau, s_tau[i]);
       }
       // without a bound: all but -inf; behind a bound's step only larger ones (the lower ids are there)
       const float pass = first ? fmaxf(tau, kLowest) : above(tau);
@@ -264,7 +269,7 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
           if (lane == 0) s_best[wave] = best;
           __syncthreads();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) best = s_best[i] > best ? s_best[i] : best;
+          for (int i = 0; i < NW; ++i) best = s_best[i] > best ? s_best[i] : best;
           if (tid == 0) s_list[cnt] = best;
           ++cnt;
           below = best;
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
         __syncthreads();
       }
       if (cnt > kPass / 2) {  // cut to the largest: a step adds up to kMaxTop where it overfills the list
-        rank_keys(s_list, cnt, g.top, s_top, tid, 256);
+        rank_keys(s_list, cnt, g.top, s_top, tid, B);
         __syncthreads();
         if (tid < g.top) s_list[tid] = s_top[tid];
         if (tid == 0) s_cnt = g.top;
@@ -287,8 +292,8 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   const bool wave_bad = __builtin_amdgcn_ballot_w64(bad) != 0;
   if (lane == 0) s_m[wave] = all, s_bad[wave] = wave_bad;
   __syncthreads();
-  all = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) all = fmaxf(all, s_m[i]), bad |= s_bad[i] != 0;
   const float d = fmaxf((m - all) * c, -300.0f), f = __builtin_amdgcn_exp2f(d);
   sx = group_sum<64>(f * fmaf(d, s, sx));
   s = group_sum<64>(f * s);
@@ -296,13 +301,13 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
   Key* out = g.segs == 1 ? s_top : reinterpret_cast<Key*>(g.keys) + (row * g.segs + blockIdx.x) * g.top;
   if constexpr (TOP) {
     __syncthreads();  // s_top of a cut before
-    for (int i = cnt + tid; i < g.top; i += 256) out[i] = 0;
-    rank_keys(s_list, cnt, g.top, out, tid, 256);
+    for (int i = cnt + tid; i < g.top; i += B) out[i] = 0;
+    rank_keys(s_list, cnt, g.top, out, tid, B);
   }
   __syncthreads();
   Sums r{all, 0.0, 0.0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.s += s_s[i], r.sx += s_sx[i];
+  for (int i = 0; i < NW; ++i) r.s += s_s[i], r.sx += s_sx[i];
   r.sx *= 0.6931471805599453;
   if (bad) r.s = __longlong_as_double(0x7FF8000000000000ll);
   if (g.segs > 1) {
@@ -313,10 +318,10 @@ __global__ __launch_bounds__(256) void k_logprob(LogpArgs g) {
     if (wave == 0) fill<XT>(g, row, cnt, s_top);
     __syncthreads();
   }
-  finish<XT>(g, row, r, s_top, tid, 256);
+  finish<XT>(g, row, r, s_top, tid, B);
 }
 
-// A row's segments: one wave.  Up to kPass keys are ranked among all; of more the
+// A row's segments: one wave.  Up to 64 keys are ranked among all; of more the
 // largest are bounded first, as in the segment: a lane's keys in steps of 64, at
 // most kMaxJoin of them.  Keys of 0 are none.
 template <int XT>
@@ -331,15 +336,10 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogpArgs g) {
   Part q[2];  // up to 128 segments
 #pragma unroll
   for (int i = 0; i < 2; ++i) q[i] = lane + 64 * i < g.segs ? p[lane + 64 * i] : Part{kLowest, 0.0f, 0.0f, 0.0f};
-  int have = 0;
-  if (n <= kPass) {
+  Key key[kPass / 64];  // the keys, up to kPass of them
 #pragma unroll
-    for (int i = 0; i < kPass / 64; ++i) {
-      const Key x = lane + 64 * i < n ? k[lane + 64 * i] : 0;
-      if (lane + 64 * i < n) s_list[lane + 64 * i] = x;
-      have += __popcll(__builtin_amdgcn_ballot_w64(x != 0));
-    }
-  }
+  for (int i = 0; i < kPass / 64; ++i) key[i] = n <= kPass && lane + 64 * i < n ? k[lane + 64 * i] : 0;
+  if (lane == 0) s_cnt = 0;
   const float m = group_max<64>(fmaxf(q[0].m, q[1].m));
   double s = 0.0, sx = 0.0;
 #pragma unroll
@@ -352,20 +352,30 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogpArgs g) {
   }
   const Sums r{m, wave_total(s), wave_total(sx)};
   __syncthreads();
+  Key best = 0;
   if (n <= kPass) {
-    rank_keys(s_list, n, g.top, s_top, lane, 64);
+#pragma unroll
+    for (int i = 0; i < kPass / 64; ++i) best = key[i] > best ? key[i] : best;
   } else {
-    Key best = 0;
     for (int i = lane; i < n; i += 64) best = k[i] > best ? k[i] : best;
-    if (lane == 0) s_cnt = 0;
-    const Key nth = wave_nth(best, g.top), tau = nth > 1 ? nth : 1;
-    __syncthreads();
-    for (int i = lane; i < n; i += 64)
-      if (k[i] >= tau) s_list[atomicAdd(&s_cnt, 1)] = k[i];
-    __syncthreads();
-    have = s_cnt;
-    rank_keys(s_list, have, g.top, s_top, lane, 64);
   }
+  Key tau = 1;
+  if (n > 64) {
+    const Key nth = wave_nth(best, g.top);
+    if (nth > tau) tau = nth;
+  }
+  auto pass = [&](Key x) {
+    if (x >= tau) s_list[atomicAdd(&s_cnt, 1)] = x;
+  };
+  if (n <= kPass) {
+#pragma unroll
+    for (int i = 0; i < kPass / 64; ++i) pass(key[i]);
+  } else {
+    for (int i = lane; i < n; i += 64) pass(k[i]);
+  }
+  __syncthreads();
+  const int have = s_cnt;
+  rank_keys(s_list, have, g.top, s_top, lane, 64);
   __syncthreads();
   if (have < g.top) {
     fill<XT>(g, row, have, s_top);
@@ -387,23 +397,33 @@ LogpPlan logprob_plan(int64_t rows, int vocab) {
   if (segs > kMaxSegs) segs = kMaxSegs;
   p.steps = (int)((total + segs - 1) / segs);
   p.segs = (total + p.steps - 1) / p.steps;
+  p.waves = 4;
+  // A row that one step of sixteen waves holds, at least half full, and a compute unit
+  // for each row: no second kernel.  us, in one and in two, the 5 largest of fp32, one
+  // row of 32000 in a graph 9.4 and 9.2, from the host 11.6 and 14.3; 64 rows 10.3 and
+  // 11.2, 256 rows 13.7 and 16.0; one of 4000 9.6 and 8.3, of 65000 (two steps) 13.5
+  // and 9.0.
+  constexpr int wide = 1024 * 32;
+  if (rows <= cus && vocab > wide / 2 && vocab + 7 <= wide) p = LogpPlan{32, 16, 1, 1};
   return p;
 }
 
-hipError_t launch_logprob(const LogpArgs& g, int xt, int values, hipStream_t st) {
+hipError_t launch_logprob(const LogpArgs& g, int xt, const LogpPlan& p, hipStream_t st) {
   const unsigned y = g.rows < 32768 ? (unsigned)g.rows : 32768u, z = (unsigned)((g.rows + y - 1) / y);
-  const dim3 grid(g.segs, y, z), block(256);
-#define MD_LOGP(X_, N_)                                                                        \
+  const dim3 grid(g.segs, y, z), block(64 * p.waves);
+#define MD_LOGP(X_, N_, W_)                                                                    \
   do {                                                                                         \
-    if (g.top) hipLaunchKernelGGL((k_logprob<X_, N_, true>), grid, block, 0, st, g);           \
-    else hipLaunchKernelGGL((k_logprob<X_, N_, false>), grid, block, 0, st, g);                \
+    if (g.top) hipLaunchKernelGGL((k_logprob<X_, N_, W_, true>), grid, block, 0, st, g);       \
+    else hipLaunchKernelGGL((k_logprob<X_, N_, W_, false>), grid, block, 0, st, g);            \
   } while (0)
   if (xt == XF32) {
-    if (values == 32) MD_LOGP(XF32, 32);
-    else MD_LOGP(XF32, 8);
+    if (p.waves == 16) MD_LOGP(XF32, 32, 16);
+    else if (p.values == 32) MD_LOGP(XF32, 32, 4);
+    else MD_LOGP(XF32, 8, 4);
   } else {
-    if (values == 32) MD_LOGP(XBF16, 32);
-    else MD_LOGP(XBF16, 8);
+    if (p.waves == 16) MD_LOGP(XBF16, 32, 16);
+    else if (p.values == 32) MD_LOGP(XBF16, 32, 4);
+    else MD_LOGP(XBF16, 8, 4);
   }
 #undef MD_LOGP
   hipError_t e = hipGetLastError();

@@ -278,7 +278,7 @@ md_status md_token_logprobs(const void* logits, int32_t xtype, int64_t stride, i
     g.part = workspace;
     g.keys = static_cast<char*>(workspace) + part_bytes(rows, g.segs);
   }
-  const hipError_t e = md::launch_logprob(g, xtype, plan.values, stream);
+  const hipError_t e = md::launch_logprob(g, xtype, plan, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "log probabilities launch");
 }
 

@@ -136,6 +136,40 @@ def test_rows_that_have_no_distribution(V):
         assert torch.equal(a[:1], b)
 
 
+@pytest.mark.parametrize("V", [16384, 16385, 24001, 32761, 32762])
+def test_rows_of_one_step(V):
+    """Around the lengths that one workgroup takes in one step: each of the cases above."""
+    rng = np.random.default_rng(V)
+    for xt in ("f32", "bf16"):
+        test_sizes(1, V, xt)
+        test_equal_logits_go_to_the_lower_id(V, xt)
+        for offset in (1, 7):
+            _check(_logits(rng, 3, V, xt, V + 13, offset), rng.integers(0, V, (3, 2)).astype(np.int32), 4, 1.0)
+        for rows in (256, 257) if (V, xt) == (16385, "f32") else ():
+            _check(_logits(rng, rows, V, xt), rng.integers(0, V, (rows, 1)).astype(np.int32), 3, 1.0)
+    test_masked_logits(V)
+    test_rows_that_have_no_distribution(V)
+
+
+@pytest.mark.parametrize("top", [1, 13, 32])
+def test_many_segments_and_few_keys(top):
+    """Rows of many segments whose largest all lie in one of them, or in all; most
+    segments masked; equal ones."""
+    import torch
+    V = 262149
+    rng = np.random.default_rng(top)
+    x = _logits(rng, 6, V, "bf16")
+    x[0] = -1.0
+    x[0, 70000:70040] = torch.arange(40, device="cuda").bfloat16()
+    x[1] = 0.25
+    x[2, 4096:] = float("-inf")
+    x[3, : V - 5] = float("-inf")
+    x[4] = float("-inf")
+    x[4, ::8192] = 3.0
+    x[5, 1::2] = float("-inf")
+    _check(x, rng.integers(0, V, (6, 2)).astype(np.int32), top, 1.0)
+
+
 def test_many_rows_and_rows_behind():
     """More rows than a grid's second axis; outputs given by the caller, whose
     rows behind the call's stay."""
