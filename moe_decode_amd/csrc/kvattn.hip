@@ -542,8 +542,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_attn(KvAtt
 // f16, and so is a weight p times a unit times vs / R, R the power of two at or
 // below the largest value scale met so far.  NS = 2 (fp32 outputs) takes a second
 // f16 for what the first one leaves, 22 bits together, and the unit 2^14, which
-// keeps both parts of weights down to 2^-18 whole; it does not fit the registers at
-// 128 channels (22 spilled) and 256 (89).  NS = 1: a row's reference
+// keeps both parts of weights down to 2^-18 whole; plain calls of 128 channels do not
+// fit the registers (22 spilled).  NS = 1: a row's reference
 // follows its maximum only where that has grown by 2^7, so p stays below 2^7 and
 // the unit is 2^7 (a weight below 2^-21 loses bits, 2^-32 at most); without that
 // some column's maximum moves in most tiles and the sums are rescaled there
@@ -632,8 +632,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attn_rows(KvAttn a
   // blocks of 32 tokens of a softmax step: a masked call with two parts of each
   // weight and 128 channels or more takes them one by one, which spares registers:
   // reloads of spilled ones wait for the next tile's loads too (2 x 61 drafts on up
-  // to 65535 tokens, 32 heads on 8 of 128: 317 us with 27 spilled, 263 with none;
-  // 256 channels: 92 spilled, 47)
+  // to 65535 tokens, 32 heads on 8 of 128: 317 us with 27 spilled, 263 with none)
   constexpr int NB = M && NS == 2 && D > 64 ? 1 : 2;
   constexpr float kLag = NS == 1 ? 7.0f : 0.0f, kUnit = NS == 1 ? 128.0f : 16384.0f;
   constexpr int L = kTile * D / 16 / 256;  // 16-byte chunks of codes per thread, keys or values
@@ -1003,10 +1002,11 @@ KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int s
   KvPlan p{};
   // More than four column tiles: the form that shares its loads among 128
   // columns (80 columns, 16 sequences of 4000: 41 us, 51 in the other one; 64:
-  // 41 both).  fp32 outputs of 256 channels do not fit its registers, so there
+  // 41 both).  fp32 outputs of 256 channels leave it one wave a SIMD, so there
   // it is kept for columns by the hundreds (us here and in the other one: 240
-  // columns, 4 sequences of 1000: 53 and 26; 600, 4 of 8000: 197 and 167; 1000,
-  // one of 30000: 235 and 308; 8192, one of 4096: 405 and 446).
+  // columns, 4 sequences of 1000: 42 and 23; 600, 4 of 8000: 176 and 170; 1000,
+  // one of 30000: 182 and 250; 8192, one of 4096: 214 and 223; over trees 96
+  // columns, 9 of 5000: 77 and 57; 240: 42 and 22; 600: 154 and 161; 1000: 197 and 250).
   const int64_t cols = (int64_t)b.max_q * G;
   p.tile = cols > (c.D == 256 && yt == XF32 ? 768 : 64) ? kRowCols : 16;
   p.splits = 1;
