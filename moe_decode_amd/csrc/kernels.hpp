@@ -265,7 +265,8 @@ hipError_t launch_qk_norm_rope(const RopeArgs& g, bool pairs, int xt, int yt, hi
 constexpr int kRouteFew = 8;  // tokens of the form that has a workgroup for each expert
 struct RouteArgs {
   double* part;               // [S][T][E]
-  int S, T, H, E, k, sigmoid, groups, kept, lanes, best_two, renorm;  // lanes: of a wave for each group
+  int S, T, H, E, k, sigmoid, groups, kept, lane_bits, best_two, renorm;  // lane_bits: 2^ lanes of a wave for each group
+  int per, per_inv;           // experts of a group; e / per = e per_inv >> 16 for e below 256
   bool f32;                   // x
   float scale;
   const float *bias, *balance;

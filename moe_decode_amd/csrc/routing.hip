@@ -515,12 +515,20 @@ enum Logits { kExact, kBounded, kListed };
 // A wave for each token: lane l holds experts l + 64 i.  Groups are valued by
 // 64 / groups lanes each (a power of two); the k winners are taken one at a
 // time: the larger key (its high word, then its low one), then the lower expert.
+// What the winners bring with them waits in LDS until all are known (carried through
+// the rounds by selects and lane reads 22 us where this takes 16.5).
 // Measured: one token of 128 experts 5.2 us (a chain of loads, fp64 exp and k
-// rounds), 128 of 256 7.6, 8191 of 256 in fp32 21 (bound by the vector ALU's issue;
-// in fp64 28).
-template <Logits FROM, typename F = std::conditional_t<FROM == kBounded, float, double>>  // F: of scores
-MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int64_t n, int S) {
+// rounds), 128 of 256 7.2, 8191 of 256 in fp32 16.5 (bound by the vector ALU's issue).
+template <bool B>
+struct RouteLds {  // of each expert
+  using F = std::conditional_t<B, float, double>;  // scores
+  F c[256], s[256];    // s: B: what c may be off by
+  double l[B ? 256 : 1];
+};
+template <Logits FROM>
+MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, int64_t t, int64_t at, int64_t n, int S) {
   constexpr bool B = FROM == kBounded;
+  using F = typename RouteLds<B>::F;
   const int lane = threadIdx.x;
   const int E = g.E;
   // (loaded first: they are on their way with the partials)
@@ -625,20 +633,20 @@ MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int6
         hi[i] = (uint32_t)(k >> 32);
         lo[i] = (uint32_t)k;
       }
+      lds.c[e] = c[i];
+      lds.s[e] = B ? delta[i] : s[i];
+      if constexpr (B) lds.l[e] = l[i];
     }
   }
+  __builtin_amdgcn_wave_barrier();
   if (g.kept < g.groups) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < E) s_c[lane + 64 * i] = c[i];
-    __builtin_amdgcn_wave_barrier();
-    const int per = E / g.groups, L = g.lanes, grp = lane / L;
+    const int per = g.per, L = 1 << g.lane_bits, grp = lane >> g.lane_bits;
     auto larger = [](F p, F q) { return p > q ? p : q; };  // no NaN here
     auto smaller = [](F p, F q) { return p > q ? q : p; };
     F a = -INFINITY, b = -INFINITY;  // the group's largest two
     if (grp < g.groups)
-      for (int j = lane % L; j < per; j += L) {
-        const F v = s_c[grp * per + j];
+      for (int j = lane & (L - 1); j < per; j += L) {
+        const F v = lds.c[grp * per + j];
         b = larger(b, smaller(a, v));
         a = larger(a, v);
       }
@@ -664,22 +672,20 @@ MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int6
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !(keep >> (e / per * L) & 1)) hi[i] = lo[i] = 0;
+      if (e < E && !(keep >> ((e * g.per_inv >> 16) << g.lane_bits) & 1)) hi[i] = lo[i] = 0;
     }
   }
   int my_e = 0;
-  F my_s = 0, last_c = 0, last_d = 0;
-  double my_l = 0.0;
+  uint32_t behind = 0;  // behind the last winner: what the others may reach at most
   for (int j = 0; j < g.k + (B ? 1 : 0); ++j) {
-    if (B && j == g.k) {  // behind the last winner: what the others may reach at most
+    if (B && j == g.k) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (hi[i]) hi[i] = order_key32(c[i] + delta[i]);
     }
     const uint32_t h = wave_max_u32(max(max(hi[0], hi[1]), max(hi[2], hi[3])));
-    if (B && h == 0) break;  // k experts are all that may be chosen
     if (B && j == g.k) {
-      open |= !(last_c - last_d > key_logit(h));
+      behind = h;
       break;
     }
     uint64_t has[4];
@@ -702,35 +708,29 @@ MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int6
 #pragma unroll
     for (int i = 3; i >= 0; --i)
       if (has[i]) who = __builtin_ctzll(has[i]), slot = i;
-    F v = s[0], cc = c[0], dd = B ? delta[0] : 0;
-    double lv = l[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (slot == i) v = s[i], cc = c[i], lv = l[i], dd = B ? delta[i] : 0;
-    v = lane_of(v, who);
-    if constexpr (B) {
-      cc = lane_of(cc, who);
-      dd = lane_of(dd, who);
-      if (j) open |= !(last_c - cc > last_d + dd);
-      last_c = cc;
-      last_d = dd;
-      lv = lane_of(lv, who);
-    }
-    if (lane == j) my_s = v, my_e = who + 64 * slot, my_l = lv;
+    if (lane == j) my_e = who + 64 * slot;
     if (lane == who) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (slot == i) hi[i] = lo[i] = 0;
     }
   }
+  const F my_s = lds.s[my_e];
   if constexpr (B) {
+    const float my_c = lds.c[my_e], c0 = __shfl_up(my_c, 1, 64), d0 = __shfl_up(my_s, 1, 64);
+    open |= __builtin_amdgcn_ballot_w64(lane > 0 && lane < g.k && !(c0 - my_c > d0 + my_s)) != 0;
+    // (0: k experts are all that may be chosen)
+    open |= behind && !(lane_of(my_c, g.k - 1) - lane_of(my_s, g.k - 1) > key_logit(behind));
     if (open) {
       if (lane == 0) g.list[atomicAdd(g.count, 1)] = (int)t;  // the order does not matter: each token stands for itself
       return;
     }
   }
   double gate = (double)my_s;
-  if constexpr (B) gate = g.sigmoid ? 1.0 / (1.0 + exp(-my_l)) : exp(my_l - (double)m) * (double)top_s;
+  if constexpr (B) {
+    const double my_l = lds.l[my_e];
+    gate = g.sigmoid ? 1.0 / (1.0 + exp(-my_l)) : exp(my_l - (double)m) * (double)top_s;
+  }
   if (g.renorm) {
     double sum = 0.0;
     for (int j = 0; j < g.k; ++j) sum += lane_of(gate, j);
@@ -744,15 +744,15 @@ MD_DEV void route_choose(const RouteArgs& g, F* s_c, int64_t t, int64_t at, int6
 
 template <Logits FROM>
 __global__ __launch_bounds__(64) void k_route_select(RouteArgs g) {
-  __shared__ std::conditional_t<FROM == kBounded, float, double> s_c[256];
+  __shared__ RouteLds<FROM == kBounded> lds;
   if constexpr (FROM == kListed) {
     const int n = min(*g.count, g.T), S = list_plan(n, g.E, g.H).S;
     for (int at = blockIdx.x; at < n; at += gridDim.x) {
-      route_choose<FROM>(g, s_c, g.list[at], at, n, S);
-      __syncthreads();  // s_c
+      route_choose<FROM>(g, lds, g.list[at], at, n, S);
+      __syncthreads();  // the LDS of the one before
     }
   } else {
-    route_choose<FROM>(g, s_c, blockIdx.x, blockIdx.x, g.T, g.S);
+    route_choose<FROM>(g, lds, blockIdx.x, blockIdx.x, g.T, g.S);
   }
 }
 

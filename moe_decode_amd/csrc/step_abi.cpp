@@ -173,8 +173,10 @@ md_status md_moe_route(const md_routing* r, const void* x, int32_t xtype, int32_
   g.sigmoid = r->score == MD_SCORE_SIGMOID;
   g.groups = r->groups;
   g.kept = r->groups_kept;
-  g.lanes = 1;
-  while (2 * g.lanes * r->groups <= 64) g.lanes *= 2;
+  g.lane_bits = 0;
+  while (2 * r->groups << g.lane_bits <= 64) ++g.lane_bits;
+  g.per = E / r->groups;
+  g.per_inv = 65536 / g.per + 1;
   g.best_two = r->best_two;
   g.renorm = r->renorm;
   g.scale = r->scale;
