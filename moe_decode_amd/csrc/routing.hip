@@ -148,19 +148,27 @@ __global__ __launch_bounds__(256) void k_route_gemm(const void* __restrict__ x, 
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load(u, u);  // a quarter has four steps at least
-    for (int st = 0; st < steps; st += kAhead) {
+    auto mul = [&](int u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[u][a].at(j), wv[u][b].at(j), acc[a][b], 0, 0, 0);
+    };
+    // steps come in fours; no branch around a load: the waits count loads, and would count on none of these
+    for (int st = kAhead; st < steps; st += kAhead) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-              acc[a][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[u][a].at(j), wv[u][b].at(j), acc[a][b], 0, 0, 0);
-        if (st + kAhead < steps) load(u, st + kAhead + u);
+        mul(u);
+        __builtin_amdgcn_sched_barrier(0);
+        load(u, st + u);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) mul(u);
     if (wave) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s_acc[wave - 1][i][lane] = acc[i >> 3][(i >> 2) & 1][i & 3];
