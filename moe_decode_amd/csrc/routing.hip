@@ -539,34 +539,45 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
   using F = typename RouteLds<B>::F;
   const int lane = threadIdx.x;
   const int E = g.E;
-  // (loaded first: they are on their way with the partials)
-  float bias[4], bal[4];
+  // (loaded first: they are on their way with the partials; past the last expert that one again, its
+  // values unused: no branch around a load)
+  int at_e[4];
+  float bias[4] = {0, 0, 0, 0}, bal[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bias[i] = g.bias && lane + 64 * i < E ? g.bias[lane + 64 * i] : 0.0f;
-    bal[i] = g.balance && lane + 64 * i < E ? g.balance[lane + 64 * i] : 0.0f;
+  for (int i = 0; i < 4; ++i) at_e[i] = min(lane + 64 * i, E - 1);
+  if (g.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = g.bias[at_e[i]];
+  }
+  if (g.balance) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bal[i] = g.balance[at_e[i]];
   }
   double l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) l[i] = 0.0;
+  using P = std::conditional_t<B, float, double>;
+  auto rows = [&](int p) { return reinterpret_cast<const P*>(g.part) + ((int64_t)p * n + at) * E; };
   // the slices in order, some on their way at a time
   constexpr int U = B ? 2 : 8;
-  for (int p = 0; p < S; p += U) {
-    double v[4][U];
+  if (S == 1) {
+    const P* r = rows(0);
 #pragma unroll
-    for (int j = 0; j < U; ++j)
+    for (int i = 0; i < 4; ++i) l[i] = (double)r[at_e[i]];
+  } else {
+    for (int p = 0; p < S; p += U) {
+      P v[4][U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p + j < S && lane + 64 * i < E) {
-          const int64_t o = ((int64_t)(p + j) * n + at) * E + lane + 64 * i;
-          v[i][j] = B ? (double)reinterpret_cast<const float*>(g.part)[o] : g.part[o];
-        } else {
-          v[i][j] = 0.0;
-        }
+      for (int j = 0; j < U; ++j) {
+        const P* r = rows(min(p + j, S - 1));
 #pragma unroll
-    for (int j = 0; j < U; ++j)
+        for (int i = 0; i < 4; ++i) v[i][j] = r[at_e[i]];
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[i] += v[i][j];
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[i] += p + j < S ? (double)v[i][j] : 0.0;
+    }
   }
   float f[4], m = -INFINITY, far = 0.0f;
 #pragma unroll
