@@ -64,9 +64,9 @@ __global__ __launch_bounds__(256) void k_route_few(const void* __restrict__ x, i
 // [lane % 16] in element v.  A lane's four neighbouring columns go to four
 // instructions: which column is which k does not matter to a sum.  LIST: of the
 // tokens that a list names, as many as its count says; the grid's workgroups share
-// out tiles and slices.  Measured: 128 tokens x 6144 x 256 13.5 us (0.4 Gflop; 5.5 at
-// the rate of a large product, twice as many slices 17 with the choice 4 slower), a
-// list of some 100 tokens 14, 8191 tokens 420 (61 Tflop/s).
+// out tiles and slices.  Measured: 128 tokens x 6144 x 256 13.1 us (0.4 Gflop; 5.5 at
+// the rate of a large product; twice as many slices: with the choice 23.6 us where
+// this takes 19.6), a list of some 100 tokens 15, 8191 tokens 420 (61 Tflop/s).
 constexpr int kGT = 32;
 constexpr int kAhead = 4;
 
@@ -525,8 +525,9 @@ enum Logits { kExact, kBounded, kListed };
 // time: the larger key (its high word, then its low one), then the lower expert.
 // What the winners bring with them waits in LDS until all are known (carried through
 // the rounds by selects and lane reads 22 us where this takes 16.5).
-// Measured: one token of 128 experts 5.2 us (a chain of loads, fp64 exp and k
-// rounds), 128 of 256 7.2, 8191 of 256 in fp32 16.5 (bound by the vector ALU's issue).
+// Measured: one token of 128 experts 4.1 us (a chain of loads, fp64 exp and k
+// rounds), 128 of 256 5.8, 8191 of 256 in fp32 16.1 (bound by the vector ALU's issue);
+// with loads behind branches, each waited for by itself, 5.2, 7.2 and 16.5.
 template <bool B>
 struct RouteLds {  // of each expert
   using F = std::conditional_t<B, float, double>;  // scores
