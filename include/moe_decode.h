@@ -553,11 +553,15 @@ md_status md_kv_attention(const md_kv_cache *c /*host*/, const md_kv_batch *b /*
  *   where bit j % 64 of its word j / 64 is set (its own too only then; bits
  *   past the run are not read), and every position before the run; with window
  *   > 0, of a of the run's tokens seen, the last max(window - a, 0) of those
- *   positions, and the first `sinks`.  NULL: no tree (words is not read).
+ *   positions, and the first `sinks`.  The window takes no bit away: masks of
+ *   paths that may be longer than it come from md_kv_tree_window with the same
+ *   window and sinks, and a row then sees what its path gives when its tokens
+ *   are decoded one by one.  NULL: no tree (words is not read).
  * A row that sees nothing gives zeros.  Everything else as md_kv_attention with
- * causal 1 (a tree of one chain gives its bits, but for fp32 outputs of many
- * columns of 128 channels or more, whose scores are taken in other blocks, and
- * where splits are dealt out by the lengths on the device).  Errors: as there; a null mask -> MD_ERR_INVALID_ARG; sinks < 0 ->
+ * causal 1 (without a window a tree of one chain gives its bits, but for fp32
+ * outputs of many columns of 128 channels or more, whose scores are taken in
+ * other blocks, and where splits are dealt out by the lengths on the device).
+ * Errors: as there; a null mask -> MD_ERR_INVALID_ARG; sinks < 0 ->
  * MD_ERR_INVALID_ARG; words < 1 or 64 * words < max_q -> MD_ERR_SHAPE; a tree
  * off 8 bytes -> MD_ERR_ALIGNMENT; words > 16384 -> MD_ERR_UNSUPPORTED. */
 typedef struct md_kv_mask {
@@ -589,6 +593,15 @@ md_status md_kv_attention_masked(const md_kv_cache *c /*host*/, const md_kv_batc
  * MD_ERR_UNSUPPORTED; 64 * words < max_q -> MD_ERR_SHAPE. */
 md_status md_kv_tree(const md_kv_batch *b /*host*/, const int32_t *parents, uint64_t *masks, int32_t words,
                      int32_t *positions, hipStream_t stream);
+
+/* md_kv_tree for a sliding window: of a token and its ancestors only the last
+ * `window` (0: all of them) have bits, and those whose place in the text is
+ * among the first `sinks`.  Beside the same window and sinks in
+ * md_kv_attention_masked a row sees, of its path through cache and run, exactly
+ * the last `window` tokens up to its own and the first `sinks`.  positions as
+ * there.  Errors: as there; a negative window or sinks -> MD_ERR_INVALID_ARG. */
+md_status md_kv_tree_window(const md_kv_batch *b /*host*/, const int32_t *parents, int32_t window, int32_t sinks,
+                            uint64_t *masks, int32_t words, int32_t *positions, hipStream_t stream);
 
 /* The values that n pages hold (pages: device, n int32): k and v as
  * [n][kv_heads][page][head_dim] in ytype, both with the token before the

@@ -37,7 +37,7 @@ EXPORTS = ("md_abi_version", "md_status_string", "md_last_error_detail", "md_row
            "md_kv_append", "md_kv_attention_workspace_size", "md_kv_attention", "md_kv_read_pages",
            "md_kv_copy_pages", "md_kv_pages_reset", "md_kv_pages_extend", "md_kv_pages_fork",
            "md_kv_pages_truncate", "md_kv_pages_compact",
-           "md_kv_attention_masked_workspace_size", "md_kv_attention_masked", "md_kv_tree", "md_qk_norm_rope",
+           "md_kv_attention_masked_workspace_size", "md_kv_attention_masked", "md_kv_tree", "md_kv_tree_window", "md_qk_norm_rope",
            "md_moe_route_workspace_size", "md_moe_route", "md_moe_routed_workspace_size",
            "md_moe_layer_forward_routed", "md_token_logprobs_workspace_size", "md_token_logprobs")
 STAGES = {"shared": 0, "router": 1, "select": 2, "gateup": 3, "down": 4, "combine": 5}
@@ -126,6 +126,7 @@ def lib():
             "md_kv_attention_masked_workspace_size": (i32, [vp, vp, i32, vp, i32, psz]),
             "md_kv_attention_masked": (i32, [vp, vp, vp, i32, i32, i64, ctypes.c_float, vp, vp, i32, i64, vp, sz, vp]),
             "md_kv_tree": (i32, [vp, vp, vp, i32, vp, vp]),
+            "md_kv_tree_window": (i32, [vp, vp, i32, i32, vp, i32, vp, vp]),
             "md_qk_norm_rope": (i32, [vp, vp, i32, vp, i32, i64, vp, i32, i64, i32, vp, i64, vp, i64, i32, vp]),
             "md_moe_route_workspace_size": (i32, [i32, i32, i32, psz]),
             "md_moe_route": (i32, [vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
@@ -813,8 +814,11 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
     last `window` of them, and with sinks the first `sinks` of the sequence);
     else every position of its sequence.  tree (int64 [rows][words], as kv_tree
     makes them): the run's tokens are the nodes of a tree, a row sees those whose
-    bits are set and the positions before the run.  out: fp32 or bf16 (out_dtype,
-    fp32 by default); rows behind the last sequence are left as they are."""
+    bits are set, whatever the window, and the positions before the run (window
+    > 0: the last of them, window less the tokens whose bits are set, and the
+    first `sinks`); kv_tree with the same window and sinks sets no bit past them.
+    out: fp32 or bf16 (out_dtype, fp32 by default); rows behind the last sequence
+    are left as they are."""
     import torch
     if q.dim() != 3 or batch.device != cache.device:
         raise ValueError(f"q [rows][q_heads][head_dim] and the batch on {cache.device} wanted")
@@ -863,11 +867,13 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
     return out
 
 
-def kv_tree(batch, parents, masks=None, positions=None, stream=None):
+def kv_tree(batch, parents, masks=None, positions=None, stream=None, window=0, sinks=0):
     """The masks of the batch's trees of drafts, and their tokens' positions in
     the text, from each token's parent (int32 [rows] on the GPU: its number
-    within the run, or -1).  Returns masks (int64 [rows][max_q / 64 rounded up],
-    for kv_attention) and positions (int32 [rows], for qk_norm_rope)."""
+    within the run, or -1).  window > 0 (with kv_attention's own): a token's mask
+    has the last `window` tokens of its path, and those of it among the first
+    `sinks` of the text.  Returns masks (int64 [rows][max_q / 64 rounded up], for
+    kv_attention) and positions (int32 [rows], for qk_norm_rope)."""
     import torch
     rows, dev = parents.shape[0], batch.device
     _dense("parents", parents, (rows,), torch.int32, dev)
@@ -878,7 +884,8 @@ def kv_tree(batch, parents, masks=None, positions=None, stream=None):
             _dense("masks", masks, (rows, masks.shape[1]), torch.int64, dev)
         positions = _result(stream, torch.empty, rows, dtype=torch.int32, device=dev) if positions is None else \
             _dense("positions", positions, (rows,), torch.int32, dev)
-        _check(lib().md_kv_tree(batch.desc(rows), _ptr(parents), _ptr(masks), masks.shape[1], _ptr(positions), st))
+        _check(lib().md_kv_tree_window(batch.desc(rows), _ptr(parents), window, sinks, _ptr(masks), masks.shape[1],
+                                       _ptr(positions), st))
     return masks, positions
 
 

@@ -246,8 +246,8 @@ hipError_t launch_kv_read(const KvCache& c, const int* pages, int n, void* k, vo
 hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int n, hipStream_t st);
 KvPlan kv_attn_plan(const KvCache& c, const KvBatch& b, int G, int window, int sinks, int causal, int yt, bool masked);
 hipError_t launch_kv_attn(const KvAttn& a, int D, int yt, hipStream_t st);
-hipError_t launch_kv_tree(const KvBatch& b, const int* parents, uint64_t* masks, int words, int* positions,
-                          hipStream_t st);
+hipError_t launch_kv_tree(const KvBatch& b, const int* parents, int window, int sinks, uint64_t* masks, int words,
+                          int* positions, hipStream_t st);
 
 // ---- norms and rotation of queries and keys (rope.hip) ----------------------
 struct RopeArgs {

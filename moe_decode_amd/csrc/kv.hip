@@ -307,8 +307,11 @@ hipError_t launch_kv_copy(const KvCache& c, const int* src, const int* dst, int 
 
 // Trees of drafts: a thread walks from a token up to the root.  Parents lie
 // before their children, so the bits of a row fill its words from the last one
-// down, each word written once.
-__global__ __launch_bounds__(64) void k_kv_tree(KvBatch b, const int* parents, uint64_t* masks, int words, int* positions) {
+// down, each word written once.  The ancestor k steps up stands k places before
+// the token in the text: with a window its bit is kept where k < window, or where
+// that place is one of the first `sinks`.
+__global__ __launch_bounds__(64) void k_kv_tree(KvBatch b, const int* parents, int window, int sinks, uint64_t* masks,
+                                                int words, int* positions) {
   const int s = blockIdx.y, i = blockIdx.x * 64 + threadIdx.x;
   const int r0 = b.q_start[s], r1 = b.q_start[s + 1];
   if (r0 < 0 || r1 < r0 || r1 > b.rows) return;
@@ -322,22 +325,22 @@ __global__ __launch_bounds__(64) void k_kv_tree(KvBatch b, const int* parents, u
     good = p >= -1 && p < j;
     j = p;
   }
+  const int pos = good ? b.kv_len[s] - (r1 - r0) + depth - 1 : -1;
   uint64_t* out = masks + ((int64_t)r0 + i) * words;
-  int j = good ? i : -1;
+  int j = good ? i : -1, k = 0;
   for (int w = words - 1; w >= 0; --w) {
     uint64_t bits = 0;
-    while (j >= 0 && j >> 6 == w) {
-      bits |= 1ull << (j & 63);
-      j = up[j];
-    }
+    for (; j >= 0 && j >> 6 == w; j = up[j], ++k)
+      if (!window || k < window || pos - k < sinks) bits |= 1ull << (j & 63);
     out[w] = bits;
   }
-  if (positions) positions[r0 + i] = good ? b.kv_len[s] - (r1 - r0) + depth - 1 : -1;
+  if (positions) positions[r0 + i] = pos;
 }
 
-hipError_t launch_kv_tree(const KvBatch& b, const int* parents, uint64_t* masks, int words, int* positions,
-                          hipStream_t st) {
-  hipLaunchKernelGGL(k_kv_tree, dim3((b.max_q + 63) / 64, b.S), dim3(64), 0, st, b, parents, masks, words, positions);
+hipError_t launch_kv_tree(const KvBatch& b, const int* parents, int window, int sinks, uint64_t* masks, int words,
+                          int* positions, hipStream_t st) {
+  hipLaunchKernelGGL(k_kv_tree, dim3((b.max_q + 63) / 64, b.S), dim3(64), 0, st, b, parents, window, sinks, masks, words,
+                     positions);
   return hipGetLastError();
 }
 

@@ -438,6 +438,11 @@ md_status md_kv_attention_masked(const md_kv_cache* c, const md_kv_batch* b, con
 
 md_status md_kv_tree(const md_kv_batch* b, const int32_t* parents, uint64_t* masks, int32_t words, int32_t* positions,
                      hipStream_t stream) {
+  return md_kv_tree_window(b, parents, 0, 0, masks, words, positions, stream);
+}
+
+md_status md_kv_tree_window(const md_kv_batch* b, const int32_t* parents, int32_t window, int32_t sinks, uint64_t* masks,
+                            int32_t words, int32_t* positions, hipStream_t stream) {
   if (!b) return fail(MD_ERR_INVALID_ARG, "null batch descriptor");
   if (b->n_seqs <= 0 || b->rows < 0 || b->max_q <= 0)
     return fail(MD_ERR_SHAPE, "batch: n_seqs %d rows %d max_q %d", b->n_seqs, b->rows, b->max_q);
@@ -446,12 +451,13 @@ md_status md_kv_tree(const md_kv_batch* b, const int32_t* parents, uint64_t* mas
                 b->rows, kMaxTokens, b->max_q, kMaxTree);
   if (words > kMaxWords) return fail(MD_ERR_UNSUPPORTED, "tree: %d words > %d", words, kMaxWords);
   if (words < 1 || 64 * words < b->max_q) return fail(MD_ERR_SHAPE, "tree: %d words for runs of %d", words, b->max_q);
+  if (window < 0 || sinks < 0) return fail(MD_ERR_INVALID_ARG, "tree: window %d, sinks %d", window, sinks);
   if (b->rows == 0) return ok();
   if (!b->q_start || !b->kv_len || !parents || !masks) return fail(MD_ERR_INVALID_ARG, "tree: null pointer");
   if (!aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(parents) || (positions && !aligned4(positions)) ||
       (reinterpret_cast<uintptr_t>(masks) & 7u))
     return fail(MD_ERR_ALIGNMENT, "tree: masks not 8-byte aligned, or another array not 4-byte");
-  const hipError_t e = md::launch_kv_tree(dev(b), parents, masks, words, positions, stream);
+  const hipError_t e = md::launch_kv_tree(dev(b), parents, window, sinks, masks, words, positions, stream);
   return e == hipSuccess ? ok() : hip_fail(e, "tree launch");
 }
 
