@@ -832,6 +832,8 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         if tree is not None:
             words = tree.shape[1] if tree.dim() == 2 else 0
             _dense("tree", tree, (rows, words), torch.int64, cache.device)
+            if rows and not words:      # (its address is null, which the C call takes for no tree)
+                raise ValueError("tree: masks of no words")
         mask = KVMaskDesc(window, sinks, words, _ptr(tree))
     with _on(cache.device, stream) as st:
         if out is None:
