@@ -711,6 +711,9 @@ def i8_linear(W, x, bias=None, y=None, out_dtype=None, workspace=None, stream=No
     return y
 
 
+_I32_MAX = (1 << 31) - 1        # of a C int: ctypes passes the low 32 bits of what is larger
+
+
 class KVMaskDesc(ctypes.Structure):
     _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("words", ctypes.c_int32),
                 ("tree", ctypes.c_void_p)]
@@ -799,7 +802,7 @@ def kv_append(cache, batch, k, v, stream=None):
 
 def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0, out_dtype=None):
     import torch
-    need = ctypes.c_size_t(0)
+    need, window = ctypes.c_size_t(0), min(window, _I32_MAX)
     _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads,
                                                 int(causal), window, _xtype(out_dtype or torch.float32),
                                                 ctypes.byref(need)))
@@ -824,7 +827,7 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         raise ValueError(f"q [rows][q_heads][head_dim] and the batch on {cache.device} wanted")
     rows, heads, dim = q.shape
     qs = _rows("q", q, heads, cache.head_dim, cache.device)
-    mask = None
+    window, sinks, mask = min(window, _I32_MAX), min(sinks, _I32_MAX), None  # more is as much
     if tree is not None or sinks:
         if not causal:
             raise ValueError("a tree or sinks without causal")
@@ -878,6 +881,7 @@ def kv_tree(batch, parents, masks=None, positions=None, stream=None, window=0, s
     kv_attention) and positions (int32 [rows], for qk_norm_rope)."""
     import torch
     rows, dev = parents.shape[0], batch.device
+    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
     _dense("parents", parents, (rows,), torch.int32, dev)
     with _on(dev, stream) as st:
         if masks is None:
