@@ -332,10 +332,12 @@ class MoELayer:
         return b
 
 
-def moe_workspace_size(layer, T):
+def moe_workspace_size(layer, T, routed=False):
+    """routed: of a call with a Routing."""
     d = layer.desc()
     need = ctypes.c_size_t(0)
-    _check(lib().md_moe_workspace_size(ctypes.byref(d), T, ctypes.byref(need)))
+    size = lib().md_moe_routed_workspace_size if routed else lib().md_moe_workspace_size
+    _check(size(ctypes.byref(d), T, ctypes.byref(need)))
     return need.value
 
 
@@ -360,9 +362,7 @@ def moe_layer_forward(layer, x, y=None, idx=None, gates=None, workspace=None, st
                 _dense("idx", idx, (T, layer.k), torch.int32, dev)
             if gates is not None:
                 _dense("gates", gates, (T, layer.k), torch.float32, dev)
-            need = ctypes.c_size_t(0)
-            _check(lib().md_moe_routed_workspace_size(ctypes.byref(d), T, ctypes.byref(need)))
-            ws, wsb = _workspace(need.value, dev, workspace, stream)
+            ws, wsb = _workspace(moe_workspace_size(layer, T, True), dev, workspace, stream)
             _check(lib().md_moe_layer_forward_routed(ctypes.byref(d), r, _ptr(x), T, _ptr(y), _ptr(idx), _ptr(gates),
                                                      _ptr(ws), wsb, st))
         return y
@@ -800,12 +800,33 @@ def kv_append(cache, batch, k, v, stream=None):
                                   vs, _xtype(k.dtype), st))
 
 
-def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0, out_dtype=None):
+def _mask_desc(causal, window, sinks, tree, rows, device):
+    """What a call with a tree or sinks passes beside its window; None for a plain one."""
+    if tree is None and not sinks:
+        return None
     import torch
-    need, window = ctypes.c_size_t(0), min(window, _I32_MAX)
-    _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads,
-                                                int(causal), window, _xtype(out_dtype or torch.float32),
-                                                ctypes.byref(need)))
+    if not causal:
+        raise ValueError("a tree or sinks without causal")
+    words = 0
+    if tree is not None:
+        words = tree.shape[1] if tree.dim() == 2 else 0
+        _dense("tree", tree, (rows, words), torch.int64, device)
+        if rows and not words:      # (its address is null, which the C call takes for no tree)
+            raise ValueError("tree: masks of no words")
+    return KVMaskDesc(window, sinks, words, _ptr(tree))
+
+
+def kv_attention_workspace_size(cache, batch, rows, q_heads, causal=True, window=0, out_dtype=None, sinks=0, tree=None):
+    import torch
+    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)
+    mask = _mask_desc(causal, window, sinks, tree, rows, cache.device)
+    need, yt = ctypes.c_size_t(0), _xtype(out_dtype or torch.float32)
+    if mask is None:
+        _check(lib().md_kv_attention_workspace_size(cache._ref, batch.desc(rows), q_heads, int(causal), window, yt,
+                                                    ctypes.byref(need)))
+    else:
+        _check(lib().md_kv_attention_masked_workspace_size(cache._ref, batch.desc(rows), q_heads, ctypes.byref(mask), yt,
+                                                           ctypes.byref(need)))
     return need.value
 
 
@@ -827,17 +848,8 @@ def kv_attention(cache, batch, q, scale=None, causal=True, window=0, out=None, o
         raise ValueError(f"q [rows][q_heads][head_dim] and the batch on {cache.device} wanted")
     rows, heads, dim = q.shape
     qs = _rows("q", q, heads, cache.head_dim, cache.device)
-    window, sinks, mask = min(window, _I32_MAX), min(sinks, _I32_MAX), None  # more is as much
-    if tree is not None or sinks:
-        if not causal:
-            raise ValueError("a tree or sinks without causal")
-        words = 0
-        if tree is not None:
-            words = tree.shape[1] if tree.dim() == 2 else 0
-            _dense("tree", tree, (rows, words), torch.int64, cache.device)
-            if rows and not words:      # (its address is null, which the C call takes for no tree)
-                raise ValueError("tree: masks of no words")
-        mask = KVMaskDesc(window, sinks, words, _ptr(tree))
+    window, sinks = min(window, _I32_MAX), min(sinks, _I32_MAX)     # more is as much
+    mask = _mask_desc(causal, window, sinks, tree, rows, cache.device)
     with _on(cache.device, stream) as st:
         if out is None:
             out = _result(stream, torch.empty, rows, heads, dim, dtype=out_dtype or torch.float32,
