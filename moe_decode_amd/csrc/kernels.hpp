@@ -273,7 +273,7 @@ struct RouteArgs {
   float* logits;
   int* idx;
   float* gates;
-  float *wnorm, *xnorm, *most;  // squared norms [H / 256][E], [S][T]; [2]: the largest row's, of a finite balance
+  float *wnorm, *xnorm, *most;  // squared norms [H / 256][E], [S][T]; [1]: the largest row's
   int *count, *list;          // [1], [T]: tokens that are done in fp64
 };
 struct RoutePlan {

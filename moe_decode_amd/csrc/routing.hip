@@ -297,8 +297,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_route_fast(const void* __restric
                                                        const uint16_t* __restrict__ planes,
                                                        const float* __restrict__ scales, int E, int Ks, int S,
                                                        float* __restrict__ part, float* __restrict__ xnorm,
-                                                       const float* __restrict__ wnorm, const float* __restrict__ balance,
-                                                       float* __restrict__ most) {
+                                                       const float* __restrict__ wnorm, float* __restrict__ most) {
   constexpr int KS = kFastStep, C = KS / 8, XP = XT == XF32 ? 2 : 1;  // columns, chunks of 16 bytes, parts of x
   constexpr int kTile = kTT * KS;                                     // values of a part of x's tile
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * XP * kTile];
@@ -386,18 +385,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_route_fast(const void* __restric
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.0;
-  if (blockIdx.x == 0) {  // what every token's bound needs: the largest squared norm and finite balance
-    float n = 0.0f, bal = 0.0f;  // E is up to 256
+  if (blockIdx.x == 0) {  // what every token's bound needs: the largest row's squared norm
+    float n = 0.0f;  // E is up to 256
     if (tid < E) {
 #pragma unroll 16
       for (int c = 0; c < H / 256; ++c) n += wnorm[(int64_t)c * E + tid];
-      if (balance && balance[tid] > -INFINITY) bal = fabsf(balance[tid]);
     }
     n = group_max<64>(n);
-    bal = group_max<64>(bal);
-    if (lane == 0 && wave < 4) s_back[0][wave] = n, s_back[1][wave] = bal;
+    if (lane == 0 && wave < 4) s_back[0][wave] = n;
     __syncthreads();
-    if (tid < 2) most[tid] = fmaxf(fmaxf(s_back[tid][0], s_back[tid][1]), fmaxf(s_back[tid][2], s_back[tid][3]));
+    if (tid == 0) *most = fmaxf(fmaxf(s_back[0][0], s_back[0][1]), fmaxf(s_back[0][2], s_back[0][3]));
     __syncthreads();
   }
   f32x16 d[2][2];  // of two steps: the sums of the one before are added beside the products of this one
@@ -622,9 +619,11 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
   // s (1 - s) times off (1.03: the slope around it) and its own roundings, 2^-23 of
   // s below 1 in the quotient, less in the others; a softmax's terms by the factor
   // exp(2 off), 14 2^-24 of s in exp, sum and quotient, and what exp's argument is
-  // rounded by, s log(top_s / s) 2^-23; the sums with the balance and here once more
-  float off = 0.0f, most = 0.0f, delta[4];  // most: of a group's experts
+  // rounded by, s log(top_s / s) 2^-23; the sums with the balance and here by 2^-24
+  // of c each (of its own c: an expert closed by -1e9 leaves the others' bounds alone)
+  float off = 0.0f, most = 0.0f, edge = 0.0f, delta[4];  // most: of a group's experts, less what follows their c
   bool open = false;
+  auto size = [](float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; };  // an infinity is exact
   if constexpr (B) {
     float xn = 0.0f;
     for (int p = 0; p < S; ++p) xn += g.xnorm[(int64_t)p * g.T + t];
@@ -632,7 +631,7 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
     const float nx = sqrtf(xn) * 1.001f, nw = sqrtf(g.most[0]) * 1.001f;  // their own sums' rounding
     off = fast_error(g.f32) * nx * nw + 0x1p-119f * (nx + nw) + 0x1p-22f * far;
     open = !(off < 0.01f);  // past where the slopes hold, or no number
-    const float edge = g.sigmoid ? 0x1p-21f * (1.0f + g.most[1]) : 0x1p-24f * top_s + 0x1p-23f * g.most[1] + 1e-14f;
+    edge = g.sigmoid ? 0x1p-21f : 0x1p-24f * top_s + 1e-14f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       delta[i] = edge + (g.sigmoid ? 1.03f * off * s[i] * (1.0f - s[i]) : s[i] * (2.1f * off + 0x1.2p-20f));
@@ -646,6 +645,7 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
     if (e < E) {
       c[i] = g.balance ? s[i] + (F)bal[i] : s[i];
       if (c[i] != c[i]) c[i] = -INFINITY;
+      if constexpr (B) delta[i] += 0x1p-23f * size(c[i]);
       if constexpr (B) {
         hi[i] = order_key32(c[i]);
       } else {
@@ -684,10 +684,14 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
     }
     const uint64_t keep = __builtin_amdgcn_ballot_w64(grp < g.groups && rank < g.kept);
     if constexpr (B) {
-      const uint64_t last = __builtin_amdgcn_ballot_w64(grp < g.groups && rank == g.kept - 1);
-      const uint64_t next = __builtin_amdgcn_ballot_w64(grp < g.groups && rank == g.kept);
-      const float gap = lane_of(value, __builtin_ctzll(last)) - lane_of(value, __builtin_ctzll(next));
-      open |= !(gap > most * (g.best_two ? 4.0f : 2.0f));
+      // The least that a kept group may be worth, and the most that another may.  An expert's bounds rise
+      // with its c, so those of the largest ones bound the group: 2^-24 of each in its own sum, of their sum
+      // and of the one here, twice that allowed
+      const float margin = g.best_two ? 2.0f * most + 0x1p-21f * (size(a) + size(b)) : most + 0x1p-21f * size(a);
+      const bool in = grp < g.groups;
+      const float least = -group_max<64>(in && rank < g.kept ? margin - value : -INFINITY);
+      const float best = group_max<64>(in && rank >= g.kept ? value + margin : -INFINITY);
+      open |= !(least > best);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -816,7 +820,7 @@ RoutePlan route_plan(int64_t T, int H, int E, int xt, bool fast) {
     p.planes = take(4 * ets * kFT * H);
     p.scales = take(4 * ets * kFT * (H / 64));
     p.wnorm = take(4 * (size_t)E * (H / 256));
-    p.most = take(8);
+    p.most = take(4);
     p.xnorm = take(4 * rows);
     p.count = take(4);
     p.list = take(4 * (size_t)T);
@@ -837,10 +841,10 @@ static hipError_t launch_fast(const RouteArgs& g, const RoutePlan& p, const void
   float* part = reinterpret_cast<float*>(g.part);
   if (ets == 2)
     hipLaunchKernelGGL((k_route_fast<XT, 8>), dim3(tiles), dim3(512), 0, st, x, g.T, H, planes, scales, g.E, p.Ks, p.S, part,
-                       g.xnorm, g.wnorm, g.balance, g.most);
+                       g.xnorm, g.wnorm, g.most);
   else
     hipLaunchKernelGGL((k_route_fast<XT, 4>), dim3(tiles), dim3(256), 0, st, x, g.T, H, planes, scales, g.E, p.Ks, p.S, part,
-                       g.xnorm, g.wnorm, g.balance, g.most);
+                       g.xnorm, g.wnorm, g.most);
   hipLaunchKernelGGL((k_route_select<kBounded>), dim3(g.T), dim3(64), 0, st, g);
   hipLaunchKernelGGL((k_route_gemm<XT, true>), dim3(kListGroups), dim3(256), 0, st, x, g.T, H, Wr, g.E, 0, g.part, g.count,
                      g.list);
