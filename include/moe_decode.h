@@ -718,7 +718,10 @@ md_status md_qk_norm_rope(const md_rope *r /*host*/, const int32_t *positions, i
  * and of the longest row of W_r; an instruction there is taken to be off by 2^-23 of
  * its sum), and does in fp64 only the tokens whose choice that leaves open: the
  * choice is the definition's there too, and a gate is off by what its logits' bound
- * allows, relatively by at most 4.1 times it (measured: 1e-7).
+ * allows, relatively by at most 4.1 times it and never by more than 2^-7.9, since a
+ * token whose bound passes 2^-10 is done in fp64 (measured: 1e-7).  The same token's
+ * gates may differ by that between a long call and a short one; a call that asks for
+ * the logits has them all in fp64.
  * x: T x H fp32 or bf16; logits (T x E fp32, may be NULL).  T: 0..2^20 (0: nothing
  * to do); H, E, k as md_moe_route_topk; groups: up to 64.  A NaN is the smallest of
  * all (as -inf is, which closes an expert in balance); idx then still names k

@@ -630,7 +630,9 @@ MD_DEV void route_choose(const RouteArgs& g, RouteLds<FROM == kBounded>& lds, in
     far = group_max<64>(far);
     const float nx = sqrtf(xn) * 1.001f, nw = sqrtf(g.most[0]) * 1.001f;  // their own sums' rounding
     off = fast_error(g.f32) * nx * nw + 0x1p-119f * (nx + nw) + 0x1p-22f * far;
-    open = !(off < 0.01f);  // past where the slopes hold, or no number
+    // past this a gate might be off by more than a step of bf16 (4.1 off), or off is no number.  W_r of N(0, 0.05)
+    // and x of N(0, 1) stay below it at the largest width
+    open = !(off < 0x1p-10f);
     edge = g.sigmoid ? 0x1p-21f : 0x1p-24f * top_s + 1e-14f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)

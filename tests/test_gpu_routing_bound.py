@@ -172,3 +172,21 @@ def test_options_captured():
             assert torch.equal(gi, want)
             l = x.double() @ W.double().t() + bias.double()
             assert ((gg - wg).abs().double() <= wg.abs() * (4.1 * _bound(x, W, l) + 4 * U)).all()
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("options", [dict(score="sigmoid"), dict(renorm=False)])
+def test_a_bound_above_2_to_minus_10_takes_fp64(xt, options):
+    """A large value of x that W_r does not see leaves the logits as they are and makes
+    their bound one that would allow gates 0.8% off: they are fp64's, to the bit."""
+    import moe_decode_amd as md
+    import torch
+    T, H, E = 3001, 6144, 256
+    g, x, W = _problem(T, H, E, xt, 31)
+    x[:, 70], W[:, 70] = 2000.0, 0.0
+    off = _bound(x, W, x.double() @ W.double().t())
+    assert 2.0 ** -10 < off.min() and off.max() < 2.0 ** -8
+    r = md.Routing(8, **options)
+    idx, gates = md.moe_route(x, W, r)
+    want, wg = md.moe_route(x, W, r, logits=torch.empty(T, E, device="cuda"))
+    assert torch.equal(idx, want) and torch.equal(gates, wg)
