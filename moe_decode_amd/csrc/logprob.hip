@@ -384,13 +384,16 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogpArgs g) {
   finish<XT>(g, row, r, s_top, lane, 64);
 }
 
-// Values a thread and step: 32, or 8 where that leaves compute units without work;
-// segments of a row: enough for some workgroups on every compute unit.
+// Values a thread and step: 32, or 8 where that leaves compute units without work or
+// where one step of 8 holds a row (us, 32 and 8, without alternatives and with the 8
+// largest: 4096 rows of 100 bf16 16.0 and 10.2, 31.0 and 18.8, of 2000 fp32 16.8 and
+// 11.1, 32.2 and 20.3; 600 rows alike in both); segments of a row: enough for some
+// workgroups on every compute unit.
 LogpPlan logprob_plan(int64_t rows, int vocab) {
   LogpPlan p{};
   const int64_t cus = device_cus();
   auto steps_of = [&](int n) { return (vocab + 7 + 256 * n - 1) / (256 * n); };  // a row may begin up to 7 values past 16 bytes
-  p.values = rows * steps_of(32) >= 2 * cus ? 32 : 8;
+  p.values = rows * steps_of(32) >= 2 * cus && steps_of(8) > 1 ? 32 : 8;
   const int total = steps_of(p.values);
   int64_t segs = (kSegGroups * cus + rows - 1) / rows;
   if (segs > total) segs = total;
