@@ -36,14 +36,9 @@ MD_DEV void cos_sin(double r, float& c, float& s) {
   s = k >= 2 ? -b : b;
 }
 
-template <int XT, int N>
-MD_DEV void load_n(const void* p, int64_t i, float* v) {  // N = 4 or 8 values from value i on
-  if constexpr (N == 8) {
-    float w[8];
-    load8<XT>(p, i, w);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) v[m] = w[m];
-  } else if constexpr (XT == XF32) {
+template <int XT>
+MD_DEV void load4(const void* p, int64_t i, float* v) {
+  if constexpr (XT == XF32) {
     const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   } else {
@@ -110,8 +105,8 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs g) {
     const int64_t at = row * (is_q ? g.q_stride : g.k_stride) + (int64_t)hh * D;
     float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (here) {
-      load_n<XT, 4>(x, at + at_a, a);
-      load_n<XT, 4>(x, at + at_b, b);
+      load4<XT>(x, at + at_a, a);
+      load4<XT>(x, at + at_b, b);
     }
     const float* w = is_q ? g.q_weight : g.k_weight;
     float ss = 0.0f;
@@ -122,8 +117,8 @@ __global__ __launch_bounds__(256) void k_qk_norm_rope(RopeArgs g) {
       if (w) {
         const float r = 1.0f / sqrtf(fmaf(ss, inv_d, g.eps));
         float wa[4], wb[4];
-        load_n<XF32, 4>(w, at_a, wa);
-        load_n<XF32, 4>(w, at_b, wb);
+        load4<XF32>(w, at_a, wa);
+        load4<XF32>(w, at_b, wb);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           a[i] *= r * wa[i];
