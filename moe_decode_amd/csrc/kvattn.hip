@@ -24,6 +24,11 @@
 // visible) take the same two forms; they differ in which tiles a column sees (kv.hpp:
 // the first ones, then those of the window) and in how a cut tile's scores are
 // masked: sixteen bits a lane, made of the row's borders and its words of the tree.
+// They round their operands as plain calls do, for bf16 outputs more than for fp32
+// ones: a query to two digits, or queries and weights to one f16.  That moves some
+// outputs to a neighbouring bf16 value (2.5% of them, 9.6%) and their distance from
+// the definition, which the output's own rounding makes, from 1.658e-3 of the
+// outputs' size to 1.659e-3 and 1.671e-3 (rms; windows of 4096 and 1024 positions).
 //
 // Operand layout.  Keys enter as the A operand (rows = tokens), queries as B
 // (columns = (query, head) pairs that share the key head), so the scores come
@@ -584,7 +589,7 @@ constexpr int kRowCols = 128;  // columns of a workgroup
 // Tiles of a split of the sequence q.  Plain calls: what the host's bounds gave.
 // Masked ones: all column tiles' tiles, by the lengths on the device, over the
 // workgroups that run at once (a.deal; one more would wait for all of them), four at
-// least and as many as leave a.splits of them enough (2 x 61 drafts on 65535 and 37843 tokens, 32 heads on 8 of 128:
+// least and as many as leave a.splits of them enough (2 x 61 drafts on 65535 and 27963 tokens, 32 heads on 8 of 128:
 // 263 us with splits of the longest one's, 228).  Every thread of the workgroup calls it; there are at most 256
 // sequences where a.splits > 1.
 template <bool M>

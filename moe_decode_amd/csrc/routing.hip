@@ -8,8 +8,8 @@
 // Scores that lie next to each other decide, so everything up to a gate is
 // fp64 (the logits are rounded to fp32 once, as the layer's own router's are):
 // products of two fp32 values are exact there, and the choice is the
-// definition's.  Where the fp64 matrix cores would be what a call waits for (78
-// Tflop/s), the logits are formed on the fp16 ones first, with a bound on their
+// definition's.  Where the fp64 matrix cores would be what a call waits for (73
+// Tflop/s in a large product), the logits are formed on the fp16 ones first, with a bound on their
 // error, and only the tokens whose choice that bound leaves open are done in fp64.
 #include <hip/hip_runtime.h>
 
@@ -64,9 +64,11 @@ __global__ __launch_bounds__(256) void k_route_few(const void* __restrict__ x, i
 // [lane % 16] in element v.  A lane's four neighbouring columns go to four
 // instructions: which column is which k does not matter to a sum.  LIST: of the
 // tokens that a list names, as many as its count says; the grid's workgroups share
-// out tiles and slices.  Measured: 128 tokens x 6144 x 256 13.1 us (0.4 Gflop; 5.5 at
-// the rate of a large product; twice as many slices: with the choice 23.6 us where
-// this takes 19.6), a list of some 100 tokens 15, 8191 tokens 420 (61 Tflop/s).
+// out tiles and slices.  Measured: 128 tokens x 6144 x 256 12.7 us (0.4 Gflop; 5.5 at
+// the rate of a large product; twice as many slices: a call 22.1 us where this takes
+// 18.5), a list of some 100 tokens 15, 8191 tokens 420 (61 Tflop/s).  The layer's own
+// chunk router (k_router_mfma) stays beside it: it leaves the activations' bf16 pairs
+// for the experts from the tiles that it stages, and layer calls keep its bits.
 constexpr int kGT = 32;
 constexpr int kAhead = 4;
 
