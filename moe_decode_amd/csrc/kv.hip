@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64) void k_kv_tree(KvBatch b, const int* parents, i
   for (int w = words - 1; w >= 0; --w) {
     uint64_t bits = 0;
     for (; j >= 0 && j >> 6 == w; j = up[j], ++k)
-      if (!window || k < window || pos - k < sinks) bits |= 1ull << (j & 63);
+      if (!window || k < window || (unsigned)(pos - k) < (unsigned)sinks) bits |= 1ull << (j & 63);
     out[w] = bits;
   }
   if (positions) positions[r0 + i] = pos;

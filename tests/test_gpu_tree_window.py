@@ -96,3 +96,13 @@ def test_no_window_keeps_every_ancestor_and_bad_chains_have_none():
     assert torch.equal(fpos, pos) and (few[30] == 0).all() and (few[31] == 0).all() and pos[31] == -1
     keep = [None if p is None else _kept(p, 40, 2, 0) for p in M.tree_bits(parents)]
     assert np.array_equal(few.cpu().numpy(), M.pack(keep, 2))
+
+
+@pytest.mark.parametrize("sinks", [0, 1])
+def test_places_before_the_text_are_no_first_positions(sinks):
+    """A run longer than its sequence: its first tokens stand at -2 and -1, and no sinks hold them."""
+    import moe_decode_amd as md
+    b = _batch([3], [1], np.zeros((1, 1), np.int32))
+    masks, pos = md.kv_tree(b, _i32([-1, 0, 1]), window=1, sinks=sinks)
+    assert pos.tolist() == [-2, -1, 0]
+    assert np.array_equal(masks.cpu().numpy(), M.pack([[0], [1], [2]], 1))
